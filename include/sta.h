@@ -257,6 +257,141 @@ sta_status sta_backward_noalloc(sta_plan_t plan, const void *q, const void *k, c
  * is the hook the failure-detection tests use; ordinary callers never need it. */
 void sta_set_wait_limit_ns(uint64_t ns);
 
+/* ------------------------------------------------------------------------
+ * Token sequences: causal sliding-window attention with sinks, and an 8-bit
+ * key/value cache.  The one-dimensional counterpart of the calls above, for
+ * models that produce their tokens in order.  These calls have no counterpart
+ * in the method's description ("Fast Video Generation with Sliding Tile
+ * Attention").
+ *
+ * Conventions, beside those at the top of this file:
+ *   - There is no plan.  Every call takes its sizes in a struct, enqueues on
+ *     `stream` of the current device and returns; it allocates nothing and
+ *     can be captured into a CUDA graph.  Calls that overlap on the GPU need
+ *     workspaces of their own, and a captured call keeps its workspace.
+ *   - Tensors are addressed by sta_rows: rows of head_dim contiguous elements
+ *     at strides of the caller's choice (in elements, each a multiple of 8
+ *     and, where its extent is above 1, positive), so [batch][heads][N][d]
+ *     and [batch][N][heads][d] tensors are read and written in place.  Data
+ *     pointers are 16-byte aligned (STA_ERR_ALIGNMENT for either).
+ *   - Output tensors must not overlap inputs or one another.
+ *   - Query row i of a sequence with Nq queries and Nk keys sits at position
+ *     i + Nk - Nq.  It sees the keys j at or before its position that are
+ *     among the last `window` positions up to it (window = 0: all of them)
+ *     or among the first `sinks` of the sequence.  Rows that see nothing
+ *     (positions below 0) get O = 0, LSE = -inf and gradients of 0.
+ *   - K and V rows past a sequence's end, and keys that no query of a call
+ *     sees, never reach a result.  A non-finite K or V row that one query of
+ *     a 128-row block sees may reach the block's other rows.
+ */
+
+/* element types */
+#define STA_TYPE_BF16 0
+#define STA_TYPE_FP16 1
+#define STA_TYPE_E4M3 2 /* 8-bit floating point, largest value 448 (cache only) */
+#define STA_TYPE_INT8 3 /* -127 .. 127 (cache only) */
+
+typedef struct {
+  void *data;               /* element (0, 0, 0, 0) */
+  int64_t batch, head, row; /* strides in elements; batch is not used by packed calls */
+} sta_rows;
+
+typedef struct {
+  int32_t batch;           /* sequences */
+  int32_t heads, kv_heads; /* kv_heads divides heads: query head h reads key head h / (heads / kv_heads) */
+  int32_t head_dim;        /* in {64, 128} */
+  int32_t q_len, kv_len;   /* rows of every sequence; packed: rows of the longest one */
+  int32_t q_rows, kv_rows; /* packed calls only: rows of the packed tensors */
+  int32_t window;          /* visible positions up to and including the query's own; 0: no limit */
+  int32_t sinks;           /* first tokens of a sequence that stay visible */
+  int32_t type;            /* STA_TYPE_BF16 or STA_TYPE_FP16: q, k, v, o and their gradients */
+  float scale;             /* softmax scale; <= 0 means 1/sqrt(head_dim) */
+} sta_window_problem;
+
+/* Workspace bytes of sta_window_forward and sta_window_backward for a problem
+ * (either pointer may be NULL).  Size limits (STA_ERR_SHAPE): batch * heads *
+ * q_len, batch * kv_heads * kv_len and the packed row counts times heads below
+ * 2^31 - 1024. */
+sta_status sta_window_workspace_size(const sta_window_problem *problem, size_t *fwd_bytes, size_t *bwd_bytes);
+
+/* O = softmax(q k^T * scale over each query's visible keys) v and lse = the
+ * log-sum-exp of the same scores (fp32, [batch][heads][q_len], packed
+ * [heads][q_rows]; nullable).  Statistics and sums are fp32; P is rounded to
+ * the tensors' type for the product with V.
+ *   cu_q, cu_kv: NULL for the dense form.  Packed form: both device arrays of
+ * batch + 1 int32; sequence b is rows [cu[b], cu[b + 1]) of every head, at
+ * most q_len / kv_len of them, inside [0, q_rows) / [0, kv_rows) (what lies
+ * outside is dropped).  Rows of o and lse outside every sequence are not
+ * written.  Calls of few query rows (a rule on the problem's sizes alone) split
+ * the keys over the GPU and join the parts; the others run on the tensor
+ * cores' 128-row tiles. */
+sta_status sta_window_forward(const sta_window_problem *problem, const sta_rows *q, const sta_rows *k,
+                              const sta_rows *v, const sta_rows *o, float *lse, const int32_t *cu_q,
+                              const int32_t *cu_kv, void *workspace, size_t workspace_bytes, void *stream,
+                              uint32_t flags);
+
+/* Gradients of sta_window_forward (the formulas of sta_backward over the
+ * visible pairs).  lse as the forward wrote it; dk and dv sum over the query
+ * heads that share a key head, in fp32 and in a fixed order. */
+sta_status sta_window_backward(const sta_window_problem *problem, const sta_rows *q, const sta_rows *k,
+                               const sta_rows *v, const sta_rows *o, const float *lse, const sta_rows *dout,
+                               const sta_rows *dq, const sta_rows *dk, const sta_rows *dv, const int32_t *cu_q,
+                               const int32_t *cu_kv, void *workspace, size_t workspace_bytes, void *stream,
+                               uint32_t flags);
+
+/* A cache of keys and values in 8 bits: `pages` pages of page_size tokens, one
+ * fp32 scale for every `block` tokens of a page and key head, for keys and
+ * values apart.  Layouts: k, v [pages][kv_heads][page_size][head_dim] codes,
+ * k_scale, v_scale [pages][kv_heads][page_size / block]; a code c stands for
+ * c * scale.  A sequence's tokens fill the pages of its row of a page table
+ * (device int32 [batch][table_pages]) in order; an entry outside [0, pages)
+ * marks an absent page, whose tokens are not written, not read and not seen. */
+typedef struct {
+  int32_t pages, kv_heads, page_size;
+  int32_t block;    /* tokens per scale: 16, 32, 64 or 128, a divisor of page_size */
+  int32_t head_dim; /* in {64, 128} */
+  int32_t type;     /* STA_TYPE_E4M3 or STA_TYPE_INT8 */
+  void *k, *v;
+  float *k_scale, *v_scale;
+} sta_cache;
+
+/* Append rows to the cache: rows [0, count[b]) of k and v (type in_type,
+ * [batch][kv_heads][rows]; count NULL: `rows` of each sequence, larger counts
+ * are cut to it) become tokens start[b], start[b] + 1, ... of sequence b
+ * (start[b] < 0, or a page the table does not hold: not written).  Tokens from
+ * start[b] on that the sequence's last block held are forgotten.  Per
+ * block and head the scale becomes max(the scale of the block's earlier
+ * tokens, the new rows' largest magnitude / the largest code, 2^-100); where
+ * it grows, the earlier tokens' codes are rounded again at the new scale, so a
+ * block's codes always share one scale.  A code is x * (1 / scale) in fp32,
+ * rounded to nearest even and cut to the largest code; NaN is no magnitude
+ * and becomes code 0; infinities count as the input type's largest
+ * value.  No two sequences of a call may write the same page. */
+sta_status sta_cache_write(const sta_cache *cache, int32_t batch, int32_t rows, const sta_rows *k, const sta_rows *v,
+                           int32_t in_type, const int32_t *page_table, int32_t table_pages, const int32_t *start,
+                           const int32_t *count, void *stream, uint32_t flags);
+
+/* Read tokens back: rows [0, count[b]) of k and v (type out_type) receive the
+ * values of tokens start[b], start[b] + 1, ... of sequence b, rounded to
+ * nearest.  Rows past count[b], and of absent pages, are not written. */
+sta_status sta_cache_read(const sta_cache *cache, int32_t batch, int32_t rows, const sta_rows *k, const sta_rows *v,
+                          int32_t out_type, const int32_t *page_table, int32_t table_pages, const int32_t *start,
+                          const int32_t *count, void *stream, uint32_t flags);
+
+/* Workspace bytes of sta_cache_attention. */
+sta_status sta_cache_workspace_size(const sta_cache *cache, int32_t batch, int32_t heads, int32_t q_len,
+                                    int32_t table_pages, int32_t window, int32_t sinks, size_t *bytes);
+
+/* Attention of q_len new queries per sequence (their keys and values already
+ * in the cache) over the cache: the forward of sta_window_forward with
+ * Nk = lengths[b] (device int32, cut to [0, table_pages * page_size]) and
+ * Nq = q_len.  q, o: type `type`; lse fp32 [batch][heads][q_len], nullable.
+ * Meant for few queries: every 8 query rows of a key head read its keys once. */
+sta_status sta_cache_attention(const sta_cache *cache, int32_t batch, int32_t heads, int32_t q_len, int32_t window,
+                               int32_t sinks, float scale, int32_t type, const sta_rows *q, const sta_rows *o,
+                               float *lse, const int32_t *page_table, int32_t table_pages, const int32_t *lengths,
+                               void *workspace, size_t workspace_bytes, void *stream, uint32_t flags);
+
 /* Static description of a status code. */
 const char *sta_status_string(sta_status status);
 

@@ -1,0 +1,196 @@
+// cache.cu -- writing to and reading from the 8-bit key/value cache.
+//
+// Every `block` tokens of a page and key head share one fp32 scale s, and a
+// code c stands for c * s.  Writing rows x into a block:
+//   s = max(scale of the block's earlier tokens, max |x| / qmax, 2^-100),
+//   c = round(x * (1 / s)),  and where s grew by earlier tokens: their codes
+//   become round(c * s_old * (1 / s)).
+// Bound by memory: 2 bytes read and 1 written per element, 1 read and 2
+// written on the way back.
+#include "seq_common.cuh"
+
+namespace sta {
+namespace {
+
+constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100: its reciprocal is finite
+
+template <int kType> struct Code;  // STA_TYPE_E4M3 / STA_TYPE_INT8
+template <> struct Code<STA_TYPE_E4M3> {
+  static constexpr float kMax = 448.f;
+  // two codes of two values (lo in bits 0..7), to nearest even, cut to +-448;
+  // NaN becomes 0
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    lo = lo == lo ? lo : 0.f;
+    hi = hi == hi ? hi : 0.f;
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+    return __half22float2(*reinterpret_cast<__half2 *>(&h));
+  }
+};
+template <> struct Code<STA_TYPE_INT8> {
+  static constexpr float kMax = 127.f;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    // __float2int_rn of NaN is 0
+    const int a = __float2int_rn(fminf(fmaxf(lo, -127.f), 127.f)), b = __float2int_rn(fminf(fmaxf(hi, -127.f), 127.f));
+    return (lo == lo ? (uint32_t)a & 0xffu : 0u) | ((hi == hi ? (uint32_t)b & 0xffu : 0u) << 8);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return make_float2((float)(int8_t)(w & 0xffu), (float)(int8_t)((w >> 8) & 0xffu));
+  }
+};
+
+__device__ __forceinline__ int clamp_count(const CacheMove &m, int b) {
+  return m.count ? min(max(__ldg(m.count + b), 0), m.rows) : m.rows;
+}
+
+// One CTA per (block of tokens touched, key head, sequence and tensor).
+template <int D, int kType, class T>
+__global__ void __launch_bounds__(128) cache_write_kernel(const CacheMove m) {
+  const CacheParams &c = m.c;
+  const bool is_v = blockIdx.z & 1;
+  const int b = blockIdx.z >> 1, h = blockIdx.y;
+  const int start = __ldg(m.start + b), count = clamp_count(m, b);
+  if (start < 0 || count == 0) return;
+  const long long end = (long long)start + count;
+  const long long first = ((long long)start / c.block + blockIdx.x) * c.block;  // first token of the block
+  if (first >= end || first + c.block > (long long)c.table_pages * c.page_size) return;
+  const int page = page_of(c, b, (int)first);
+  if (page < 0) return;
+  const int in_page = (int)(first % c.page_size);
+  uint8_t *codes = (is_v ? c.v : c.k) + (((long long)page * c.kv_heads + h) * c.page_size + in_page) * D;
+  float *scale = (is_v ? c.v_scale : c.k_scale) + ((long long)page * c.kv_heads + h) * (c.page_size / c.block) +
+                 in_page / c.block;
+  const Rows &x = is_v ? m.v : m.k;
+  const int lo = (int)max(0ll, start - first), hi = (int)min((long long)c.block, end - first);  // new tokens of the block
+  constexpr int kPer = D / 8;  // 16-byte pieces per row
+  constexpr int kMaxPieces = 128 * kPer / 128;
+  const char *src = x.p + 2 * ((long long)b * x.b + (long long)h * x.h + (first - start) * x.r);
+  uint4 held[kMaxPieces];
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxPieces; ++i) {
+    const int piece = threadIdx.x + 128 * i, row = lo + piece / kPer;
+    if (row < hi) {
+      held[i] = *reinterpret_cast<const uint4 *>(src + 2 * ((long long)row * x.r + piece % kPer * 8));
+      const uint32_t w[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = Elem<T>::unpack(w[e]);
+        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));  // fmaxf drops NaN
+      }
+    }
+  }
+  amax = fminf(amax, Elem<T>::kMax);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  __shared__ float part[4];
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+  const float old = lo > 0 ? *scale : 0.f;
+  __syncthreads();  // every thread has read the old scale, too
+  amax = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+  const float s = fmaxf(old, fmaxf(amax / Code<kType>::kMax, kScaleFloor));
+  const float inv = 1.f / s;
+  if (threadIdx.x == 0) *scale = s;
+#pragma unroll
+  for (int i = 0; i < kMaxPieces; ++i) {
+    const int piece = threadIdx.x + 128 * i, row = lo + piece / kPer;
+    if (row < hi) {
+      const uint32_t w[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
+      uint32_t q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = Elem<T>::unpack(w[e]);
+        q[e] = Code<kType>::pack(f.x * inv, f.y * inv);
+      }
+      *reinterpret_cast<uint2 *>(codes + row * D + piece % kPer * 8) =
+          make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+    }
+  }
+  if (lo > 0 && s > old) {
+    // the block's earlier tokens at the new scale
+    for (int i = threadIdx.x; i < lo * D / 4; i += 128) {
+      uint32_t *w = reinterpret_cast<uint32_t *>(codes) + i;
+      const float2 a = Code<kType>::unpack(*w & 0xffffu), z = Code<kType>::unpack(*w >> 16);
+      *w = Code<kType>::pack(a.x * old * inv, a.y * old * inv) | (Code<kType>::pack(z.x * old * inv, z.y * old * inv) << 16);
+    }
+  }
+}
+
+// A thread per 16 codes of one row.
+template <int D, int kType, class T>
+__global__ void __launch_bounds__(256) cache_read_kernel(const CacheMove m) {
+  const CacheParams &c = m.c;
+  constexpr int kPer = D / 16;
+  const bool is_v = blockIdx.z & 1;
+  const int b = blockIdx.z >> 1, h = blockIdx.y;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long row = i / kPer;
+  const int part = (int)(i % kPer), start = __ldg(m.start + b);
+  if (start < 0 || row >= clamp_count(m, b)) return;
+  if (start + row >= (long long)c.table_pages * c.page_size) return;
+  const int pos = start + (int)row, page = page_of(c, b, pos);
+  if (page < 0) return;
+  const int in_page = pos % c.page_size;
+  const long long ph = (long long)page * c.kv_heads + h;
+  const uint4 w = *reinterpret_cast<const uint4 *>((is_v ? c.v : c.k) + (ph * c.page_size + in_page) * D + 16 * part);
+  const float s = (is_v ? c.v_scale : c.k_scale)[ph * (c.page_size / c.block) + in_page / c.block];
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t out[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = Code<kType>::unpack(in[e] & 0xffffu), g = Code<kType>::unpack(in[e] >> 16);
+    out[2 * e] = Elem<T>::pack(f.x * s, f.y * s);
+    out[2 * e + 1] = Elem<T>::pack(g.x * s, g.y * s);
+  }
+  const Rows &x = is_v ? m.v : m.k;
+  uint4 *dst = reinterpret_cast<uint4 *>(x.p + 2 * ((long long)b * x.b + (long long)h * x.h + row * x.r + 16 * part));
+  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+template <int D, int kType, class T>
+cudaError_t write_launch(const CacheMove &m, cudaStream_t stream) {
+  // a run of `rows` tokens that starts anywhere touches at most this many blocks
+  const dim3 grid((m.rows + m.c.block - 2) / m.c.block + 1, m.c.kv_heads, 2 * m.batch);
+  cache_write_kernel<D, kType, T><<<grid, 128, 0, stream>>>(m);
+  return cudaGetLastError();
+}
+template <int D, int kType, class T>
+cudaError_t read_launch(const CacheMove &m, cudaStream_t stream) {
+  const dim3 grid((unsigned)(((long long)m.rows * (D / 16) + 255) / 256), m.c.kv_heads, 2 * m.batch);
+  cache_read_kernel<D, kType, T><<<grid, 256, 0, stream>>>(m);
+  return cudaGetLastError();
+}
+
+template <class F>
+cudaError_t by_types(int d, int cache_type, int io_type, F &&f) {
+  auto io = [&](auto dim, auto code) {
+    return io_type == STA_TYPE_BF16 ? f(dim, code, __nv_bfloat16{}) : f(dim, code, __half{});
+  };
+  auto cache = [&](auto dim) {
+    return cache_type == STA_TYPE_E4M3 ? io(dim, std::integral_constant<int, STA_TYPE_E4M3>{})
+                                       : io(dim, std::integral_constant<int, STA_TYPE_INT8>{});
+  };
+  return d == 128 ? cache(std::integral_constant<int, 128>{}) : cache(std::integral_constant<int, 64>{});
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheMove &m, int cache_type, int io_type, cudaStream_t stream) {
+  return by_types(m.c.d, cache_type, io_type, [&](auto d, auto code, auto t) {
+    return write_launch<decltype(d)::value, decltype(code)::value, decltype(t)>(m, stream);
+  });
+}
+
+cudaError_t launch_cache_read(const CacheMove &m, int cache_type, int io_type, cudaStream_t stream) {
+  return by_types(m.c.d, cache_type, io_type, [&](auto d, auto code, auto t) {
+    return read_launch<decltype(d)::value, decltype(code)::value, decltype(t)>(m, stream);
+  });
+}
+
+}  // namespace sta

@@ -1,0 +1,247 @@
+// seq_api.cpp -- host side of the token-sequence calls of include/sta.h:
+// argument checks, workspace sizes, parameter blocks and launches.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/sta.h"
+#include "seq_kernels.h"
+
+namespace {
+
+constexpr size_t kStatusBytes = 256;
+constexpr long long kMaxRows = (1ll << 31) - 1024;
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
+
+// A tensor of `batch` x `heads` x `rows` rows: its pointer and strides.
+sta_status check_rows(const sta_rows *x, long long batch, long long heads, long long rows) {
+  if (!x || !x->data) return STA_ERR_INVALID_ARG;
+  const int64_t s[3] = {x->batch, x->head, x->row};
+  const long long n[3] = {batch, heads, rows};
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] <= 1) continue;  // an extent of one: the stride is not used
+    if (s[i] <= 0 || s[i] >= (1ll << 38)) return STA_ERR_INVALID_ARG;
+    if (s[i] % 8) return STA_ERR_ALIGNMENT;
+  }
+  return aligned16(x->data) ? STA_OK : STA_ERR_ALIGNMENT;
+}
+
+sta::Rows rows_of(const sta_rows *x) {
+  return sta::Rows{static_cast<char *>(x->data), x->batch, x->head, x->row};
+}
+
+bool io_type_ok(int32_t t) { return t == STA_TYPE_BF16 || t == STA_TYPE_FP16; }
+
+sta_status check_problem(const sta_window_problem *p) {
+  if (!p) return STA_ERR_INVALID_ARG;
+  if (p->batch < 1 || p->heads < 1 || p->kv_heads < 1 || p->q_len < 0 || p->kv_len < 0 || p->q_rows < 0 ||
+      p->kv_rows < 0 || p->heads % p->kv_heads || p->batch > 65535 || p->heads > 65535)
+    return STA_ERR_SHAPE;
+  if (p->head_dim != 64 && p->head_dim != 128) return STA_ERR_UNSUPPORTED;
+  if (!io_type_ok(p->type)) return STA_ERR_UNSUPPORTED;
+  if (p->window < 0 || p->sinks < 0 || !(p->scale == p->scale) || std::isinf(p->scale)) return STA_ERR_INVALID_ARG;
+  // positions reach kv_len and -q_len: kept clear of kNoWindow
+  if (p->q_len >= sta::kNoWindow / 2 || p->kv_len >= sta::kNoWindow / 2) return STA_ERR_SHAPE;
+  const long long bh = (long long)p->batch * p->heads;
+  if (bh * p->q_len >= kMaxRows || (long long)p->batch * p->kv_heads * p->kv_len >= kMaxRows ||
+      (long long)p->heads * p->q_rows >= kMaxRows || (long long)p->kv_heads * p->kv_rows >= kMaxRows)
+    return STA_ERR_SHAPE;
+  return STA_OK;
+}
+
+// Rows of lse and D.
+size_t stat_rows(const sta_window_problem *p) {
+  const size_t dense = (size_t)p->batch * p->heads * p->q_len, packed = (size_t)p->heads * p->q_rows;
+  return dense > packed ? dense : packed;
+}
+
+size_t window_fwd_bytes(const sta_window_problem *) { return kStatusBytes; }
+size_t window_bwd_bytes(const sta_window_problem *p) { return kStatusBytes + round256(stat_rows(p) * 4); }
+
+sta::WinParams window_params(const sta_window_problem *p, const int32_t *cu_q, const int32_t *cu_kv, void *ws) {
+  sta::WinParams w{};
+  w.batch = p->batch, w.heads = p->heads, w.kv_heads = p->kv_heads, w.group = p->heads / p->kv_heads, w.d = p->head_dim;
+  w.q_len = p->q_len, w.kv_len = p->kv_len, w.q_rows = p->q_rows, w.kv_rows = p->kv_rows;
+  w.window = p->window == 0 || p->window > sta::kNoWindow ? sta::kNoWindow : p->window;
+  w.sinks = p->sinks < sta::kNoWindow ? p->sinks : sta::kNoWindow;
+  w.cu_q = cu_q, w.cu_kv = cu_kv;
+  w.scale = p->scale > 0.f ? p->scale : 1.f / std::sqrt((float)p->head_dim);
+  w.scale_log2 = w.scale * 1.4426950408889634f;
+  w.status = static_cast<int *>(ws);
+  return w;
+}
+
+sta_status finish(void *ws, cudaStream_t stream, uint32_t flags) {
+  if (flags & STA_CALL_CHECK) {
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return STA_ERR_CUDA;
+    int st = 0;
+    if (ws && cudaMemcpy(&st, ws, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return STA_ERR_CUDA;
+    if (st != 0) return STA_ERR_TIMEOUT;
+  }
+  return STA_OK;
+}
+
+sta_status check_tensors(const sta_window_problem *p, bool packed, const sta_rows *const *q_side, int nq,
+                         const sta_rows *const *kv_side, int nkv) {
+  const long long batch = packed ? 1 : p->batch;
+  for (int i = 0; i < nq; ++i)
+    if (const sta_status st = check_rows(q_side[i], batch, p->heads, packed ? p->q_rows : p->q_len)) return st;
+  for (int i = 0; i < nkv; ++i)
+    if (const sta_status st = check_rows(kv_side[i], batch, p->kv_heads, packed ? p->kv_rows : p->kv_len)) return st;
+  return STA_OK;
+}
+
+sta_status check_workspace(const void *ws, size_t have, size_t need) {
+  if (!ws || have < need) return STA_ERR_WORKSPACE;
+  return aligned16(ws) ? STA_OK : STA_ERR_ALIGNMENT;
+}
+
+sta_status check_cache(const sta_cache *c, int32_t batch, int32_t table_pages) {
+  if (!c) return STA_ERR_INVALID_ARG;
+  if (c->pages < 1 || c->kv_heads < 1 || c->kv_heads > 65535 || c->page_size < 1 || batch < 1 || batch > 32767 ||
+      table_pages < 1 || (long long)table_pages * c->page_size >= sta::kNoWindow / 2 ||
+      (long long)c->pages * c->page_size > 0x7fffffffll)
+    return STA_ERR_SHAPE;
+  if (c->head_dim != 64 && c->head_dim != 128) return STA_ERR_UNSUPPORTED;
+  if (c->type != STA_TYPE_E4M3 && c->type != STA_TYPE_INT8) return STA_ERR_UNSUPPORTED;
+  if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) return STA_ERR_UNSUPPORTED;
+  if (c->page_size % c->block) return STA_ERR_SHAPE;
+  return STA_OK;
+}
+
+sta_status check_cache_pointers(const sta_cache *c, const int32_t *table, const int32_t *per_sequence) {
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale || !table || !per_sequence) return STA_ERR_INVALID_ARG;
+  const void *p[] = {c->k, c->v, c->k_scale, c->v_scale};
+  for (const void *x : p)
+    if (!aligned16(x)) return STA_ERR_ALIGNMENT;
+  return STA_OK;
+}
+
+sta::CacheParams cache_params(const sta_cache *c, const int32_t *table, int32_t table_pages) {
+  sta::CacheParams p{};
+  p.pages = c->pages, p.kv_heads = c->kv_heads, p.page_size = c->page_size, p.block = c->block, p.d = c->head_dim;
+  p.k = static_cast<uint8_t *>(c->k), p.v = static_cast<uint8_t *>(c->v);
+  p.k_scale = c->k_scale, p.v_scale = c->v_scale;
+  p.table = table, p.table_pages = table_pages;
+  return p;
+}
+
+sta_status move_call(bool write, const sta_cache *c, int32_t batch, int32_t rows, const sta_rows *k, const sta_rows *v,
+                     int32_t type, const int32_t *table, int32_t table_pages, const int32_t *start,
+                     const int32_t *count, void *stream_, uint32_t flags) {
+  if (const sta_status st = check_cache(c, batch, table_pages)) return st;
+  if (rows < 0 || (long long)batch * c->kv_heads * rows >= kMaxRows) return STA_ERR_SHAPE;
+  if (!io_type_ok(type)) return STA_ERR_UNSUPPORTED;
+  if (flags & ~STA_CALL_CHECK) return STA_ERR_INVALID_ARG;
+  if (const sta_status st = check_cache_pointers(c, table, start)) return st;
+  if (const sta_status st = check_rows(k, batch, c->kv_heads, rows)) return st;
+  if (const sta_status st = check_rows(v, batch, c->kv_heads, rows)) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (rows > 0) {
+    const sta::CacheMove m{cache_params(c, table, table_pages), batch, rows, rows_of(k), rows_of(v), start, count};
+    const cudaError_t e = write ? sta::launch_cache_write(m, c->type, type, stream)
+                                : sta::launch_cache_read(m, c->type, type, stream);
+    if (e != cudaSuccess) return STA_ERR_CUDA;
+  }
+  return finish(nullptr, stream, flags);
+}
+
+}  // namespace
+
+extern "C" {
+
+sta_status sta_window_workspace_size(const sta_window_problem *p, size_t *fwd, size_t *bwd) {
+  if (const sta_status st = check_problem(p)) return st;
+  if (fwd) *fwd = window_fwd_bytes(p);
+  if (bwd) *bwd = window_bwd_bytes(p);
+  return STA_OK;
+}
+
+sta_status sta_window_forward(const sta_window_problem *p, const sta_rows *q, const sta_rows *k, const sta_rows *v,
+                              const sta_rows *o, float *lse, const int32_t *cu_q, const int32_t *cu_kv, void *ws,
+                              size_t ws_bytes, void *stream_, uint32_t flags) {
+  if (const sta_status st = check_problem(p)) return st;
+  if ((flags & ~STA_CALL_CHECK) || (cu_q == nullptr) != (cu_kv == nullptr)) return STA_ERR_INVALID_ARG;
+  const sta_rows *qs[] = {q, o}, *ks[] = {k, v};
+  if (const sta_status st = check_tensors(p, cu_q, qs, 2, ks, 2)) return st;
+  if (const sta_status st = check_workspace(ws, ws_bytes, window_fwd_bytes(p))) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  sta::WinParams w = window_params(p, cu_q, cu_kv, ws);
+  w.q = rows_of(q), w.k = rows_of(k), w.v = rows_of(v), w.o = rows_of(o), w.lse = lse;
+  if ((flags & STA_CALL_CHECK) && cudaMemsetAsync(ws, 0, sizeof(int), stream) != cudaSuccess) return STA_ERR_CUDA;
+  if (p->q_len > 0 && sta::launch_window_forward(w, p->type, stream) != cudaSuccess) return STA_ERR_CUDA;
+  return finish(ws, stream, flags);
+}
+
+sta_status sta_window_backward(const sta_window_problem *p, const sta_rows *q, const sta_rows *k, const sta_rows *v,
+                               const sta_rows *o, const float *lse, const sta_rows *dout, const sta_rows *dq,
+                               const sta_rows *dk, const sta_rows *dv, const int32_t *cu_q, const int32_t *cu_kv,
+                               void *ws, size_t ws_bytes, void *stream_, uint32_t flags) {
+  if (const sta_status st = check_problem(p)) return st;
+  if ((flags & ~STA_CALL_CHECK) || (cu_q == nullptr) != (cu_kv == nullptr) || !lse) return STA_ERR_INVALID_ARG;
+  const sta_rows *qs[] = {q, o, dout, dq}, *ks[] = {k, v, dk, dv};
+  if (const sta_status st = check_tensors(p, cu_q, qs, 4, ks, 4)) return st;
+  if (const sta_status st = check_workspace(ws, ws_bytes, window_bwd_bytes(p))) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  sta::WinParams w = window_params(p, cu_q, cu_kv, ws);
+  w.q = rows_of(q), w.k = rows_of(k), w.v = rows_of(v), w.o = rows_of(o), w.dout = rows_of(dout);
+  w.dq = rows_of(dq), w.dk = rows_of(dk), w.dv = rows_of(dv);
+  w.lse = const_cast<float *>(lse);
+  w.dd = reinterpret_cast<float *>(static_cast<char *>(ws) + kStatusBytes);
+  if ((flags & STA_CALL_CHECK) && cudaMemsetAsync(ws, 0, sizeof(int), stream) != cudaSuccess) return STA_ERR_CUDA;
+  if ((p->q_len > 0 || p->kv_len > 0) && sta::launch_window_backward(w, p->type, stream) != cudaSuccess)
+    return STA_ERR_CUDA;
+  return finish(ws, stream, flags);
+}
+
+sta_status sta_cache_write(const sta_cache *c, int32_t batch, int32_t rows, const sta_rows *k, const sta_rows *v,
+                           int32_t in_type, const int32_t *table, int32_t table_pages, const int32_t *start,
+                           const int32_t *count, void *stream, uint32_t flags) {
+  return move_call(true, c, batch, rows, k, v, in_type, table, table_pages, start, count, stream, flags);
+}
+
+sta_status sta_cache_read(const sta_cache *c, int32_t batch, int32_t rows, const sta_rows *k, const sta_rows *v,
+                          int32_t out_type, const int32_t *table, int32_t table_pages, const int32_t *start,
+                          const int32_t *count, void *stream, uint32_t flags) {
+  return move_call(false, c, batch, rows, k, v, out_type, table, table_pages, start, count, stream, flags);
+}
+
+sta_status sta_cache_workspace_size(const sta_cache *c, int32_t batch, int32_t heads, int32_t q_len,
+                                    int32_t table_pages, int32_t window, int32_t sinks, size_t *bytes) {
+  if (const sta_status st = check_cache(c, batch, table_pages)) return st;
+  if (!bytes || window < 0 || sinks < 0) return STA_ERR_INVALID_ARG;
+  if (heads < 1 || heads > 65535 || heads % c->kv_heads || q_len < 0 || q_len >= sta::kNoWindow / 2 ||
+      (long long)batch * heads * q_len >= kMaxRows)
+    return STA_ERR_SHAPE;
+  *bytes = kStatusBytes;
+  return STA_OK;
+}
+
+sta_status sta_cache_attention(const sta_cache *c, int32_t batch, int32_t heads, int32_t q_len, int32_t window,
+                               int32_t sinks, float scale, int32_t type, const sta_rows *q, const sta_rows *o,
+                               float *lse, const int32_t *table, int32_t table_pages, const int32_t *lengths, void *ws,
+                               size_t ws_bytes, void *stream_, uint32_t flags) {
+  size_t need = 0;
+  if (const sta_status st = sta_cache_workspace_size(c, batch, heads, q_len, table_pages, window, sinks, &need)) return st;
+  if (!io_type_ok(type)) return STA_ERR_UNSUPPORTED;
+  if ((flags & ~STA_CALL_CHECK) || !(scale == scale) || std::isinf(scale)) return STA_ERR_INVALID_ARG;
+  if (const sta_status st = check_cache_pointers(c, table, lengths)) return st;
+  if (const sta_status st = check_rows(q, batch, heads, q_len)) return st;
+  if (const sta_status st = check_rows(o, batch, heads, q_len)) return st;
+  if (const sta_status st = check_workspace(ws, ws_bytes, need)) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  sta::CacheAttn a{};
+  a.c = cache_params(c, table, table_pages);
+  a.batch = batch, a.heads = heads, a.group = heads / c->kv_heads, a.q_len = q_len;
+  a.window = window == 0 || window > sta::kNoWindow ? sta::kNoWindow : window;
+  a.sinks = sinks < sta::kNoWindow ? sinks : sta::kNoWindow;
+  a.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt((float)c->head_dim)) * 1.4426950408889634f;
+  a.q = rows_of(q), a.o = rows_of(o), a.lse = lse, a.lengths = lengths;
+  if (q_len > 0 && sta::launch_cache_attention(a, c->type, type, stream) != cudaSuccess) return STA_ERR_CUDA;
+  return finish(nullptr, stream, flags);
+}
+
+}  // extern "C"

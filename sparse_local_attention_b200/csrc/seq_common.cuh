@@ -1,0 +1,78 @@
+// seq_common.cuh -- device helpers shared by the token-sequence kernels:
+// element conversions, the rows of a (packed or dense) sequence, and the
+// addressing of a paged cache.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cstdint>
+
+#include "seq_kernels.h"
+
+namespace sta {
+
+// fp32 <-> the 16-bit types, two at a time; lo in bits 0..15.
+template <class T> struct Elem;
+template <> struct Elem<__nv_bfloat16> {
+  static constexpr float kMax = 3.3895313892515355e38f;
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+template <> struct Elem<__half> {
+  static constexpr float kMax = 65504.f;
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+
+// Rows [q0, q0 + nq) of the query tensors and [k0, k0 + nk) of the key tensors
+// hold sequence b; `slice` is its batch index in the tensors (0 when packed).
+struct Sequence {
+  int slice, q0, nq, k0, nk;
+};
+
+__device__ __forceinline__ void packed_range(const int32_t *cu, int b, int rows, int longest, int &first, int &n) {
+  first = min(max(__ldg(cu + b), 0), rows);
+  const int end = min(max(__ldg(cu + b + 1), first), rows);
+  n = min(end - first, longest);
+}
+
+__device__ __forceinline__ Sequence sequence(const WinParams &p, int b) {
+  Sequence s{b, 0, p.q_len, 0, p.kv_len};
+  if (p.cu_q) {
+    s.slice = 0;
+    packed_range(p.cu_q, b, p.q_rows, p.q_len, s.q0, s.nq);
+    packed_range(p.cu_kv, b, p.kv_rows, p.kv_len, s.k0, s.nk);
+  }
+  return s;
+}
+
+// Index of a query row in lse and D.
+__device__ __forceinline__ long long stat_row(const WinParams &p, const Sequence &s, int h, int row) {
+  return p.cu_q ? (long long)h * p.q_rows + s.q0 + row : ((long long)s.slice * p.heads + h) * p.q_len + row;
+}
+
+__device__ __forceinline__ bool visible(int pos, int key, int window, int sinks) {
+  return key <= pos && (key > pos - window || key < sinks);
+}
+
+// Page that holds token `pos` of sequence b, or -1 (absent, or past the table).
+__device__ __forceinline__ int page_of(const CacheParams &c, int b, int pos) {
+  const int i = pos / c.page_size;
+  if (pos < 0 || i >= c.table_pages) return -1;
+  const int page = __ldg(c.table + (long long)b * c.table_pages + i);
+  return (unsigned)page < (unsigned)c.pages ? page : -1;
+}
+
+}  // namespace sta

@@ -1,0 +1,70 @@
+// seq_kernels.h -- parameter blocks and launchers of the token-sequence
+// operators, shared by their host API (seq_api.cpp) and the CUDA kernels.
+// Internal to libsta.so.
+#pragma once
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "../../include/sta.h"
+
+namespace sta {
+
+// A window that hides nothing: every position minus it is far below zero.
+constexpr int kNoWindow = 1 << 30;
+
+// Strides of a tensor of rows, in elements.
+struct Rows {
+  char *p;
+  long long b, h, r;
+};
+
+// One problem of sta_window_forward / sta_window_backward.
+struct WinParams {
+  int batch, heads, kv_heads, group, d;
+  int q_len, kv_len;    // rows of every sequence, or of the longest one (packed)
+  int q_rows, kv_rows;  // packed: rows of the tensors
+  int window, sinks;    // window >= 1
+  const int32_t *cu_q, *cu_kv;
+  float scale, scale_log2;
+  Rows q, k, v, o, dout, dq, dk, dv;
+  float *lse;
+  float *dd;  // backward: D = rowsum(dO o O), laid out like lse
+  int *status;
+  unsigned long long wait_limit_ns;
+};
+
+// The cache of sta_cache, with its pages addressed through a table.
+struct CacheParams {
+  int pages, kv_heads, page_size, block, d;
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  const int32_t *table;
+  int table_pages;
+};
+
+// sta_cache_write / sta_cache_read.
+struct CacheMove {
+  CacheParams c;
+  int batch, rows;
+  Rows k, v;
+  const int32_t *start, *count;
+};
+
+cudaError_t launch_cache_write(const CacheMove &m, int cache_type, int io_type, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheMove &m, int cache_type, int io_type, cudaStream_t stream);
+
+// sta_cache_attention.
+struct CacheAttn {
+  CacheParams c;
+  int batch, heads, group, q_len, window, sinks;
+  float scale_log2;
+  Rows q, o;
+  float *lse;
+  const int32_t *lengths;
+};
+cudaError_t launch_cache_attention(const CacheAttn &a, int cache_type, int io_type, cudaStream_t stream);
+
+cudaError_t launch_window_forward(const WinParams &p, int type, cudaStream_t stream);
+cudaError_t launch_window_backward(const WinParams &p, int type, cudaStream_t stream);
+
+}  // namespace sta

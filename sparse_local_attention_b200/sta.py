@@ -32,7 +32,9 @@ STA_CALL_CHECK = 0x1
 EXPORTED = ["sta_plan_create", "sta_plan_destroy", "sta_plan_workspace_size", "sta_plan_kv_tiles",
             "sta_plan_q_tiles", "sta_plan_geometry", "sta_permute", "sta_forward", "sta_backward",
             "sta_status_string", "sta_set_wait_limit_ns", "sta_backward_noalloc", "sta_plan_launches",
-            "sta_plan_host_workspace_size", "sta_forward_host", "sta_plan_work_items"]
+            "sta_plan_host_workspace_size", "sta_forward_host", "sta_plan_work_items",
+            "sta_window_workspace_size", "sta_window_forward", "sta_window_backward", "sta_cache_write",
+            "sta_cache_read", "sta_cache_workspace_size", "sta_cache_attention"]
 STA_WORK_FORWARD, STA_WORK_FORWARD_HOST, STA_WORK_DKDV, STA_WORK_DQ = 0, 1, 2, 3
 
 
@@ -50,6 +52,12 @@ class _Problem(ctypes.Structure):
                 ("flags", ctypes.c_uint32)]
 
 
+class _Rows(ctypes.Structure):  # sta_rows
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("head", ctypes.c_int64),
+                ("row", ctypes.c_int64)]
+
+
+_ROWS = ctypes.POINTER(_Rows)
 _lib = None
 
 
@@ -85,6 +93,15 @@ def lib() -> ctypes.CDLL:
     L.sta_plan_host_workspace_size.argtypes = [vp, szp]
     L.sta_forward_host.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, vp, ctypes.c_uint32]
     L.sta_plan_work_items.argtypes = [vp, ctypes.c_int32, i32p, sz, szp, i32p]
+    i32, u32 = ctypes.c_int32, ctypes.c_uint32  # the token-sequence calls (window.py, kv_cache.py); vp: by reference
+    L.sta_window_workspace_size.argtypes = [vp, szp, szp]
+    L.sta_window_forward.argtypes = [vp, *[_ROWS] * 4, vp, vp, vp, vp, sz, vp, u32]
+    L.sta_window_backward.argtypes = [vp, *[_ROWS] * 4, vp, *[_ROWS] * 4, vp, vp, vp, sz, vp, u32]
+    for name in ("sta_cache_write", "sta_cache_read"):
+        getattr(L, name).argtypes = [vp, i32, i32, _ROWS, _ROWS, i32, vp, i32, vp, vp, vp, u32]
+    L.sta_cache_workspace_size.argtypes = [vp, i32, i32, i32, i32, i32, i32, szp]
+    L.sta_cache_attention.argtypes = [vp, i32, i32, i32, i32, i32, ctypes.c_float, i32, _ROWS, _ROWS, vp, vp, i32, vp,
+                                      vp, sz, vp, u32]
     L.sta_status_string.argtypes = [ctypes.c_int]
     L.sta_status_string.restype = ctypes.c_char_p
     L.sta_set_wait_limit_ns.argtypes = [ctypes.c_uint64]

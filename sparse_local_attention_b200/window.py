@@ -1,0 +1,298 @@
+"""Causal sliding-window attention with sinks over token sequences.
+
+The one-dimensional counterpart of sliding tile attention, for models that
+produce their tokens in order: a query sees the last ``window`` tokens up to
+its own and the first ``sinks`` tokens of its sequence.  Argument marshalling
+for sta_window_forward / sta_window_backward of include/sta.h, which state the
+semantics; the work runs in the CUDA kernels of libsta.so.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import functools
+from typing import Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from .sta import STA_CALL_CHECK, _check, _ptr, _Rows, lib
+
+STA_TYPE_BF16, STA_TYPE_FP16, STA_TYPE_E4M3, STA_TYPE_INT8 = 0, 1, 2, 3
+IO_TYPES = {torch.bfloat16: STA_TYPE_BF16, torch.float16: STA_TYPE_FP16}
+
+
+class _WindowProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "heads", "kv_heads", "head_dim", "q_len", "kv_len", "q_rows",
+                                              "kv_rows", "window", "sinks", "type")] + [("scale", ctypes.c_float)]
+
+
+def _rows(t: torch.Tensor) -> _Rows:
+    b, h, r, _ = t.stride()
+    return _Rows(t.data_ptr(), b, h, r)
+
+
+def _in_place(t: torch.Tensor) -> bool:
+    """Whether the kernels can address the tensor's rows where they are:
+    contiguous rows, 16-byte aligned, at positive strides that are multiples
+    of 8 elements (a stride of an extent of one is not used)."""
+    if t.stride(3) != 1 or t.data_ptr() % 16:
+        return False
+    return all(n <= 1 or (s > 0 and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()[:3]))
+
+
+def _input(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
+    """An input of [batch, heads, rows, d]: read in place if its strides allow it, else copied."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+    return t if _in_place(t) else t.clone(memory_format=torch.contiguous_format)
+
+
+def _output(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
+    if _input(t, name, shape, dtype, device) is not t:
+        raise ValueError(f"{name}: expected 16-byte aligned rows at strides of multiples of 8, got strides {t.stride()}")
+    return t
+
+
+def _flat(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> Optional[torch.Tensor]:
+    """A contiguous device tensor of exactly this shape (int32 tables, fp32 statistics), or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t
+
+
+@contextlib.contextmanager
+def _switched(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors on {device}")
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _on(device, stream):
+    """Context of a call: the tensors' device is current, and so is `stream` if
+    one is given, so that what the call allocates belongs to it."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return _switched(device, stream)
+
+
+def _current_stream(device) -> ctypes.c_void_p:
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _scratch(workspace: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {device}")
+    return workspace
+
+
+def _new(like: torch.Tensor, packed: bool) -> torch.Tensor:
+    """An output laid out as `like`; packed: zero, since rows outside every sequence are not written."""
+    t = torch.empty_like(like)
+    if not _in_place(t):
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    return t.zero_() if packed else t
+
+
+@functools.lru_cache(maxsize=256)
+def _sized(batch, heads, kv_heads, head_dim, q_len, kv_len, q_rows, kv_rows, window, sinks, dtype, scale):
+    """(problem, forward bytes, backward bytes) of one problem."""
+    p = _WindowProblem(batch, heads, kv_heads, head_dim, q_len, kv_len, q_rows, kv_rows, window, sinks, dtype, scale)
+    fwd, bwd = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().sta_window_workspace_size(ctypes.byref(p), ctypes.byref(fwd), ctypes.byref(bwd)),
+           "sta_window_workspace_size")
+    return p, fwd.value, bwd.value
+
+
+class _Call:
+    """The checked arguments that the forward and backward of one problem share."""
+
+    def __init__(self, q, k, v, window, sinks, scale, cu_q, cu_kv, max_q, max_kv):
+        for t, name in ((q, "q"), (k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+            if t.dim() != 4:
+                raise ValueError(f"{name}: expected [batch, heads, rows, head_dim], got {tuple(t.shape)}")
+        if q.dtype not in IO_TYPES:
+            raise ValueError(f"q: expected bfloat16 or float16, got {q.dtype}")
+        if (cu_q is None) != (cu_kv is None):
+            raise ValueError("cu_q and cu_kv go together")
+        self.dtype, self.device = q.dtype, q.device
+        self.q_shape, self.kv_shape = tuple(q.shape), (q.shape[0], k.shape[1], k.shape[2], q.shape[3])
+        self.q = _input(q, "q", self.q_shape, q.dtype, q.device)
+        self.k = _input(k, "k", self.kv_shape, q.dtype, q.device)
+        self.v = _input(v, "v", self.kv_shape, q.dtype, q.device)
+        batch, heads, nq, d = self.q_shape
+        kv_heads, nk = self.kv_shape[1:3]
+        self.packed = cu_q is not None
+        self.cu_q, self.cu_kv = cu_q, cu_kv
+        if self.packed:
+            if batch != 1:
+                raise ValueError("packed sequences: expected a batch of 1")
+            batch = cu_q.numel() - 1
+            _flat(cu_q, "cu_q", (batch + 1,), torch.int32, q.device)
+            _flat(cu_kv, "cu_kv", (batch + 1,), torch.int32, q.device)
+            rows = (nq, nk)
+            nq, nk = min(int(max_q) or nq, nq), min(int(max_kv) or nk, nk)
+        else:
+            rows = (0, 0)
+        self.empty = 0 in self.q_shape or (self.packed and batch == 0)
+        if not self.empty:
+            self.problem, self.fwd_bytes, self.bwd_bytes = _sized(
+                batch, heads, kv_heads, d, nq, nk, *rows, int(window), int(sinks), IO_TYPES[q.dtype], float(scale))
+
+
+def _forward(c: _Call, o=None, lse=None, workspace=None, check=False, want_lse=True):
+    if o is None:
+        o = _new(c.q, c.packed)
+    else:
+        _output(o, "o", c.q_shape, c.dtype, c.device)
+    if lse is None and want_lse:
+        lse = torch.empty(c.q_shape[:3], dtype=torch.float32, device=c.device)
+        if c.packed:
+            lse.fill_(float("-inf"))
+    _flat(lse, "lse", c.q_shape[:3], torch.float32, c.device)
+    if not c.empty:
+        if 0 in c.kv_shape:  # no keys at all: every row is empty
+            o.zero_()
+            if lse is not None:
+                lse.fill_(float("-inf"))
+            return o, lse
+        ws = _scratch(workspace, c.fwd_bytes, c.device)
+        st = lib().sta_window_forward(ctypes.byref(c.problem), _rows(c.q), _rows(c.k), _rows(c.v), _rows(o), _ptr(lse),
+                                      _ptr(c.cu_q), _ptr(c.cu_kv), _ptr(ws), ws.numel() * ws.element_size(),
+                                      _current_stream(c.device), STA_CALL_CHECK if check else 0)
+        _check(st, "sta_window_forward")
+    return o, lse
+
+
+def _backward(c: _Call, o, lse, dout, dq=None, dk=None, dv=None, workspace=None, check=False):
+    o = _input(o, "o", c.q_shape, c.dtype, c.device)
+    dout = _input(dout, "dout", c.q_shape, c.dtype, c.device)
+    _flat(lse, "lse", c.q_shape[:3], torch.float32, c.device)
+    given = []
+    for t, like, shape, name in ((dq, c.q, c.q_shape, "dq"), (dk, c.k, c.kv_shape, "dk"), (dv, c.v, c.kv_shape, "dv")):
+        given.append(_new(like, c.packed) if t is None else _output(t, name, shape, c.dtype, c.device))
+    dq, dk, dv = given
+    if c.empty or 0 in c.kv_shape:
+        for t in given:
+            t.zero_()
+        return dq, dk, dv
+    ws = _scratch(workspace, c.bwd_bytes, c.device)
+    st = lib().sta_window_backward(ctypes.byref(c.problem), _rows(c.q), _rows(c.k), _rows(c.v), _rows(o), _ptr(lse),
+                                   _rows(dout), _rows(dq), _rows(dk), _rows(dv), _ptr(c.cu_q), _ptr(c.cu_kv),
+                                   _ptr(ws), ws.numel() * ws.element_size(), _current_stream(c.device),
+                                   STA_CALL_CHECK if check else 0)
+    _check(st, "sta_window_backward")
+    return dq, dk, dv
+
+
+def _device_of(q) -> torch.device:
+    if not isinstance(q, torch.Tensor):
+        raise TypeError(f"q: expected a torch.Tensor, got {type(q).__name__}")
+    if not q.is_cuda:
+        raise ValueError(f"q: expected a CUDA tensor, got one on {q.device}")
+    return q.device
+
+
+def window_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int = 0, sinks: int = 0,
+                   scale: float = 0.0, cu_q: Optional[torch.Tensor] = None, cu_kv: Optional[torch.Tensor] = None,
+                   max_q: int = 0, max_kv: int = 0, o: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None,
+                   check: bool = False, want_lse: bool = True):
+    """(o, lse) of sliding-window attention with sinks.
+
+    q [batch, heads, Nq, d], k and v [batch, kv_heads, Nk, d], bf16 or fp16, d
+    64 or 128, kv_heads a divisor of heads; query row i sits at position
+    i + Nk - Nq.  window 0: no limit.  Any strides with contiguous, 16-byte
+    aligned rows are read in place; other inputs are copied first.
+
+    Packed sequences: a batch of 1 whose rows [cu[b], cu[b + 1]) hold sequence
+    b (cu_q, cu_kv: int32 device tensors); max_q and max_kv are bounds on the
+    sequences' lengths (default: the rows there are; longer sequences are cut).
+    Rows outside every sequence are left as they were in an `o` or `lse` that
+    is passed in, and 0 (-inf) in a new one."""
+    with _on(_device_of(q), stream):
+        return _forward(_Call(q, k, v, window, sinks, scale, cu_q, cu_kv, max_q, max_kv), o, lse, workspace, check,
+                        want_lse)
+
+
+def window_backward(q, k, v, o, lse, dout, window: int = 0, sinks: int = 0, scale: float = 0.0, cu_q=None, cu_kv=None,
+                    max_q: int = 0, max_kv: int = 0, dq=None, dk=None, dv=None, workspace=None, stream=None,
+                    check: bool = False):
+    """(dq, dk, dv) of window_forward from its inputs, its o and lse, and the
+    gradient of o.  dk and dv sum over the query heads that share a key head."""
+    with _on(_device_of(q), stream):
+        return _backward(_Call(q, k, v, window, sinks, scale, cu_q, cu_kv, max_q, max_kv), o, lse, dout, dq, dk, dv,
+                         workspace, check)
+
+
+def _accumulators(tensors):
+    """The leaves' gradient accumulators, marked with the stream of this use.
+
+    A gradient that is accumulated into a leaf runs on the stream on which the
+    leaf was first used for as long as a graph of that use lives.  A backward
+    pass captured on another stream would have to join that stream, which ends
+    the capture and the process, so such a capture is refused.  The caller
+    holds the result until its own graph does (the mark goes with it)."""
+    capturing = torch.cuda.is_current_stream_capturing()
+    here = torch.cuda.current_stream().cuda_stream
+    nodes = [torch.autograd.graph.get_gradient_edge(t).node for t in tensors if t.requires_grad and t.is_leaf]
+    for n in nodes:
+        if capturing and n.metadata.get("sta_stream", here) != here:
+            raise RuntimeError("sliding_window_attention: an eager graph of the same leaf tensors is still alive; "
+                               "release it (and its outputs) before capturing, or capture on detached leaves")
+        n.metadata.setdefault("sta_stream", here)
+    return nodes
+
+
+class _SlidingWindowAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, args):
+        with _on(q.device, None):
+            c = _Call(q, k, v, *args)
+            o, lse = _forward(c)
+        ctx.save_for_backward(q, k, v, o, lse)
+        ctx.args = args
+        return o
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        q, k, v, o, lse = ctx.saved_tensors
+        with _on(q.device, None):
+            dq, dk, dv = _backward(_Call(q, k, v, *ctx.args), o, lse, dout)
+        return dq, dk, dv, None
+
+
+def sliding_window_attention(q, k, v, window: int = 0, sinks: int = 0, scale: float = 0.0, cu_q=None, cu_kv=None,
+                             max_q: int = 0, max_kv: int = 0) -> torch.Tensor:
+    """window_forward's o, differentiable: when q, k or v requires a gradient
+    the backward is one sta_window_backward call.  Shared key heads and
+    broadcast inputs get the sum of their gradients."""
+    args = (window, sinks, scale, cu_q, cu_kv, max_q, max_kv)
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, v)):
+        device = _device_of(q)
+        with _on(device, None):
+            held = _accumulators((q, k, v))
+            o = _SlidingWindowAttention.apply(q, k, v, args)
+            del held
+            return o
+    return window_forward(q, k, v, *args, want_lse=False)[0]

@@ -1,0 +1,390 @@
+"""Sliding-window attention with sinks: forward and backward against the fp64
+definition, over types, head layouts, lengths, strides and masks; packed
+sequences; graphs, streams and refusals."""
+import ctypes
+
+import pytest
+import torch
+
+import seq_ref
+from sparse_local_attention_b200 import sliding_window_attention, sta, window_backward, window_forward
+from sparse_local_attention_b200.window import _WindowProblem
+
+BF16, FP16 = torch.bfloat16, torch.float16
+
+
+def randn(*shape, seed, dtype, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dtype)
+
+
+def make(heads, kv_heads, nq, nk, d, dtype, batch=1, seed=0, do_scale=1.0):
+    return (randn(batch, heads, nq, d, seed=seed, dtype=dtype), randn(batch, kv_heads, nk, d, seed=seed + 1, dtype=dtype),
+            randn(batch, kv_heads, nk, d, seed=seed + 2, dtype=dtype),
+            randn(batch, heads, nq, d, seed=seed + 3, dtype=dtype, scale=do_scale))
+
+
+def compare(q, k, v, do, window, sinks, scale=0.0, backward=True):
+    """Device results of a dense batch against the definition, sequence by sequence."""
+    qd, kd, vd, dod = (t.cuda() for t in (q, k, v, do))
+    o, lse = window_forward(qd, kd, vd, window, sinks, scale, check=True)
+    grads = window_backward(qd, kd, vd, o, lse, dod, window, sinks, scale, check=True) if backward else ()
+    mask = seq_ref.mask_of(q.shape[2], k.shape[2], window, sinks)
+    for b in range(q.shape[0]):
+        want = seq_ref.attention(q[b], k[b], v[b], mask, scale or q.shape[3] ** -0.5, do[b] if backward else None, q.dtype)
+        for name, got in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
+            seq_ref.check(got[b], want[name], f"{name} of sequence {b}")
+    return (o, lse, *grads)
+
+
+CASES = [
+    # heads, kv_heads, nq, nk, d, window, sinks
+    (1, 1, 1, 1, 64, 1, 0),
+    (4, 2, 1, 300, 128, 100, 4),       # one token
+    (6, 2, 3, 1000, 64, 0, 0),         # a few tokens, no window
+    (2, 2, 128, 128, 64, 0, 0),        # one whole tile
+    (3, 1, 127, 127, 128, 50, 3),      # one row short of a tile, an odd group
+    (2, 1, 129, 129, 64, 128, 1),      # one row past a tile
+    (4, 4, 260, 260, 128, 1, 0),       # every row sees itself alone
+    (2, 2, 300, 700, 64, 77, 130),     # sinks past one tile, keys before the queries
+    (5, 5, 513, 513, 128, 256, 200),   # sinks that meet the window
+    (2, 1, 200, 64, 64, 30, 4),        # more queries than keys: rows that see nothing
+    (8, 1, 333, 901, 128, 300, 16),    # one key head for all
+    (2, 2, 640, 640, 64, 10000, 5),    # a window longer than the sequence
+    (2, 2, 70, 0, 64, 10, 2),          # no keys
+    (4, 4, 1500, 1500, 64, 96, 700),   # sinks over many tiles
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_against_the_definition(case, dtype):
+    heads, kv_heads, nq, nk, d, window, sinks = case
+    compare(*make(heads, kv_heads, nq, nk, d, dtype, batch=2, seed=nq + nk), window, sinks)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,do_scale,q_scale", [(FP16, 1e-3, 1.0), (BF16, 1e-6, 1.0), (FP16, 30.0, 4.0), (BF16, 1e4, 6.0)])
+def test_small_and_large_values(dtype, do_scale, q_scale):
+    """Gradients far below 1 keep their relative precision; peaked and large scores do not overflow."""
+    q, k, v, do = make(4, 2, 600, 600, 128, dtype, seed=5, do_scale=do_scale)
+    compare((q.float() * q_scale).to(dtype), k, v, do, 500, 4)
+
+
+@pytest.mark.gpu
+def test_scale_and_equal_scores():
+    q, k, v, do = make(2, 2, 400, 400, 64, BF16, seed=9)
+    compare(q, k, v, do, 90, 7, scale=0.37)
+    # equal scores: O is the mean of the visible values, the sum of P is exact
+    o, lse, *_ = compare(torch.zeros_like(q), k, v, do, 90, 7)
+    n = seq_ref.mask_of(400, 400, 90, 7).sum(-1).double()
+    assert (lse[0, 0].double().cpu() - n.log()).abs().max() < 1e-5
+
+
+@pytest.mark.gpu
+def test_gradients_against_differences():
+    """dq, dk, dv along random directions against central differences of the fp64 definition."""
+    q, k, v, do = make(4, 2, 150, 150, 64, FP16, seed=21)
+    mask, scale = seq_ref.mask_of(150, 150, 40, 6), 64 ** -0.5
+    _, _, dq, dk, dv = compare(q, k, v, do, 40, 6)
+
+    def loss(q, k, v):
+        return (seq_ref.attention(q[0], k[0], v[0], mask, scale)["o"][0] * do[0].double()).sum()
+
+    for i, (x, g) in enumerate(((q, dq), (k, dk), (v, dv))):
+        r = torch.randn(x.shape, generator=torch.Generator().manual_seed(i), dtype=torch.float64)
+        args = [t.double() for t in (q, k, v)]
+        h = 1e-5
+        up, down = list(args), list(args)
+        up[i], down[i] = args[i] + h * r, args[i] - h * r
+        want = (loss(*up) - loss(*down)) / (2 * h)
+        g64 = g.double().cpu()
+        # each element within a few roundings of fp16 (2^-11): the sum within their root mean square
+        assert abs((g64 * r).sum() - want) <= 8 * 2.0 ** -11 * (g64 * r).norm() + 1e-6, i
+
+
+def packed(lens_q, lens_k, heads, kv_heads, d, dtype, tail=37, seed=0):
+    tot_q, tot_k = sum(lens_q) + tail, sum(lens_k) + tail
+    q, k, v, do = (t for t in (randn(1, heads, tot_q, d, seed=seed, dtype=dtype), randn(1, kv_heads, tot_k, d, seed=seed + 1, dtype=dtype),
+                               randn(1, kv_heads, tot_k, d, seed=seed + 2, dtype=dtype), randn(1, heads, tot_q, d, seed=seed + 3, dtype=dtype)))
+    cu = [torch.tensor([0] + list(x), dtype=torch.int32).cumsum(0).to(torch.int32) for x in (lens_q, lens_k)]
+    return q, k, v, do, *cu
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (FP16, 64)])
+@pytest.mark.parametrize("lens_q,lens_k,window,sinks", [
+    ([5, 128, 1, 0, 300, 129], None, 64, 4),
+    ([1, 1, 1], [200, 0, 513], 100, 2),       # single tokens
+    ([130, 2, 257], [130, 700, 300], 0, 0),   # chunks with earlier keys
+    ([20, 200], [7, 40], 1000, 3),            # more queries than keys
+], ids=["mixed", "tokens", "chunks", "empty rows"])
+@pytest.mark.parametrize("bounds", [True, False], ids=["bounds", "no bounds"])
+def test_packed_sequences(dtype, d, lens_q, lens_k, window, sinks, bounds):
+    """Each sequence as if alone.  What lies between and behind sequences
+    (NaN here) reaches nothing, and rows behind the last one stay as they were."""
+    lens_k = lens_k or lens_q
+    q, k, v, do, cu_q, cu_k = packed(lens_q, lens_k, 6, 2, d, dtype, seed=sum(lens_q))
+    for t, n in ((q, sum(lens_q)), (k, sum(lens_k)), (v, sum(lens_k)), (do, sum(lens_q))):
+        t[:, :, n:] = float("nan")
+    qd, kd, vd, dod, cq, ck = (t.cuda() for t in (q, k, v, do, cu_q, cu_k))
+    kw = dict(cu_q=cq, cu_kv=ck, check=True, **(dict(max_q=max(lens_q), max_kv=max(lens_k)) if bounds else {}))
+    o, lse = torch.full_like(qd, 7.0), torch.full(q.shape[:3], 7.0).cuda()
+    window_forward(qd, kd, vd, window, sinks, o=o, lse=lse, **kw)
+    dq, dk, dv = torch.full_like(qd, 7.0), torch.full_like(kd, 7.0), torch.full_like(vd, 7.0)
+    window_backward(qd, kd, vd, o, lse, dod, window, sinks, dq=dq, dk=dk, dv=dv, **kw)
+    for b in range(len(lens_q)):
+        rq, rk = slice(int(cu_q[b]), int(cu_q[b + 1])), slice(int(cu_k[b]), int(cu_k[b + 1]))
+        mask = seq_ref.mask_of(lens_q[b], lens_k[b], window, sinks)
+        want = seq_ref.attention(q[0, :, rq], k[0, :, rk], v[0, :, rk], mask, d ** -0.5, do[0, :, rq], dtype)
+        for name, got, r in (("o", o, rq), ("lse", lse, rq), ("dq", dq, rq), ("dk", dk, rk), ("dv", dv, rk)):
+            seq_ref.check(got[0, :, r], want[name], f"{name} of sequence {b}")
+    for t, n in ((o, sum(lens_q)), (lse, sum(lens_q)), (dq, sum(lens_q)), (dk, sum(lens_k)), (dv, sum(lens_k))):
+        assert bool((t[:, :, n:] == 7.0).all())
+    # outputs that the call makes: zero (-inf) there
+    o2, lse2 = window_forward(qd, kd, vd, window, sinks, **kw)
+    n = sum(lens_q)
+    assert torch.equal(o2[:, :, :n], o[:, :, :n]) and torch.equal(lse2[:, :, :n], lse[:, :, :n])
+    assert bool((o2[:, :, n:] == 0).all()) and bool((lse2[:, :, n:] == float("-inf")).all())
+
+
+@pytest.mark.gpu
+def test_packed_bounds_cut_and_bad_starts_are_dropped():
+    """max_q below a length computes the sequence's first max_q rows against its
+    first max_kv keys; starts outside the tensor are cut to it."""
+    q, k, v, do, cu, _ = packed([200, 90], [200, 90], 2, 2, 64, BF16, tail=0, seed=3)
+    qd, kd, vd = (t.cuda() for t in (q, k, v))
+    o = torch.full_like(qd, 7.0)
+    window_forward(qd, kd, vd, 50, 4, cu_q=cu.cuda(), cu_kv=cu.cuda(), max_q=100, max_kv=100, o=o, check=True)
+    want = seq_ref.attention(q[0, :, :100], k[0, :, :100], v[0, :, :100], seq_ref.mask_of(100, 100, 50, 4), 64 ** -0.5)
+    seq_ref.check(o[0, :, :100], want["o"], "o")
+    assert bool((o[:, :, 100:200] == 7.0).all())
+    wild = torch.tensor([-5, 200, 10 ** 6], dtype=torch.int32).cuda()  # [0, 200) and [200, 290)
+    o3, _ = window_forward(qd, kd, vd, 50, 4, cu_q=wild, cu_kv=wild, check=True)
+    o4, _ = window_forward(qd, kd, vd, 50, 4, cu_q=cu.cuda(), cu_kv=cu.cuda(), check=True)
+    assert torch.equal(o3, o4)
+
+
+@pytest.mark.gpu
+def test_hidden_keys_reach_nothing():
+    """Keys that no query of the call sees hold NaN and infinities (and values
+    of the type's lowest and highest)."""
+    for nq, nk, window, sinks in ((40, 900, 100, 5), (1, 700, 64, 2), (300, 1200, 200, 130)):
+        q, k, v, do = make(4, 2, nq, nk, 64, BF16, seed=nq)
+        seen = seq_ref.mask_of(nq, nk, window, sinks).any(0)
+        clean = seq_ref.attention(q[0], k[0], v[0], seq_ref.mask_of(nq, nk, window, sinks), 0.125, do[0])
+        for bad in (float("nan"), float("inf"), float("-inf"), torch.finfo(BF16).min, torch.finfo(BF16).max):
+            kb, vb = k.clone(), v.clone()
+            kb[:, :, ~seen] = bad
+            vb[:, :, ~seen] = bad
+            qd, kd, vd, dod = (t.cuda() for t in (q, kb, vb, do))
+            o, lse = window_forward(qd, kd, vd, window, sinks, check=True)
+            dq, dk, dv = window_backward(qd, kd, vd, o, lse, dod, window, sinks, check=True)
+            for name, got in (("o", o), ("lse", lse), ("dq", dq)):
+                seq_ref.check(got[0], clean[name], name)
+            for name, got in (("dk", dk), ("dv", dv)):
+                seq_ref.check(got[0][:, seen], tuple(t[:, seen] for t in clean[name]), name)
+                assert bool((got[0][:, ~seen] == 0).all()), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("nq,nk", [(1, 257), (190, 333)])
+def test_strides_orders_and_broadcasts(nq, nk):
+    """Rows outside heads, slices of wider tensors, unaligned views and expanded
+    inputs give what contiguous copies give."""
+    q, k, v, do = (t.cuda() for t in make(4, 4, nq, nk, 64, BF16, batch=2, seed=8))
+    args = (100, 3)
+    o, lse = window_forward(q, k, v, *args, check=True)
+    grads = window_backward(q, k, v, o, lse, do, *args, check=True)
+
+    def last(t):  # [batch, rows, heads, d] behind the same view
+        return t.transpose(1, 2).contiguous().transpose(1, 2)
+
+    def wide(t):  # heads inside a fused projection
+        w = torch.full((*t.shape[:3], 3 * t.shape[3]), float("nan"), dtype=t.dtype, device="cuda")
+        w[..., 64:128] = t
+        return w[..., 64:128]
+
+    def odd(t):  # an address and strides off the kernels' alignment
+        w = torch.zeros((*t.shape[:3], t.shape[3] + 3), dtype=t.dtype, device="cuda")
+        w[..., 1:65] = t
+        return w[..., 1:65]
+
+    for f in (last, wide, odd):
+        qf, kf, vf, df = f(q), f(k), f(v), f(do)
+        of, lf = window_forward(qf, kf, vf, *args, check=True)
+        assert torch.equal(of, o) and torch.equal(lf, lse), f.__name__
+        gf = window_backward(qf, kf, vf, f(o), lse, df, *args, check=True)
+        for name, a, b in zip(("dq", "dk", "dv"), gf, grads):
+            assert torch.equal(a, b), (f.__name__, name)
+    # outputs of the caller's layout
+    of = last(torch.zeros_like(q))
+    window_forward(q, k, v, *args, o=of, check=True)
+    assert torch.equal(of, o) and of.stride() == last(q).stride()
+    # one key head and one batch entry broadcast over the others: gradients sum over the copies
+    ke = k[:1, :1].clone().requires_grad_()
+    out = sliding_window_attention(q, ke.expand_as(k), ke.expand_as(v), *args)
+    (g,) = torch.autograd.grad(out, ke, do)
+    kk = ke.detach().expand_as(k).contiguous()
+    o2, l2 = window_forward(q, kk, kk, *args)
+    _, dk2, dv2 = window_backward(q, kk, kk, o2, l2, do, *args)
+    want = (dk2.float().sum((0, 1)) + dv2.float().sum((0, 1)))
+    # autograd adds eight copies twice over and k's and v's parts, in bf16
+    assert (g[0, 0].float() - want).abs().max() <= 12 * 2.0 ** -8 * (dk2.float().abs().sum((0, 1)) + dv2.float().abs().sum((0, 1))).max()
+
+
+@pytest.mark.gpu
+def test_autograd_matches_the_calls_and_is_deterministic():
+    q, k, v, do = (t.cuda() for t in make(6, 2, 500, 500, 128, BF16, batch=2, seed=4))
+    o, lse = window_forward(q, k, v, 128, 4)
+    want = window_backward(q, k, v, o, lse, do, 128, 4)
+    for _ in range(2):
+        leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+        out = sliding_window_attention(*leaves, 128, 4)
+        assert torch.equal(out, o)
+        for a, b in zip(torch.autograd.grad(out, leaves, do), want):
+            assert torch.equal(a, b)
+    with torch.no_grad():
+        assert torch.equal(sliding_window_attention(*leaves, 128, 4), o)
+
+
+@pytest.mark.gpu
+def test_graph_streams_and_concurrent_calls():
+    """A training step captures into a graph and replays with the same bits on
+    new data; calls on two streams at once do not disturb each other; a call
+    on a given stream allocates there."""
+    sets = [[t.cuda() for t in make(4, 2, 300, 300, 64, FP16, seed=s)] for s in (1, 50)]
+    args = (90, 4)
+    ref = []
+    for q, k, v, do in sets:
+        o, lse = window_forward(q, k, v, *args, check=True)
+        ref.append((o, lse, *window_backward(q, k, v, o, lse, do, *args, check=True)))
+    static = [t.clone() for t in sets[0]]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = window_forward(*static[:3], *args)
+        got = (o, lse, *window_backward(*static[:3], o, lse, static[3], *args))
+    for s in (1, 0, 1):
+        for a, b in zip(static, sets[s]):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, ref[s]):
+            assert torch.equal(a, b)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            q, k, v, do = sets[i]
+            o, lse = window_forward(q, k, v, *args, stream=st if i else st.cuda_stream)
+            outs[i].append((o, lse, *window_backward(q, k, v, o, lse, do, *args, stream=st)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in outs[i]:
+            for a, b in zip(r, ref[i]):
+                assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_capture_of_leaves_with_a_live_eager_graph_is_refused():
+    leaves = [t.cuda().requires_grad_() for t in make(2, 2, 64, 64, 64, BF16)[:3]]
+    alive = sliding_window_attention(*leaves, 16, 2)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        graph.capture_begin()
+        with pytest.raises(RuntimeError, match="still alive"):
+            sliding_window_attention(*leaves, 16, 2)
+        graph.capture_end()
+    del alive
+    grads = [torch.zeros_like(t) for t in leaves]
+    torch.cuda.synchronize()
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        out = sliding_window_attention(*leaves, 16, 2)
+        for g, x in zip(grads, torch.autograd.grad(out, leaves, torch.ones_like(out))):
+            g.copy_(x)
+
+
+# ------------------------------------------------------------------ refusals (no GPU)
+def problem(**kw):
+    base = dict(batch=1, heads=4, kv_heads=2, head_dim=64, q_len=10, kv_len=20, q_rows=0, kv_rows=0, window=4, sinks=1,
+                type=0, scale=0.0)
+    base.update(kw)
+    return _WindowProblem(*[base[n] for n, _ in _WindowProblem._fields_])
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=0), 2), (dict(heads=3), 2), (dict(q_len=-1), 2), (dict(kv_len=1 << 30), 2),
+    (dict(batch=60000, heads=4, q_len=10000), 2), (dict(head_dim=96), 3), (dict(type=2), 3), (dict(window=-1), 1),
+    (dict(sinks=-2), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(q_rows=1 << 30), 2),
+])
+def test_bad_problems_are_refused(kw, status):
+    n = ctypes.c_size_t()
+    assert sta.lib().sta_window_workspace_size(ctypes.byref(problem(**kw)), ctypes.byref(n), None) == status
+
+
+def test_bad_calls_are_refused_before_anything_is_enqueued():
+    L, p = sta.lib(), problem()
+    n = ctypes.c_size_t()
+    assert L.sta_window_workspace_size(ctypes.byref(p), None, ctypes.byref(n)) == 0 and n.value > 0
+    row = lambda ptr=4096, b=2560, h=640, r=64: sta._Rows(ptr, b, h, r)  # noqa: E731
+
+    def fwd(q=row(), k=row(), v=row(), o=row(), lse=None, cu=(None, None), ws=4096, size=1 << 20, flags=0):
+        return L.sta_window_forward(ctypes.byref(p), q, k, v, o, lse, *cu, ws, size, None, flags)
+
+    assert fwd(q=None) == 1 and fwd(o=row(ptr=0)) == 1 and fwd(flags=2) == 1 and fwd(cu=(4096, None)) == 1
+    assert fwd(k=row(ptr=4104)) == 4 and fwd(v=row(r=65)) == 4 and fwd(q=row(h=0)) == 1 and fwd(q=row(r=-64)) == 1
+    assert fwd(ws=None) == 5 and fwd(size=16) == 5 and fwd(ws=4100) == 4
+
+    def bwd(lse=4096, dk=row(), size=1 << 20):
+        return L.sta_window_backward(ctypes.byref(p), row(), row(), row(), row(), lse, row(), row(), dk, row(), None, None,
+                                     4096, size, None, 0)
+
+    assert bwd(lse=None) == 1 and bwd(dk=None) == 1 and bwd(dk=row(ptr=8)) == 4 and bwd(size=n.value - 1) == 5
+
+
+def test_binding_refusals():
+    q = torch.zeros(1, 2, 8, 64, dtype=BF16)
+    with pytest.raises(ValueError, match="CUDA"):
+        window_forward(q, q, q, 4)
+    with pytest.raises(TypeError):
+        window_forward([1.0], q, q, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        sliding_window_attention(q.requires_grad_(), q, q, 4)
+
+
+@pytest.mark.gpu
+def test_binding_refusals_on_device():
+    q = torch.zeros(2, 4, 8, 64, dtype=BF16, device="cuda")
+    cu = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    for bad in (dict(k=q.half()), dict(k=q[:1]), dict(v=q[..., :32]), dict(v=q.cpu()), dict(q=q[0]), dict(q=q.float()),
+                dict(cu_q=cu), dict(cu_q=cu, cu_kv=cu), dict(o=q.half()), dict(o=q[:, :, :4]),
+                dict(o=torch.zeros(2, 4, 8, 65, dtype=BF16, device="cuda")[..., 1:]), dict(lse=q.float()),
+                dict(workspace=torch.zeros(8)), dict(lse=torch.zeros(2, 4, 8, device="cuda").double())):
+        kw = dict(q=q, k=q, v=q, window=4)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            window_forward(**kw)
+    one = q[:1]
+    for bad in (cu.long(), cu.cpu()):
+        with pytest.raises(ValueError):
+            window_forward(one, one, one, 4, cu_q=bad, cu_kv=bad)
+    for kw, status in ((dict(window=-1), 1), (dict(sinks=-1), 1), (dict(scale=float("inf")), 1)):
+        with pytest.raises(sta.StaError) as e:
+            window_forward(q, q, q, **{**dict(window=4), **kw})
+        assert e.value.status == status
+    with pytest.raises(sta.StaError) as e:
+        window_forward(q, q[:, :3], q[:, :3], 4)
+    assert e.value.status == 2
+    # empty tensors
+    for shape in ((0, 4, 8, 64), (2, 4, 0, 64)):
+        e = torch.zeros(shape, dtype=BF16, device="cuda")
+        k = torch.zeros(shape[0], 4, 8, 64, dtype=BF16, device="cuda")
+        o, lse = window_forward(e, k, k, 4)
+        assert o.shape == e.shape and lse.shape == e.shape[:3]
+        grads = window_backward(e, k, k, o, lse, e, 4)
+        assert [g.shape for g in grads] == [e.shape, k.shape, k.shape] and not any(g.any() for g in grads)
