@@ -1,5 +1,6 @@
 // seq_api.cpp -- host side of the token-sequence calls of include/sta.h:
 // argument checks, workspace sizes, parameter blocks and launches.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -71,6 +72,7 @@ sta::WinParams window_params(const sta_window_problem *p, const int32_t *cu_q, c
   w.scale = p->scale > 0.f ? p->scale : 1.f / std::sqrt((float)p->head_dim);
   w.scale_log2 = w.scale * 1.4426950408889634f;
   w.status = static_cast<int *>(ws);
+  w.wait_limit_ns = sta::wait_limit_ns();
   return w;
 }
 
@@ -92,6 +94,50 @@ sta_status check_tensors(const sta_window_problem *p, bool packed, const sta_row
   for (int i = 0; i < nkv; ++i)
     if (const sta_status st = check_rows(kv_side[i], batch, p->kv_heads, packed ? p->kv_rows : p->kv_len)) return st;
   return STA_OK;
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return reinterpret_cast<EncodeTiledFn>(ok ? ptr : nullptr);
+  }();
+  return fn;
+}
+
+// A tensor of rows viewed as (64, rows, heads, batch[, 2 panels of head dim
+// 128]); a box is 128 rows of one head, all panels.
+bool tile_map(CUtensorMap *m, const sta_rows *x, int32_t type, int d, long long rows, long long heads, long long batch) {
+  const EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  // strides of extents of one are not used, but must be valid
+  auto bytes = [](long long n, int64_t stride) { return (cuuint64_t)(n > 1 ? stride * 2 : 256); };
+  const cuuint64_t dims[5] = {64, (cuuint64_t)(rows > 0 ? rows : 1), (cuuint64_t)heads, (cuuint64_t)batch, 2};
+  const cuuint64_t strides[4] = {bytes(rows, x->row), bytes(heads, x->head), bytes(batch, x->batch), 128};
+  const cuuint32_t box[5] = {64, 128, 1, 1, 2}, estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, type == STA_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+             d == 128 ? 5 : 4, x->data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+bool q_map(CUtensorMap *m, const sta_rows *x, const sta_window_problem *p, bool packed) {
+  return tile_map(m, x, p->type, p->head_dim, packed ? p->q_rows : p->q_len, p->heads, packed ? 1 : p->batch);
+}
+bool kv_map(CUtensorMap *m, const sta_rows *x, const sta_window_problem *p, bool packed) {
+  return tile_map(m, x, p->type, p->head_dim, packed ? p->kv_rows : p->kv_len, p->kv_heads, packed ? 1 : p->batch);
+}
+
+bool multiprocessors(int *n) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess &&
+         cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
 }
 
 sta_status check_workspace(const void *ws, size_t have, size_t need) {
@@ -172,7 +218,13 @@ sta_status sta_window_forward(const sta_window_problem *p, const sta_rows *q, co
   sta::WinParams w = window_params(p, cu_q, cu_kv, ws);
   w.q = rows_of(q), w.k = rows_of(k), w.v = rows_of(v), w.o = rows_of(o), w.lse = lse;
   if ((flags & STA_CALL_CHECK) && cudaMemsetAsync(ws, 0, sizeof(int), stream) != cudaSuccess) return STA_ERR_CUDA;
-  if (p->q_len > 0 && sta::launch_window_forward(w, p->type, stream) != cudaSuccess) return STA_ERR_CUDA;
+  if (p->q_len > 0) {
+    int sms = 0;
+    CUtensorMap maps[3];
+    if (!multiprocessors(&sms) || !q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
+        !kv_map(&maps[2], v, p, cu_q) || sta::launch_window_tiles(w, p->type, maps, sms, stream) != cudaSuccess)
+      return STA_ERR_CUDA;
+  }
   return finish(ws, stream, flags);
 }
 

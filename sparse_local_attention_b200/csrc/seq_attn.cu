@@ -54,23 +54,6 @@ __device__ __forceinline__ void finish(const float (&o)[D / 32], float m, float 
   if (lse && lane == 0) *lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : -INFINITY;
 }
 
-template <int D, class T>
-__global__ void __launch_bounds__(256) window_rows_kernel(const WinParams p) {
-  const int lane = threadIdx.x & 31, h = blockIdx.y, row = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const Sequence s = sequence(p, blockIdx.z);
-  if (row >= s.nq) return;
-  float q[D / 32], o[D / 32], m, l;
-  const char *qr = row_ptr(p.q, s.slice, h, s.q0 + row);
-  for (int e = 0; e < D / 32; ++e) q[e] = to_f<T>(qr, lane + 32 * e);
-  attend<D>(q, row + s.nk - s.nq, s.nk, p.window, p.sinks, p.scale_log2, o, m, l, [&](int key, auto &kf, auto &vf) {
-    const char *kr = row_ptr(p.k, s.slice, h / p.group, s.k0 + key), *vr = row_ptr(p.v, s.slice, h / p.group, s.k0 + key);
-    for (int e = 0; e < D / 32; ++e) kf[e] = to_f<T>(kr, lane + 32 * e), vf[e] = to_f<T>(vr, lane + 32 * e);
-    return true;
-  });
-  finish<D, T>(o, m, l, const_cast<char *>(row_ptr(p.o, s.slice, h, s.q0 + row)),
-               p.lse ? p.lse + stat_row(p, s, h, row) : nullptr, lane);
-}
-
 // dQ and D of one query row per warp.
 template <int D, class T>
 __global__ void __launch_bounds__(256) window_dq_rows_kernel(const WinParams p) {
@@ -169,11 +152,6 @@ __global__ void __launch_bounds__(256) cache_rows_kernel(const CacheAttn a) {
 }
 
 template <int D, class T>
-cudaError_t forward_d(const WinParams &p, cudaStream_t stream) {
-  window_rows_kernel<D, T><<<dim3((p.q_len + 7) / 8, p.heads, p.batch), 256, 0, stream>>>(p);
-  return cudaGetLastError();
-}
-template <int D, class T>
 cudaError_t backward_d(const WinParams &p, cudaStream_t stream) {
   window_dq_rows_kernel<D, T><<<dim3((p.q_len + 7) / 8, p.heads, p.batch), 256, 0, stream>>>(p);
   window_dkdv_rows_kernel<D, T><<<dim3((p.kv_len + 7) / 8, p.kv_heads, p.batch), 256, 0, stream>>>(p);
@@ -189,11 +167,6 @@ cudaError_t cache_d(const CacheAttn &a, int io_type, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_window_forward(const WinParams &p, int type, cudaStream_t stream) {
-  if (p.d == 128)
-    return type == STA_TYPE_BF16 ? forward_d<128, __nv_bfloat16>(p, stream) : forward_d<128, __half>(p, stream);
-  return type == STA_TYPE_BF16 ? forward_d<64, __nv_bfloat16>(p, stream) : forward_d<64, __half>(p, stream);
-}
 cudaError_t launch_window_backward(const WinParams &p, int type, cudaStream_t stream) {
   if (p.d == 128)
     return type == STA_TYPE_BF16 ? backward_d<128, __nv_bfloat16>(p, stream) : backward_d<128, __half>(p, stream);

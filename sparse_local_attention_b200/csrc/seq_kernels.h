@@ -2,6 +2,7 @@
 // operators, shared by their host API (seq_api.cpp) and the CUDA kernels.
 // Internal to libsta.so.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -11,6 +12,8 @@ namespace sta {
 
 // A window that hides nothing: every position minus it is far below zero.
 constexpr int kNoWindow = 1 << 30;
+
+uint64_t wait_limit_ns();  // sta_set_wait_limit_ns's value
 
 // Strides of a tensor of rows, in elements.
 struct Rows {
@@ -64,7 +67,8 @@ struct CacheAttn {
 };
 cudaError_t launch_cache_attention(const CacheAttn &a, int cache_type, int io_type, cudaStream_t stream);
 
-cudaError_t launch_window_forward(const WinParams &p, int type, cudaStream_t stream);
+// Forward on 128-row tiles; maps: q, k, v.
+cudaError_t launch_window_tiles(const WinParams &p, int type, const CUtensorMap *maps, int num_sms, cudaStream_t stream);
 cudaError_t launch_window_backward(const WinParams &p, int type, cudaStream_t stream);
 
 }  // namespace sta

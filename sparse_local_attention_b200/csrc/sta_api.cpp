@@ -296,6 +296,8 @@ sta_status enqueue_forward(const sta_plan_s *pl, const ForwardMaps &maps, const 
 
 namespace sta {
 
+uint64_t wait_limit_ns() { return g_wait_limit_ns; }
+
 // Every check of sta_backward except those of the workspace, in the order
 // sta_backward applies them; the last is the device check.
 sta_status check_backward_call(const sta_plan_s *pl, const void *const tensors[9], uint32_t flags) {

@@ -1,0 +1,472 @@
+// win_fwd.cu -- forward of causal sliding-window attention with sinks on
+// 128-row tiles (sm_100a tensor cores).
+//
+// For each query row i at position pos_i: O_i = sum_j P_ij V_j, P_ij =
+// exp(s_ij - LSE_i) over the visible keys j (j <= pos_i, and j > pos_i -
+// window or j < sinks), by one pass over the keys with the running maximum and
+// sum of the softmax in fp32.
+//
+//   * A unit is a 128-row query block of one head.  The units of a key head
+//     are numbered block by block, the heads of the group within a block, and
+//     a work item is two consecutive units (A, B): every key chunk in shared
+//     memory serves 256 query rows, with any number of heads per key head.
+//     Persistent grid, one CTA per SM, the blocks with the most keys first.
+//   * An item's keys are its sinks, then its window [lo, hi], each in chunks
+//     of 128 from its own first key on (TMA rows need no alignment), so no
+//     chunk holds keys below every row's window, and a chunk that one of the
+//     units does not see is skipped for it.  Chunks that every row of a unit
+//     sees whole take no mask; others apply a 128-bit mask per row.
+//   * Keys of a chunk past its valid ones (another sequence's, or the future)
+//     must not meet P = 0 as NaN: the product P V runs over the valid keys
+//     rounded up to 16, and the "clear" warp zeroes the V rows in between.
+//   * Warps: 0-3 / 4-7 softmax of A / B (thread = row = TMEM lane), 8 TMA
+//     producer, 9 MMA issuer, 10 clear.  S_X = Q_X K^T and O_X += P_X V with P
+//     over the first 64 columns of S (tensor memory: S_A, S_B, O_A, O_B); the
+//     part of P V whose P is written first is issued before the rest is
+//     formed; O is rescaled only when a row's maximum grows by more than 2^8.
+// P is rounded to the tensors' type, the precision of the tensor core's A
+// operand; statistics and O are fp32 until the final rounding.
+#include "seq_tile.cuh"
+
+namespace sta {
+namespace {
+
+constexpr int kBM = kTileRows;
+constexpr int kThreads = 352;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kClearWarp = 10;
+
+template <int D>
+struct Cfg {
+  static constexpr uint32_t kTile = kBM * D * 2;
+  static constexpr int kSlots = D == 128 ? 4 : 8;  // ring of K and V chunks
+  static constexpr uint32_t kTmO = 256;            // O_X at kTmO + X * D; S_X at 128 * X
+  static constexpr uint32_t kTmCols = 512;
+  static constexpr int kLead = D == 128 ? 96 : 64;  // keys of the first part of P V
+  // full[S] empty[S] raw[S] q_full q_free s_full[2] p_ready[2] pv_done[2] o_free[2] drain p_lead[2]
+  static constexpr int kNumBars = 3 * kSlots + 13;
+  static constexpr uint32_t kSmem = (2 + kSlots) * kTile + kNumBars * 8 + 64 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+struct Item {
+  Sequence s;
+  int hk;
+  int h[2], qb[2];   // query head and query block of A and B
+  bool has[2];
+  int pos0[2], lo[2], hi[2];  // position of row 0; first window key; last key (below 0: none)
+  int base, last, nsink;      // window keys [base, last], sink keys [0, nsink)
+  int ns, nc;                 // sink chunks, chunks
+  __device__ __forceinline__ void chunk(int j, int &first, int &valid) const {
+    first = j < ns ? j * kBM : base + (j - ns) * kBM;
+    valid = min(kBM, (j < ns ? nsink : last + 1) - first);
+  }
+};
+
+// a[x] without indexing a register array by a run-time x
+template <class V>
+__device__ __forceinline__ V pick(const V (&a)[2], int x) { return x ? a[1] : a[0]; }
+
+// Whether unit x sees a key of a chunk (hi is below 0 for a unit that is not there).
+__device__ __forceinline__ bool sees(const Item &it, int x, int first, int valid, int sinks) {
+  return first <= pick(it.hi, x) && (first + valid > pick(it.lo, x) || first < sinks);
+}
+
+__device__ __forceinline__ Item decode(const WinParams &p, int item) {
+  Item it;
+  const int slices = p.batch * p.kv_heads, nqb = (p.q_len + kBM - 1) / kBM;
+  const int pairs = (nqb * p.group + 1) / 2;
+  const int pair = pairs - 1 - item / slices, slice = item % slices;  // the last blocks have the most keys
+  const int b = slice / p.kv_heads;
+  it.hk = slice % p.kv_heads;
+  it.s = sequence(p, b);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int unit = 2 * pair + x;
+    it.qb[x] = unit / p.group;
+    it.h[x] = it.hk * p.group + unit % p.group;
+    const int rows = min(kBM, it.s.nq - it.qb[x] * kBM);
+    it.has[x] = it.qb[x] < nqb && rows > 0;
+    it.pos0[x] = it.qb[x] * kBM + it.s.nk - it.s.nq;
+    it.lo[x] = max(0, it.pos0[x] - p.window + 1);
+    it.hi[x] = it.has[x] ? min(it.s.nk - 1, it.pos0[x] + rows - 1) : -1;
+  }
+  it.last = max(it.hi[0], it.hi[1]);
+  it.base = p.sinks >= it.lo[0] ? 0 : it.lo[0];
+  it.nsink = min(p.sinks, it.base);
+  it.ns = (it.nsink + kBM - 1) / kBM;
+  it.nc = it.has[0] && it.last >= 0 ? it.ns + (it.last - it.base + kBM) / kBM : 0;
+  return it;
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                      const __grid_constant__ CUtensorMap tmap_v, const WinParams p, const int n_items) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *q_smem = smem, *slots = smem + 2 * C::kTile;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(slots + C::kSlots * C::kTile);
+  uint64_t *full = bars, *empty = bars + C::kSlots;
+  uint64_t *raw = bars + 2 * C::kSlots;  // a V chunk landed whose last rows are still to be cleared
+  uint64_t *q_full = bars + 3 * C::kSlots, *q_free = q_full + 1;
+  uint64_t *s_full = q_free + 1, *p_ready = s_full + 2, *pv_done = p_ready + 2, *o_free = pv_done + 2;
+  uint64_t *drain = o_free + 2, *p_lead = drain + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3 * C::kSlots; ++i) mbar_init(&bars[i], 1);
+    mbar_init(q_full, 1);
+    mbar_init(q_free, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_ready[x], 4);
+      mbar_init(&p_lead[x], 4);
+      mbar_init(&pv_done[x], 1);
+      mbar_init(&o_free[x], 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, C::kTmCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns};
+
+  if (warp == kProducerWarp) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmap_q);
+      tma_prefetch_desc(&tmap_k);
+      tma_prefetch_desc(&tmap_v);
+      uint32_t ld = 0, items = 0, raw_par = 0, raw_last = 0;  // per slot: parity of raw, last load went to raw
+      bool ok = true;
+      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+        const Item it = decode(p, item);
+        if (it.nc == 0) continue;
+        if (!mbar_wait(q_free, (items & 1) ^ 1, ctl, kErrWaitProducer)) { ok = false; break; }
+        mbar_arrive_expect_tx(q_full, (it.has[1] ? 2 : 1) * C::kTile);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (it.has[x]) load_tile<D>(q_smem + x * C::kTile, &tmap_q, it.s.q0 + it.qb[x] * kBM, it.h[x], it.s.slice, q_full);
+        ++items;
+        for (int s = 0; s < 2 * it.nc; ++s) {  // K0 V0 K1 V1 ...
+          int first, valid;
+          it.chunk(s >> 1, first, valid);
+          const uint32_t slot = ld % C::kSlots, phase = (ld / C::kSlots) & 1, bit = 1u << slot;
+          if (!mbar_wait(&empty[slot], phase ^ 1, ctl, kErrWaitProducer)) { ok = false; break; }
+          const bool clear = (s & 1) && valid % 16 != 0;
+          uint64_t *bar = clear ? &raw[slot] : &full[slot];
+          raw_last = clear ? raw_last | bit : raw_last & ~bit;
+          if (clear) raw_par ^= bit;
+          mbar_arrive_expect_tx(bar, C::kTile);
+          load_tile<D>(slots + slot * C::kTile, (s & 1) ? &tmap_v : &tmap_k, it.s.k0 + first, it.hk, it.s.slice, bar);
+          ++ld;
+        }
+      }
+      if (!ok) {
+        // let the copies already issued land before the CTA exits
+        const uint32_t start = ld > (uint32_t)C::kSlots ? ld - C::kSlots : 0;
+        for (uint32_t i = start; i < ld; ++i) {
+          const uint32_t slot = i % C::kSlots;
+          if (raw_last >> slot & 1) drain_wait(&raw[slot], (raw_par >> slot & 1) ^ 1);
+          else drain_wait(&full[slot], (i / C::kSlots) & 1);
+        }
+        if (items > 0) drain_wait(q_full, (items - 1) & 1);
+      }
+    }
+  } else if (warp == kClearWarp) {
+    uint32_t ld = 0, raw_par = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      const Item it = decode(p, item);
+      for (int j = 0; j < it.nc && ok; ++j) {
+        int first, valid;
+        it.chunk(j, first, valid);
+        if (valid % 16 == 0) continue;
+        const uint32_t slot = (ld + 2 * j + 1) % C::kSlots;
+        ok = mbar_wait_w(&raw[slot], raw_par >> slot & 1, ctl, kErrWaitProducer);
+        raw_par ^= 1u << slot;
+        if (!ok) break;
+        clear_rows<D>(slots + slot * C::kTile, valid, (valid + 15) & ~15, lane);
+        if (lane == 0) mbar_arrive(&full[slot]);
+      }
+      ld += 2 * it.nc;
+    }
+  } else if (warp == kMmaWarp) {
+    constexpr uint32_t idesc_qk = idesc_for<T>(kBM, kBM, false, false);
+    constexpr uint32_t idesc_pv = idesc_for<T>(kBM, D, false, true);
+    const uint32_t slots_addr = smem_u32(slots);
+    const uint64_t qdesc0 = smem_desc_sw128(smem_u32(q_smem), 16, 1024);
+    const uint64_t kdesc0 = smem_desc_sw128(slots_addr, 16, 1024);
+    const uint64_t vdesc0 = smem_desc_sw128(slots_addr, kTilePanel, 1024);
+    uint32_t ld = 0, items = 0;
+    uint32_t p_waits[2] = {0, 0}, o_waits[2] = {0, 0}, used[2] = {0, 0};
+    bool ok = true, issued = false;
+    auto mma_s = [&](int x, uint32_t slot) {
+      const uint64_t qd = qdesc0 + ((x * C::kTile) >> 4), kd = kdesc0 + ((slot * C::kTile) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
+        mma_ss_w(tmem + 128 * x, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+      }
+      mma_commit_w(&s_full[x]);
+    };
+    // O_X += P_X V over the first `steps` groups of 16 keys: the part whose P
+    // is written first as soon as it is there, then the rest
+    auto mma_pv = [&](int x, uint32_t slot, bool first, uint32_t ph, int steps) -> bool {
+      const uint64_t vd = vdesc0 + ((slot * C::kTile) >> 4);
+      const uint32_t o_tm = tmem + C::kTmO + x * D, p_tm = tmem + 128 * x;
+#pragma unroll
+      for (int kk = 0; kk < C::kLead / 16; ++kk)
+        if (kk < steps) mma_ts_w(o_tm, p_tm + kk * 8, vd + ((kk * 16 * 128) >> 4), idesc_pv, (first && kk == 0) ? 0u : 1u);
+      if (!mbar_wait_w(&p_ready[x], ph, ctl, kErrWaitMma)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = C::kLead / 16; kk < kBM / 16; ++kk)
+        if (kk < steps) mma_ts_w(o_tm, p_tm + kk * 8, vd + ((kk * 16 * 128) >> 4), idesc_pv, 1u);
+      mma_commit_w(&pv_done[x]);
+      return true;
+    };
+    auto wait_slot = [&](uint32_t l) -> bool {
+      if (!mbar_wait_w(&full[l % C::kSlots], (l / C::kSlots) & 1, ctl, kErrWaitMma)) return false;
+      tc_fence_after();
+      return true;
+    };
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      const Item it = decode(p, item);
+      if (it.nc == 0) continue;
+      if (!mbar_wait_w(q_full, items & 1, ctl, kErrWaitMma)) { ok = false; break; }
+      tc_fence_after();
+      ++items;
+      const uint32_t k0 = ld;
+      if (!wait_slot(k0)) { ok = false; break; }
+      int first, valid;
+      it.chunk(0, first, valid);
+      bool act[2] = {sees(it, 0, first, valid, p.sinks), sees(it, 1, first, valid, p.sinks)};
+      bool begun[2] = {false, false};
+      issued = true;
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (act[x]) mma_s(x, k0 % C::kSlots);
+      mma_commit_w(&empty[k0 % C::kSlots]);
+      if (it.nc == 1) mma_commit_w(q_free);
+      for (int j = 0; j < it.nc && ok; ++j) {
+        const uint32_t vj = k0 + 2 * j + 1, kn = vj + 1;
+        const bool more = j + 1 < it.nc;
+        if (!wait_slot(vj) || (more && !wait_slot(kn))) { ok = false; break; }
+        const int steps = (valid + 15) / 16;
+        if (more) it.chunk(j + 1, first, valid);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (act[x]) {
+            const uint32_t ph = p_waits[x] & 1;
+            ++p_waits[x];
+            if (!mbar_wait_w(&p_lead[x], ph, ctl, kErrWaitMma)) { ok = false; break; }
+            tc_fence_after();
+            if (!begun[x] && used[x] > 0) {
+              // the epilogue of this half's previous item has read O_X
+              if (!mbar_wait_w(&o_free[x], o_waits[x] & 1, ctl, kErrWaitMma)) { ok = false; break; }
+              ++o_waits[x];
+              tc_fence_after();
+            }
+            if (!mma_pv(x, vj % C::kSlots, !begun[x], ph, steps)) { ok = false; break; }
+            begun[x] = true;
+          }
+          act[x] = more && sees(it, x, first, valid, p.sinks);
+          if (act[x]) mma_s(x, kn % C::kSlots);
+        }
+        if (!ok) break;
+        mma_commit_w(&empty[vj % C::kSlots]);
+        if (more) mma_commit_w(&empty[kn % C::kSlots]);
+        if (j + 2 == it.nc) mma_commit_w(q_free);
+      }
+      ld = k0 + 2 * it.nc;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) used[x] += begun[x] ? 1 : 0;
+    }
+    if (!ok && issued) {
+      mma_commit_w(drain);
+      drain_wait(drain, 0);
+    }
+  } else {
+    // softmax warpgroup x: row `row` of unit x
+    const int x = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lane_off + 128 * x, o_tm = tmem + lane_off + C::kTmO + x * D;
+    const float sl2 = p.scale_log2;
+    uint32_t s_waits = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      const Item it = decode(p, item);
+      if (!pick(it.has, x)) continue;
+      const int pos0 = pick(it.pos0, x), qrow = pick(it.qb, x) * kBM + row;
+      const bool row_valid = qrow < it.s.nq;
+      float m = -INFINITY, l = 0.f;
+      int seen = 0;
+      for (int j = 0; j < it.nc; ++j) {
+        int first, valid;
+        it.chunk(j, first, valid);
+        if (!sees(it, x, first, valid, p.sinks)) continue;
+        if (!mbar_wait_w(&s_full[x], s_waits & 1, ctl, kErrWaitSoftmax)) { ok = false; break; }
+        ++s_waits;
+        tc_fence_after();
+        // O_X holds every chunk before this one: S was issued after their P V
+        float s[kBM];
+        {
+          uint32_t r0[32], r1[32], r2[32], r3[32];
+          tmem_ld32(s_tm, r0);
+          tmem_ld32(s_tm + 32, r1);
+          tmem_ld32(s_tm + 64, r2);
+          tmem_ld32(s_tm + 96, r3);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            s[i] = __uint_as_float(r0[i]);
+            s[32 + i] = __uint_as_float(r1[i]);
+            s[64 + i] = __uint_as_float(r2[i]);
+            s[96 + i] = __uint_as_float(r3[i]);
+          }
+        }
+        // whole: every row of the unit sees all 128 keys
+        const bool whole = valid == kBM && first + kBM - 1 <= pos0 &&
+                           (first > pos0 + kBM - 1 - p.window || first + kBM <= p.sinks);
+        if (!whole) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t bits = visible_bits(pos0 + row, first, valid, p.window, p.sinks, w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(bits & (1u << i))) s[32 * w + i] = -INFINITY;
+          }
+        }
+        float t16[16];
+#pragma unroll
+        for (int a = 0; a < 16; ++a)
+          t16[a] = max3(max3(s[8 * a], s[8 * a + 1], s[8 * a + 2]), max3(s[8 * a + 3], s[8 * a + 4], s[8 * a + 5]),
+                        fmaxf(s[8 * a + 6], s[8 * a + 7]));
+        float t4[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) t4[a] = fmaxf(fmaxf(t16[4 * a], t16[4 * a + 1]), fmaxf(t16[4 * a + 2], t16[4 * a + 3]));
+        const float mloc = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sl2;
+        const bool resc = mloc > m + 8.0f;  // also the first finite maximum
+        const float m_new = resc ? mloc : m;
+        const float alpha = resc ? ex2_approx(m - m_new) : 1.f;
+        const bool warp_resc = __any_sync(0xffffffffu, resc) && seen > 0;
+        m = m_new;
+        const float ms = m == -INFINITY ? 0.f : m;  // a row without a visible key so far: P = 0
+        float ls[8];
+#pragma unroll
+        for (int a = 0; a < 8; ++a) ls[a] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kBM / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float p0 = ex2_approx(fmaf(s[32 * c + i], sl2, -ms));
+            const float p1 = ex2_approx(fmaf(s[32 * c + i + 1], sl2, -ms));
+            ls[(i / 2) & 7] += p0 + p1;
+            pk[i / 2] = Elem<T>::pack(p0, p1);
+          }
+          tmem_st16(s_tm + c * 16, pk);
+          if (c == 1 && warp_resc) {
+#pragma unroll 1
+            for (int oc = 0; oc < D / 16; ++oc) {
+              uint32_t r[16];
+              tmem_ld16(o_tm + oc * 16, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+              tmem_st16(o_tm + oc * 16, r);
+            }
+          }
+          if (c == C::kLead / 32 - 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            warp_arrive(&p_lead[x], lane);
+          }
+        }
+        l = l * alpha + (((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7])));
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&p_ready[x], lane);
+        ++seen;
+      }
+      if (!ok) break;
+      if (seen > 0) {
+        // one P V per chunk so far: the last one's phase
+        if (!mbar_wait_w(&pv_done[x], (s_waits - 1) & 1, ctl, kErrWaitEpilogue)) { ok = false; break; }
+        tc_fence_after();
+      }
+      const bool none = l == 0.f;
+      const float inv_l = none ? 0.f : 1.f / l;
+      uint4 *dst = reinterpret_cast<uint4 *>(p.o.p + 2 * ((long long)it.s.slice * p.o.b + (long long)pick(it.h, x) * p.o.h +
+                                                         (long long)(it.s.q0 + qrow) * p.o.r));
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        if (seen > 0) {
+          tmem_ld32(o_tm + c * 32, r);
+          tmem_ld_wait();
+        }
+        if (row_valid) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = none ? 0u
+                          : Elem<T>::pack(__uint_as_float(r[8 * v + 2 * e]) * inv_l,
+                                          __uint_as_float(r[8 * v + 2 * e + 1]) * inv_l);
+            dst[c * 4 + v] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (seen > 0) {
+        tc_fence_before();
+        warp_arrive(&o_free[x], lane);
+      }
+      if (row_valid && p.lse)
+        p.lse[stat_row(p, it.s, pick(it.h, x), qrow)] = none ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmCols);
+  }
+}
+
+template <int D, class T>
+cudaError_t launch(const WinParams &p, const CUtensorMap *maps, int num_sms, cudaStream_t stream) {
+  using C = Cfg<D>;
+  const cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  const long long nqb = (p.q_len + kBM - 1) / kBM;
+  const long long items = (nqb * p.group + 1) / 2 * p.batch * p.kv_heads;
+  const int grid = (int)(items < num_sms ? items : num_sms);
+  window_fwd_kernel<D, T><<<grid, kThreads, C::kSmem, stream>>>(maps[0], maps[1], maps[2], p, (int)items);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_tiles(const WinParams &p, int type, const CUtensorMap *maps, int num_sms, cudaStream_t stream) {
+  if (p.d == 128)
+    return type == STA_TYPE_BF16 ? launch<128, __nv_bfloat16>(p, maps, num_sms, stream)
+                                 : launch<128, __half>(p, maps, num_sms, stream);
+  return type == STA_TYPE_BF16 ? launch<64, __nv_bfloat16>(p, maps, num_sms, stream)
+                               : launch<64, __half>(p, maps, num_sms, stream);
+}
+
+}  // namespace sta
