@@ -10,7 +10,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsta.so")
 SOURCES = ["sta_api.cpp", "sta_permute.cu", "sta_fwd.cu", "sta_bwd.cu", "sta_noalloc.cu",
-           "seq_api.cpp", "seq_attn.cu", "win_fwd.cu", "cache.cu"]
+           "seq_api.cpp", "seq_attn.cu", "win_fwd.cu", "win_bwd.cu",
+           "cache.cu"]
 HEADERS = ["sm100_ptx.cuh", "sta_kernels.h", "sta_common.cuh", "seq_kernels.h", "seq_common.cuh",
            "seq_tile.cuh"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17", "-lineinfo",

@@ -60,7 +60,48 @@ size_t stat_rows(const sta_window_problem *p) {
 }
 
 size_t window_fwd_bytes(const sta_window_problem *) { return kStatusBytes; }
-size_t window_bwd_bytes(const sta_window_problem *p) { return kStatusBytes + round256(stat_rows(p) * 4); }
+
+// How the backward's key blocks are cut into parts, and its workspace.  A part
+// is at least 8 chunks of 128 queries (its 128 KB of sums are written and read
+// once, about the time of two chunks) and otherwise 1 / (2 SMs) of the work, so
+// that no block is one CTA's work for longer than the rest together.
+struct BackwardLayout {
+  int seg_chunks, sink_blocks, sink_segs, norm_segs, aug_rows, n_norms;
+  size_t dd, aug, norms, parts, bytes;
+};
+
+BackwardLayout backward_layout(const sta_window_problem *p) {
+  constexpr long long kTargets = 2 * 148;
+  BackwardLayout l{};
+  auto up = [](long long n, long long m) { return (n + m - 1) / m; };
+  const long long group = p->heads / p->kv_heads, slices = (long long)p->batch * p->kv_heads;
+  const long long nkb = up(p->kv_len, 128), nqb = up(p->q_len, 128);
+  const bool windowed = p->window > 0 && p->window < p->kv_len;
+  const long long all = up(p->q_len + 7ll, 128), seen = windowed ? up(p->window + 135ll, 128) : all;
+  const long long norm = (seen < all ? seen : all) * group;
+  l.sink_blocks = windowed && p->sinks > 0 ? (int)(up(p->sinks, 128) < nkb ? up(p->sinks, 128) : nkb) : 0;
+  const long long work = slices * (nkb * norm / (windowed ? 1 : 2) + (l.sink_blocks ? l.sink_blocks * all * group : 0));
+  const long long per = up(work, kTargets) > 8 ? up(work, kTargets) : 8;
+  l.seg_chunks = (int)(per < 0x7fffffff ? per : 0x7fffffff);
+  l.norm_segs = (int)(norm > per ? up(norm, per) : 1);
+  l.sink_segs = (int)(l.sink_blocks && all * group > per ? up(all * group, per) : 1);
+  const size_t rows = (size_t)p->heads * p->batch * up(p->q_len, 8) * 8;
+  const size_t packed_row = p->q_rows ? (size_t)up(p->q_rows, 8) * 8 + 8 * (size_t)p->batch + 8 : 0;
+  const size_t aug_rows = rows > packed_row * p->heads ? rows : packed_row * p->heads;
+  l.aug_rows = (int)packed_row;  // the dense form's is set by the caller
+  l.n_norms = (int)(nqb * p->heads * p->batch);
+  size_t slots = 0;
+  if (l.norm_segs > 1) slots = (size_t)slices * (l.sink_blocks * l.sink_segs + (nkb - l.sink_blocks) * l.norm_segs);
+  else if (l.sink_segs > 1) slots = (size_t)slices * l.sink_blocks * l.sink_segs;
+  l.dd = kStatusBytes;
+  l.aug = l.dd + round256(stat_rows(p) * 4);
+  l.norms = l.aug + (aug_rows + 128) * 32;  // a chunk reads 128 rows from any multiple of 8 on
+  l.parts = l.norms + round256((size_t)l.n_norms * 4);
+  l.bytes = l.parts + slots * 2 * 128 * p->head_dim * 4;
+  return l;
+}
+
+size_t window_bwd_bytes(const sta_window_problem *p) { return backward_layout(p).bytes; }
 
 sta::WinParams window_params(const sta_window_problem *p, const int32_t *cu_q, const int32_t *cu_kv, void *ws) {
   sta::WinParams w{};
@@ -242,9 +283,19 @@ sta_status sta_window_backward(const sta_window_problem *p, const sta_rows *q, c
   w.q = rows_of(q), w.k = rows_of(k), w.v = rows_of(v), w.o = rows_of(o), w.dout = rows_of(dout);
   w.dq = rows_of(dq), w.dk = rows_of(dk), w.dv = rows_of(dv);
   w.lse = const_cast<float *>(lse);
-  w.dd = reinterpret_cast<float *>(static_cast<char *>(ws) + kStatusBytes);
+  const BackwardLayout l = backward_layout(p);
+  char *base = static_cast<char *>(ws);
+  w.dd = reinterpret_cast<float *>(base + l.dd);
+  w.aug = reinterpret_cast<uint8_t *>(base + l.aug), w.aug_rows = cu_q ? l.aug_rows : (p->q_len + 7) / 8 * 8;
+  w.norms = reinterpret_cast<float *>(base + l.norms), w.n_norms = l.n_norms;
+  w.parts = reinterpret_cast<float *>(base + l.parts);
+  w.seg_chunks = l.seg_chunks, w.sink_blocks = l.sink_blocks, w.sink_segs = l.sink_segs, w.norm_segs = l.norm_segs;
   if ((flags & STA_CALL_CHECK) && cudaMemsetAsync(ws, 0, sizeof(int), stream) != cudaSuccess) return STA_ERR_CUDA;
-  if ((p->q_len > 0 || p->kv_len > 0) && sta::launch_window_backward(w, p->type, stream) != cudaSuccess)
+  int sms = 0;
+  CUtensorMap maps[4];
+  if (!multiprocessors(&sms) || !q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
+      !kv_map(&maps[2], v, p, cu_q) || !q_map(&maps[3], dout, p, cu_q) ||
+      sta::launch_window_backward(w, p->type, maps, sms, stream) != cudaSuccess)
     return STA_ERR_CUDA;
   return finish(ws, stream, flags);
 }

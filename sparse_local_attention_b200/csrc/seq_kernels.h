@@ -31,7 +31,15 @@ struct WinParams {
   float scale, scale_log2;
   Rows q, k, v, o, dout, dq, dk, dv;
   float *lse;
-  float *dd;  // backward: D = rowsum(dO o O), laid out like lse
+  // backward
+  float *dd;       // D = rowsum(dO o O), laid out like lse
+  uint8_t *aug;    // operand panels of -LSE and -D: 256 bytes per 8 query rows
+  int aug_rows;    // panel rows per head
+  float *norms;    // largest row norm of dO per 128-row block (fp16)
+  int n_norms;
+  float *parts;    // fp32 sums of dK and dV of the parts of key blocks
+  int seg_chunks;  // chunks of 128 queries per part
+  int sink_blocks, sink_segs, norm_segs;  // key blocks that hold sinks; parts per block there and elsewhere, at most
   int *status;
   unsigned long long wait_limit_ns;
 };
@@ -69,6 +77,8 @@ cudaError_t launch_cache_attention(const CacheAttn &a, int cache_type, int io_ty
 
 // Forward on 128-row tiles; maps: q, k, v.
 cudaError_t launch_window_tiles(const WinParams &p, int type, const CUtensorMap *maps, int num_sms, cudaStream_t stream);
-cudaError_t launch_window_backward(const WinParams &p, int type, cudaStream_t stream);
+// Backward; maps: q, k, v, dO.
+cudaError_t launch_window_backward(const WinParams &p, int type, const CUtensorMap *maps, int num_sms,
+                                   cudaStream_t stream);
 
 }  // namespace sta

@@ -1,0 +1,998 @@
+// win_bwd.cu -- backward of causal sliding-window attention with sinks on
+// 128-row tiles (sm_100a tensor cores).
+//
+// With P = exp(S - LSE) over the visible pairs and D_i = sum_c dO_ic O_ic:
+//   dV = P^T dO,  dS = P o (dO V^T - D),  dK = scale dS^T Q,  dQ = scale dS K,
+// dK and dV summed over the query heads of a key head.  No atomics: every sum
+// has one order.
+//
+//   1. window_pre: D per row; per 8 query rows the operand panel that carries
+//      -LSE / scale and -D into the dK / dV kernel's products; for fp16 the
+//      largest row norm of dO per block.
+//   2. window_dkdv: an item is a 128-row key block of a key head (or a part of
+//      its queries): K and V stay in shared memory; the 128-row chunks of the
+//      queries that see the block, head after head of the group, stream
+//      through a ring.  S^T = K Q^T and dP^T = V dO^T land in tensor memory,
+//      the elementwise warps (thread = key row) turn them into P^T and dS^T,
+//      then dV += P^T dO and dK += dS^T Q accumulate in tensor memory.  Blocks
+//      that many queries see (sinks; long sequences of few heads) are cut into
+//      parts of at most seg_chunks chunks, whose fp32 sums window_join adds up
+//      in order: without it one sink block of a long sequence is one CTA's
+//      work for longer than all the others together.
+//   3. window_dq: an item is a 128-row query block of a head; its keys come as
+//      in the forward (sinks, then the window from its own first key on).
+//
+// Chunks that all rows see whole take no mask.  A contraction runs over the
+// valid rows of a chunk rounded up to 16, and the "clear" warp zeroes the rows
+// in between, so that another sequence's rows never meet a zero as NaN.
+//
+// P and dS are rounded to the tensors' type, the precision of the tensor
+// core's A operand.  fp16 has 5 exponent bits: P is held times 2^8 and dS times
+// a power of two near 4 / max_i |dO_i|, so that neither falls below its normal
+// range where it matters (|dS| <= 2 |dO_i| |V_j|: rows of V up to a norm of 8192
+// do not overflow).
+#include "seq_tile.cuh"
+
+namespace sta {
+namespace {
+
+constexpr int kBM = kTileRows;
+constexpr uint32_t kAugBytes = 4096;  // panel of 128 query rows
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Elementwise warps of NG warpgroups (warpgroup e: columns [e kBM / NG, (e + 1)
+// kBM / NG) of each chunk; thread = TMEM lane = row), then the TMA producer, the
+// MMA issuer and the clear warp.
+template <int NG>
+struct Roles {
+  static constexpr int kGroups = NG;
+  static constexpr int kMathWarps = 4 * NG;
+  static constexpr int kProducerWarp = kMathWarps, kMmaWarp = kMathWarps + 1, kClearWarp = kMathWarps + 2;
+  static constexpr int kThreads = 32 * (kMathWarps + 3);
+  static constexpr int kCols = kBM / NG;
+};
+
+template <class T> constexpr bool kIsHalf = std::is_same<T, __half>::value;
+template <class T> constexpr float kPShift = kIsHalf<T> ? 8.f : 0.f;  // log2 of P's factor
+
+// x as hi + lo of type T (lo: element 1).
+template <class T>
+__device__ __forceinline__ uint32_t hi_lo(float x) {
+  const uint32_t h = Elem<T>::pack(x, 0.f);
+  return Elem<T>::pack(x, x - Elem<T>::unpack(h).x);
+}
+
+// The panel row of one query: elements 0, 1 carry -LSE / scale (times 1 / kLseSel),
+// 2, 3 carry -D; fp16 also 4, 5 (large D) and 6, 7 (small D), against selectors
+// that undo the factors.
+template <class T> constexpr float kLseSel = kIsHalf<T> ? 16.f : 1.f;
+constexpr float kDSel = 16384.f;
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// Panel row of query `row` of head h: rows of a sequence are consecutive and
+// its first one a multiple of 8.
+__device__ __forceinline__ long long aug_row(const WinParams &p, const Sequence &s, int b, int h) {
+  if (p.cu_q) return (long long)h * p.aug_rows + (s.q0 & ~7) + 8 * b;
+  return ((long long)s.slice * p.heads + h) * p.aug_rows;
+}
+
+// The factor of dS (1 unless T is fp16), by a whole CTA.
+template <class T>
+__device__ __forceinline__ float ds_factor(const WinParams &p, float *smem_word) {
+  if constexpr (!kIsHalf<T>) return 1.f;
+  int *word = reinterpret_cast<int *>(smem_word);
+  if (threadIdx.x == 0) *word = 0;
+  __syncthreads();
+  float m = 0.f;
+  for (int i = threadIdx.x; i < p.n_norms; i += blockDim.x) m = fmaxf(m, p.norms[i]);
+  atomicMax(word, __float_as_int(m));  // nonnegative floats order like integers
+  __syncthreads();
+  const float top = __int_as_float(*word);
+  if (!(top > 0.f) || isinf(top)) return 1.f;
+  const int e = ((__float_as_int(top) >> 23) & 0xff) - 127;
+  return exp2f((float)max(-100, min(100, 2 - e)));
+}
+
+// ----------------------------------------------------------------------- 1. preprocess
+// A group of D / 8 lanes per row, a CTA per 128 rows of a head.
+template <int D, class T>
+__global__ void __launch_bounds__(256) window_pre_kernel(const WinParams p) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, part = lane % kLanes, h = blockIdx.y, b = blockIdx.z;
+  const Sequence s = sequence(p, b);
+  float norm = 0.f;
+  const long long aug0 = aug_row(p, s, b, h);
+#pragma unroll 2
+  for (int i = 0; i < kBM / (8 * kRows); ++i) {
+    const int row = blockIdx.x * kBM + (i * 8 + (threadIdx.x >> 5)) * kRows + sub;
+    const bool valid = row < s.nq;
+    float acc = 0.f, sq = 0.f, lse = 0.f;
+    long long at = 0;
+    if (valid) {
+      const long long r = s.q0 + row;
+      at = stat_row(p, s, h, row);
+      const uint4 a = reinterpret_cast<const uint4 *>(p.o.p + 2 * (s.slice * p.o.b + h * p.o.h + r * p.o.r))[part];
+      const uint4 g = reinterpret_cast<const uint4 *>(p.dout.p + 2 * (s.slice * p.dout.b + h * p.dout.h + r * p.dout.r))[part];
+      if (part == 0) lse = p.lse[at];
+      const uint32_t av[4] = {a.x, a.y, a.z, a.w}, gv[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 af = Elem<T>::unpack(av[e]), gf = Elem<T>::unpack(gv[e]);
+        acc = fmaf(af.x, gf.x, fmaf(af.y, gf.y, acc));
+        sq = fmaf(gf.x, gf.x, fmaf(gf.y, gf.y, sq));
+      }
+    }
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) {
+      acc += __shfl_xor_sync(0xffffffffu, acc, off);
+      if (kIsHalf<T>) sq += __shfl_xor_sync(0xffffffffu, sq, off);
+    }
+    norm = fmaxf(norm, sqrtf(sq));
+    if (valid && part == 0) p.dd[at] = acc;
+    if (valid && part < 2) {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (part == 0) {
+        // a row that sees nothing has LSE = -inf; all its pairs are masked
+        w[0] = hi_lo<T>(lse == -INFINITY ? 0.f : -lse / p.scale * (1.f / kLseSel<T>));
+        if constexpr (kIsHalf<T>) {
+          const float big = fabsf(acc);
+          if (big > 1024.f) w[2] = hi_lo<T>(-acc * (1.f / kDSel));
+          else if (big < 1.f / 16) w[3] = hi_lo<T>(-acc * kDSel);
+          else w[1] = hi_lo<T>(-acc);
+        } else {
+          w[1] = hi_lo<T>(-acc);
+        }
+      }
+      const long long ar = aug0 + row;
+      *reinterpret_cast<uint4 *>(p.aug + ar / 8 * 256 + part * 128 + ar % 8 * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  if constexpr (kIsHalf<T>) {
+    __shared__ int top;
+    if (threadIdx.x == 0) top = 0;
+    __syncthreads();
+    if (part == 0) atomicMax(&top, __float_as_int(norm));
+    __syncthreads();
+    if (threadIdx.x == 0) p.norms[((long long)b * p.heads + h) * gridDim.x + blockIdx.x] = __int_as_float(top);
+  }
+}
+
+// ----------------------------------------------------------------------- 2. dK, dV
+template <int D>
+struct DkvCfg {
+  static constexpr uint32_t kTile = kBM * D * 2;
+  static constexpr bool kSep = D == 64;  // P^T, dS^T in columns of their own
+  using R = Roles<kSep ? 4 : 2>;
+  static constexpr int kStages = D == 128 ? 2 : 5;
+  static constexpr uint32_t kStage = 2 * kTile + kAugBytes;  // Q, dO, the rows' panel
+  static constexpr uint32_t kSel = 2 * kAugBytes;            // selector panels of -LSE / scale and -D
+  // st_full[S] st_empty[S] raw[S] kv_full kv_free s_full s_read p_ready pd_free acc_done acc_free drain
+  static constexpr int kNumBars = 3 * kStages + 9;
+  static constexpr uint32_t kSmem = 2 * kTile + kStages * kStage + kSel + kNumBars * 8 + 64 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static constexpr uint32_t kTmS = 0, kTmDP = 128;
+  static constexpr uint32_t kTmP = kSep ? 256 : kTmS, kTmDS = kSep ? 320 : kTmDP;
+  static constexpr uint32_t kTmDV = kSep ? 384 : 256, kTmDK = kTmDV + D;
+  static_assert(kTmDK + D <= 512, "TMEM budget");
+};
+
+// A key block and the part [c0, c1) of its chunks; chunk c is rows [qa + 128
+// (c % per_head), ...) of head c / per_head of the group.
+struct KeyItem {
+  Sequence s;
+  int b, hk, key0, rows;
+  int qa, qe, per_head, c0, c1, segs;
+  long long slot;  // of the part's sums, or -1: the block is one part
+  __device__ __forceinline__ int first(int c) const { return qa + c % per_head * kBM; }
+  __device__ __forceinline__ int valid(int c) const { return min(kBM, qe - first(c)); }
+};
+
+// The queries that see a key block, and its number of parts.
+__device__ __forceinline__ void block_queries(const WinParams &p, KeyItem &it) {
+  const int off = it.s.nk - it.s.nq;
+  it.rows = min(kBM, it.s.nk - it.key0);
+  it.qa = max(0, it.key0 - off) & ~7;  // panels start at multiples of 8
+  const int past = it.key0 + it.rows - 1 + p.window - off;  // first row past the window of the last key
+  it.qe = it.rows <= 0 ? 0 : it.key0 < p.sinks ? it.s.nq : min(it.s.nq, past);
+  it.per_head = max(0, (it.qe - it.qa + kBM - 1) / kBM);
+  const int total = it.per_head * p.group;
+  it.segs = max(1, (total + p.seg_chunks - 1) / p.seg_chunks);
+}
+
+// Parts are numbered sink blocks first (sink_blocks of them with sink_segs
+// slots each), then the others (norm_segs each), key blocks ascending, the
+// sequences and key heads innermost.
+__device__ __forceinline__ bool key_item(const WinParams &p, int item, KeyItem &it) {
+  const int slices = p.batch * p.kv_heads;
+  const int slice = item % slices, unit = item / slices, sink_units = p.sink_blocks * p.sink_segs;
+  int kb, seg;
+  if (unit < sink_units) {
+    kb = unit / p.sink_segs, seg = unit % p.sink_segs;
+  } else {
+    kb = p.sink_blocks + (unit - sink_units) / p.norm_segs, seg = (unit - sink_units) % p.norm_segs;
+  }
+  it.b = slice / p.kv_heads, it.hk = slice % p.kv_heads;
+  it.s = sequence(p, it.b);
+  it.key0 = kb * kBM;
+  block_queries(p, it);
+  if (it.rows <= 0 || seg >= it.segs) return false;
+  const int total = it.per_head * p.group, per = (total + it.segs - 1) / it.segs;
+  it.c0 = min(total, seg * per), it.c1 = min(total, it.c0 + per);
+  it.slot = it.segs > 1 ? item : -1;
+  return true;
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
+    window_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
+                       const WinParams p, const int n_items) {
+  using C = DkvCfg<D>;
+  using R = typename C::R;
+  constexpr int kCW = R::kCols;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *k_s = smem, *v_s = smem + C::kTile;
+  uint8_t *stages = smem + 2 * C::kTile;
+  uint8_t *sel_s = stages + C::kStages * C::kStage;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sel_s + C::kSel);
+  uint64_t *st_full = bars, *st_empty = bars + C::kStages, *raw = bars + 2 * C::kStages;
+  uint64_t *kv_full = bars + 3 * C::kStages, *kv_free = kv_full + 1;
+  uint64_t *s_full = kv_full + 2;   // S^T, dP^T of a chunk are in TMEM
+  uint64_t *s_read = kv_full + 3;   // ... and have been read (columns of their own only)
+  uint64_t *p_ready = kv_full + 4;  // P^T, dS^T written
+  uint64_t *pd_free = kv_full + 5;  // the dV / dK products have read them (columns of their own only)
+  uint64_t *acc_done = kv_full + 6, *acc_free = kv_full + 7, *drain = kv_full + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3 * C::kStages; ++i) mbar_init(&bars[i], 1);
+    mbar_init(kv_full, 1);
+    mbar_init(kv_free, 1);
+    mbar_init(s_full, 1);
+    mbar_init(s_read, R::kMathWarps);
+    mbar_init(p_ready, R::kMathWarps);
+    mbar_init(pd_free, 1);
+    mbar_init(acc_done, 1);
+    mbar_init(acc_free, R::kMathWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == R::kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  // selector panels, every row alike: (l, l, 0, ...) picks -LSE / scale, (0, 0, 1,
+  // 1[, 2^14, 2^14, 2^-14, 2^-14]) picks -D
+  for (int c = threadIdx.x; c < (int)(C::kSel / 16); c += blockDim.x) {
+    const bool first_half = ((c * 16) % 256) < 128, d_panel = c * 16 >= (int)kAugBytes;
+    const uint32_t one = Elem<T>::pack(1.f, 1.f), l = Elem<T>::pack(kLseSel<T>, kLseSel<T>);
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (first_half && !d_panel) w.x = l;
+    if (first_half && d_panel) {
+      w.y = one;
+      if (kIsHalf<T>) w.z = Elem<T>::pack(kDSel, kDSel), w.w = Elem<T>::pack(1.f / kDSel, 1.f / kDSel);
+    }
+    reinterpret_cast<uint4 *>(sel_s)[c] = w;
+  }
+  fence_proxy_async_cta();
+  const float fac = ds_factor<T>(p, reinterpret_cast<float *>(tmem_slot + 2));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns};
+
+  if (warp == R::kProducerWarp) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmap_q);
+      tma_prefetch_desc(&tmap_k);
+      tma_prefetch_desc(&tmap_v);
+      tma_prefetch_desc(&tmap_do);
+      uint32_t ld = 0, items = 0, raw_par = 0, raw_last = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+        KeyItem it;
+        if (!key_item(p, item, it) || it.c0 == it.c1) continue;
+        if (!mbar_wait(kv_free, (items & 1) ^ 1, ctl, kErrBwdWait)) { ok = false; break; }
+        mbar_arrive_expect_tx(kv_full, 2 * C::kTile);
+        load_tile<D>(k_s, &tmap_k, it.s.k0 + it.key0, it.hk, it.s.slice, kv_full);
+        load_tile<D>(v_s, &tmap_v, it.s.k0 + it.key0, it.hk, it.s.slice, kv_full);
+        ++items;
+        for (int c = it.c0; c < it.c1; ++c) {
+          const uint32_t st = ld % C::kStages, ph = (ld / C::kStages) & 1, bit = 1u << st;
+          if (!mbar_wait(&st_empty[st], ph ^ 1, ctl, kErrBwdWait)) { ok = false; break; }
+          const int h = it.hk * p.group + c / it.per_head, first = it.first(c);
+          const bool clear = it.valid(c) % 16 != 0;
+          uint64_t *bar = clear ? &raw[st] : &st_full[st];
+          raw_last = clear ? raw_last | bit : raw_last & ~bit;
+          if (clear) raw_par ^= bit;
+          uint8_t *sb = stages + st * C::kStage;
+          mbar_arrive_expect_tx(bar, C::kStage);
+          load_tile<D>(sb, &tmap_q, it.s.q0 + first, h, it.s.slice, bar);
+          load_tile<D>(sb + C::kTile, &tmap_do, it.s.q0 + first, h, it.s.slice, bar);
+          bulk_load(sb + 2 * C::kTile, p.aug + (aug_row(p, it.s, it.b, h) + first) / 8 * 256, kAugBytes, bar);
+          ++ld;
+        }
+      }
+      if (!ok) {
+        const uint32_t start = ld > (uint32_t)C::kStages ? ld - C::kStages : 0;
+        for (uint32_t i = start; i < ld; ++i) {
+          const uint32_t st = i % C::kStages;
+          if (raw_last >> st & 1) drain_wait(&raw[st], (raw_par >> st & 1) ^ 1);
+          else drain_wait(&st_full[st], (i / C::kStages) & 1);
+        }
+        if (items > 0) drain_wait(kv_full, (items - 1) & 1);
+      }
+    }
+  } else if (warp == R::kClearWarp) {
+    uint32_t ld = 0, raw_par = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      KeyItem it;
+      if (!key_item(p, item, it)) continue;
+      for (int c = it.c0; c < it.c1 && ok; ++c, ++ld) {
+        const int valid = it.valid(c);
+        if (valid % 16 == 0) continue;
+        const uint32_t st = ld % C::kStages;
+        ok = mbar_wait_w(&raw[st], raw_par >> st & 1, ctl, kErrBwdWait);
+        raw_par ^= 1u << st;
+        if (!ok) break;
+        const int upto = (valid + 15) & ~15;
+        clear_rows<D>(stages + st * C::kStage, valid, upto, lane);
+        clear_rows<D>(stages + st * C::kStage + C::kTile, valid, upto, lane);
+        if (lane == 0) mbar_arrive(&st_full[st]);
+      }
+    }
+  } else if (warp == R::kMmaWarp) {
+    constexpr uint32_t idesc_ss = idesc_for<T>(kBM, kBM, false, false);
+    constexpr uint32_t idesc_acc = idesc_for<T>(kBM, D, false, true);
+    const uint64_t kd = smem_desc_sw128(smem_u32(k_s), 16, 1024), vd = smem_desc_sw128(smem_u32(v_s), 16, 1024);
+    const uint64_t sk0 = smem_desc_sw128(smem_u32(stages), 16, 1024);         // K-major Q / dO
+    const uint64_t sm0 = smem_desc_sw128(smem_u32(stages), kTilePanel, 1024);  // MN-major Q / dO
+    const uint64_t sel_l = smem_desc_plain(smem_u32(sel_s), 128, 256);
+    const uint64_t sel_d = smem_desc_plain(smem_u32(sel_s) + kAugBytes, 128, 256);
+    const uint64_t aug0 = smem_desc_plain(smem_u32(stages + 2 * C::kTile), 128, 256);
+    uint32_t ld = 0, items = 0, p_waits = 0, r_waits = 0;
+    bool ok = true, issued = false;
+    auto issue_s = [&](uint32_t st) {
+      const uint32_t so = (st * C::kStage) >> 4, dso = (st * C::kStage + C::kTile) >> 4;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
+        mma_ss_w(tmem + C::kTmS, kd + off, sk0 + so + off, idesc_ss, kk > 0 ? 1u : 0u);
+      }
+      mma_ss_w(tmem + C::kTmS, sel_l, aug0 + so, idesc_ss, 1u);  // - LSE / scale per query column
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
+        mma_ss_w(tmem + C::kTmDP, vd + off, sk0 + dso + off, idesc_ss, kk > 0 ? 1u : 0u);
+      }
+      mma_ss_w(tmem + C::kTmDP, sel_d, aug0 + so, idesc_ss, 1u);  // - D per query column
+      mma_commit_w(s_full);
+    };
+    auto wait_stage = [&](uint32_t l) -> bool {
+      if (!mbar_wait_w(&st_full[l % C::kStages], (l / C::kStages) & 1, ctl, kErrBwdWait)) return false;
+      tc_fence_after();
+      return true;
+    };
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      KeyItem it;
+      if (!key_item(p, item, it) || it.c0 == it.c1) continue;
+      const int n = it.c1 - it.c0;
+      if (!mbar_wait_w(kv_full, items & 1, ctl, kErrBwdWait)) { ok = false; break; }
+      tc_fence_after();
+      if (!wait_stage(ld)) { ok = false; break; }
+      issue_s(ld % C::kStages);
+      issued = true;
+      for (int i = 0; i < n && ok; ++i) {
+        const uint32_t cur = ld + i, st = cur % C::kStages;
+        if (C::kSep && i + 1 < n) {
+          // the next chunk's S^T / dP^T as soon as this chunk's have been read
+          if (!mbar_wait_w(s_read, r_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
+          ++r_waits;
+          tc_fence_after();
+          if (!wait_stage(cur + 1)) { ok = false; break; }
+          issue_s((cur + 1) % C::kStages);
+        }
+        if (!mbar_wait_w(p_ready, p_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
+        ++p_waits;
+        if (i == 0 && items > 0 && !mbar_wait_w(acc_free, (items - 1) & 1, ctl, kErrBwdWait)) { ok = false; break; }
+        tc_fence_after();
+        const int steps = (it.valid(it.c0 + i) + 15) / 16;
+        const uint32_t so = (st * C::kStage) >> 4, dso = (st * C::kStage + C::kTile) >> 4;
+#pragma unroll
+        for (int kk = 0; kk < kBM / 16; ++kk)
+          if (kk < steps)
+            mma_ts_w(tmem + C::kTmDV, tmem + C::kTmP + kk * 8, sm0 + dso + ((kk * 16 * 128) >> 4), idesc_acc,
+                     (i > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < kBM / 16; ++kk)
+          if (kk < steps)
+            mma_ts_w(tmem + C::kTmDK, tmem + C::kTmDS + kk * 8, sm0 + so + ((kk * 16 * 128) >> 4), idesc_acc,
+                     (i > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_w(&st_empty[st]);
+        if (C::kSep) mma_commit_w(pd_free);
+        if (i + 1 == n) mma_commit_w(kv_free);
+        if (!C::kSep && i + 1 < n) {
+          // P^T / dS^T lie in the S^T / dP^T columns: the next ones follow their readers in order
+          if (!wait_stage(cur + 1)) { ok = false; break; }
+          issue_s((cur + 1) % C::kStages);
+        }
+      }
+      if (!ok) break;
+      ld += n;
+      mma_commit_w(acc_done);
+      ++items;
+    }
+    if (!ok && issued) {
+      mma_commit_w(drain);
+      drain_wait(drain, 0);
+    }
+  } else {
+    // elementwise: thread = key row of the block; warpgroup e owns query columns [kCW e, kCW e + kCW)
+    const int e = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), shift = make_float2(kPShift<T>, kPShift<T>);
+    // dS = P (dP - D), with P's own factor taken out again
+    const float ds_mul = kIsHalf<T> ? fac * exp2f(-kPShift<T>) : 1.f;
+    const float2 dsm = make_float2(ds_mul, ds_mul);
+    uint32_t s_waits = 0, f_waits = 0, items = 0, chunks = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      KeyItem it;
+      if (!key_item(p, item, it)) continue;
+      const int key = it.key0 + row, off = it.s.nk - it.s.nq;
+      for (int c = it.c0; c < it.c1; ++c, ++chunks) {
+        const int first = it.first(c), valid = it.valid(c), qpos = first + off;
+        // whole: all 128 queries see all 128 keys
+        const bool whole = valid == kBM && qpos >= it.key0 + kBM - 1 &&
+                           (qpos + kBM - 1 < it.key0 + p.window || it.key0 + kBM <= p.sinks);
+        const int c_lo = key - qpos - kCW * e;  // columns below do not see this key
+        const int c_hi = min(valid, key < p.sinks ? kBM : min(kBM, key - qpos + p.window)) - kCW * e;
+        bool okw = mbar_wait_w(s_full, s_waits & 1, ctl, kErrBwdWait);
+        ++s_waits;
+        uint32_t pp[kCW / 32][16], pd[kCW / 32][16];
+        auto pds = [&](int q0, int n, const uint32_t *rs, const uint32_t *rd) {
+          const uint32_t bits = whole ? 0xffffffffu : bits_below(c_hi - q0) & ~bits_below(c_lo - q0);
+#pragma unroll
+          for (int k = 0; k < n; ++k) {
+            const int w = q0 / 2 + k;
+            const float2 sv = make_float2(__uint_as_float(rs[2 * k]), __uint_as_float(rs[2 * k + 1]));
+            const float2 t = kIsHalf<T> ? fma2(sv, sl2, shift) : mul2(sv, sl2);
+            float2 pr = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+            float2 dr = mul2(pr, make_float2(__uint_as_float(rd[2 * k]), __uint_as_float(rd[2 * k + 1])));
+            if (kIsHalf<T>) dr = mul2(dr, dsm);
+            if (!whole) {
+              if (!(bits & (1u << (2 * k)))) pr.x = 0.f, dr.x = 0.f;
+              if (!(bits & (2u << (2 * k)))) pr.y = 0.f, dr.y = 0.f;
+            }
+            pp[w >> 4][w & 15] = Elem<T>::pack(pr.x, pr.y);
+            pd[w >> 4][w & 15] = Elem<T>::pack(dr.x, dr.y);
+          }
+        };
+        const uint32_t base = tmem + lane_off + kCW * e;
+        if constexpr (C::kSep) {
+          if (okw) {
+            tc_fence_after();
+            uint32_t rs[32], rd[32];
+            tmem_ld32(base + C::kTmS, rs);
+            tmem_ld32(base + C::kTmDP, rd);
+            tmem_ld_wait();
+            reg_fence32(rs);
+            reg_fence32(rd);
+            if (c + 1 < it.c1) {
+              tc_fence_before();
+              warp_arrive(s_read, lane);
+            }
+            pds(0, 16, rs, rd);
+          }
+        } else {
+          // four quarters of 16 columns, the next quarter's load in flight
+          if (okw) {
+            tc_fence_after();
+            const uint32_t sa = base + C::kTmS, da = base + C::kTmDP;
+            uint32_t s0[16], d0[16], s1[16], d1[16];
+            tmem_ld16(sa, s0);
+            tmem_ld16(da, d0);
+            tmem_ld_wait_regs(s0, d0);
+            tmem_ld16(sa + 16, s1);
+            tmem_ld16(da + 16, d1);
+            pds(0, 8, s0, d0);
+            tmem_ld_wait_regs(s1, d1);
+            tmem_ld16(sa + 32, s0);
+            tmem_ld16(da + 32, d0);
+            pds(16, 8, s1, d1);
+            tmem_ld_wait_regs(s0, d0);
+            tmem_ld16(sa + 48, s1);
+            tmem_ld16(da + 48, d1);
+            pds(32, 8, s0, d0);
+            tmem_ld_wait_regs(s1, d1);
+            pds(48, 8, s1, d1);
+          }
+          // both warpgroups have read their columns before either writes over the first half of them
+          okw = named_bar_and(1, 32 * R::kMathWarps, okw);
+        }
+        if (!okw) { ok = false; break; }
+        if (C::kSep && chunks > 0) {
+          if (!mbar_wait_w(pd_free, f_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
+          ++f_waits;
+          tc_fence_after();
+        }
+        const uint32_t pbase = tmem + lane_off + (kCW / 2) * e;
+#pragma unroll
+        for (int hf = 0; hf < kCW / 32; ++hf) {
+          tmem_st16(pbase + C::kTmP + 16 * hf, pp[hf]);
+          tmem_st16(pbase + C::kTmDS + 16 * hf, pd[hf]);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(p_ready, lane);
+      }
+      if (!ok) break;
+      // epilogue: the first half of the warpgroups writes dV, the second half dK, kOut columns each
+      const bool any = it.c0 < it.c1;
+      if (any) {
+        bool oke = mbar_wait_w(acc_done, items & 1, ctl, kErrBwdWait);
+        if (!C::kSep) oke = named_bar_and(1, 32 * R::kMathWarps, oke);
+        if (!oke) { ok = false; break; }
+        tc_fence_after();
+      }
+      constexpr int kHalf = R::kGroups / 2, kOut = D / kHalf;
+      static_assert(kOut % 32 == 0, "whole 32-column TMEM loads");
+      const int which = e / kHalf, part = e % kHalf;
+      const uint32_t col = (which ? C::kTmDK : C::kTmDV) + part * kOut;
+      const float mul = which ? p.scale / fac : exp2f(-kPShift<T>);
+      const Rows &out = which ? p.dk : p.dv;
+      uint4 *dst = reinterpret_cast<uint4 *>(out.p + 2 * (it.s.slice * out.b + it.hk * out.h +
+                                                          (long long)(it.s.k0 + key) * out.r + part * kOut));
+      float4 *sums = reinterpret_cast<float4 *>(p.parts + ((it.slot * 2 + which) * kBM + row) * D + part * kOut);
+#pragma unroll
+      for (int c = 0; c < kOut / 32; ++c) {
+        uint32_t r[32];
+        if (any) {
+          tmem_ld32(tmem + lane_off + col + c * 32, r);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = 0u;
+        }
+        if (it.slot >= 0) {
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            sums[c * 8 + v] = make_float4(__uint_as_float(r[4 * v]) * mul, __uint_as_float(r[4 * v + 1]) * mul,
+                                          __uint_as_float(r[4 * v + 2]) * mul, __uint_as_float(r[4 * v + 3]) * mul);
+        } else if (row < it.rows) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = Elem<T>::pack(__uint_as_float(r[8 * v + 2 * i]) * mul, __uint_as_float(r[8 * v + 2 * i + 1]) * mul);
+            dst[c * 4 + v] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (any) {
+        tc_fence_before();
+        warp_arrive(acc_free, lane);
+        ++items;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == R::kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The parts of a key block added up in order.
+template <int D, class T>
+__global__ void __launch_bounds__(256) window_join_kernel(const WinParams p) {
+  const int kb = blockIdx.x, slice = blockIdx.y, slices = gridDim.y;
+  KeyItem it;
+  it.b = slice / p.kv_heads, it.hk = slice % p.kv_heads;
+  it.s = sequence(p, it.b);
+  it.key0 = kb * kBM;
+  block_queries(p, it);
+  if (it.rows <= 0 || it.segs == 1) return;
+  const bool sink = kb < p.sink_blocks;
+  const int unit = sink ? kb * p.sink_segs : p.sink_blocks * p.sink_segs + (kb - p.sink_blocks) * p.norm_segs;
+  constexpr int kPer = D / 8;
+  for (int i = threadIdx.x; i < 2 * kBM * kPer; i += 256) {
+    const int which = i / (kBM * kPer), row = i / kPer % kBM, col = i % kPer * 8;
+    if (row >= it.rows) continue;
+    float a[8] = {};
+    for (int seg = 0; seg < it.segs; ++seg) {
+      const long long slot = (long long)(unit + seg) * slices + slice;
+      const float4 *x = reinterpret_cast<const float4 *>(p.parts + ((slot * 2 + which) * kBM + row) * D + col);
+      const float4 u = x[0], v = x[1];
+      a[0] += u.x, a[1] += u.y, a[2] += u.z, a[3] += u.w, a[4] += v.x, a[5] += v.y, a[6] += v.z, a[7] += v.w;
+    }
+    const Rows &out = which ? p.dk : p.dv;
+    *reinterpret_cast<uint4 *>(out.p + 2 * (it.s.slice * out.b + it.hk * out.h + (long long)(it.s.k0 + it.key0 + row) * out.r + col)) =
+        make_uint4(Elem<T>::pack(a[0], a[1]), Elem<T>::pack(a[2], a[3]), Elem<T>::pack(a[4], a[5]), Elem<T>::pack(a[6], a[7]));
+  }
+}
+
+// ----------------------------------------------------------------------- 3. dQ
+template <int D>
+struct DqCfg {
+  static constexpr uint32_t kTile = kBM * D * 2;
+  static constexpr int kSlots = D == 128 ? 4 : 8;
+  using R = Roles<D == 64 ? 4 : 2>;
+  // full[S] empty[S] raw[S] q_full q_free s_full s_read ds_ready ds_free acc_done acc_free drain
+  static constexpr int kNumBars = 3 * kSlots + 9;
+  static constexpr uint32_t kSmem = (2 + kSlots) * kTile + kNumBars * 8 + 64 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static constexpr uint32_t kTmS = 0, kTmDP = 128, kTmDS = 256, kTmDQ = 320;
+  static_assert(kTmDQ + D <= 512, "TMEM budget");
+};
+
+struct QueryItem {
+  Sequence s;
+  int h, qb, pos0, base, last, nsink, ns, nc;
+  __device__ __forceinline__ void chunk(int j, int &first, int &valid) const {
+    first = j < ns ? j * kBM : base + (j - ns) * kBM;
+    valid = min(kBM, (j < ns ? nsink : last + 1) - first);
+  }
+};
+
+__device__ __forceinline__ bool query_item(const WinParams &p, int item, QueryItem &it) {
+  const int slices = p.batch * p.heads, nqb = (p.q_len + kBM - 1) / kBM, slice = item % slices;
+  it.qb = nqb - 1 - item / slices;  // the last blocks have the most keys
+  it.h = slice % p.heads;
+  it.s = sequence(p, slice / p.heads);
+  const int rows = min(kBM, it.s.nq - it.qb * kBM);
+  if (rows <= 0) return false;
+  it.pos0 = it.qb * kBM + it.s.nk - it.s.nq;
+  it.last = min(it.s.nk - 1, it.pos0 + rows - 1);
+  const int lo = max(0, it.pos0 - p.window + 1);
+  it.base = p.sinks >= lo ? 0 : lo;
+  it.nsink = min(p.sinks, it.base);
+  it.ns = (it.nsink + kBM - 1) / kBM;
+  it.nc = it.last >= 0 ? it.ns + (it.last - it.base + kBM) / kBM : 0;
+  return true;
+}
+
+template <int D, class T>
+__global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
+    window_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
+                     const WinParams p, const int n_items) {
+  using C = DqCfg<D>;
+  using R = typename C::R;
+  constexpr int kCW = R::kCols;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *q_s = smem, *do_s = smem + C::kTile, *slots = smem + 2 * C::kTile;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(slots + C::kSlots * C::kTile);
+  uint64_t *full = bars, *empty = bars + C::kSlots, *raw = bars + 2 * C::kSlots;
+  uint64_t *q_full = bars + 3 * C::kSlots, *q_free = q_full + 1;
+  uint64_t *s_full = q_full + 2;    // S, dP of a chunk are in TMEM
+  uint64_t *s_read = q_full + 3;    // ... and have been read
+  uint64_t *ds_ready = q_full + 4;  // dS written
+  uint64_t *ds_free = q_full + 5;   // the dQ products have read it
+  uint64_t *acc_done = q_full + 6, *acc_free = q_full + 7, *drain = q_full + 8;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3 * C::kSlots; ++i) mbar_init(&bars[i], 1);
+    mbar_init(q_full, 1);
+    mbar_init(q_free, 1);
+    mbar_init(s_full, 1);
+    mbar_init(s_read, R::kMathWarps);
+    mbar_init(ds_ready, R::kMathWarps);
+    mbar_init(ds_free, 1);
+    mbar_init(acc_done, 1);
+    mbar_init(acc_free, R::kMathWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == R::kMmaWarp) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  const float fac = ds_factor<T>(p, reinterpret_cast<float *>(tmem_slot + 2));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns};
+
+  if (warp == R::kProducerWarp) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmap_q);
+      tma_prefetch_desc(&tmap_k);
+      tma_prefetch_desc(&tmap_v);
+      tma_prefetch_desc(&tmap_do);
+      uint32_t ld = 0, items = 0, raw_par = 0, raw_last = 0;
+      bool ok = true;
+      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+        QueryItem it;
+        if (!query_item(p, item, it) || it.nc == 0) continue;
+        if (!mbar_wait(q_free, (items & 1) ^ 1, ctl, kErrBwdWait)) { ok = false; break; }
+        mbar_arrive_expect_tx(q_full, 2 * C::kTile);
+        load_tile<D>(q_s, &tmap_q, it.s.q0 + it.qb * kBM, it.h, it.s.slice, q_full);
+        load_tile<D>(do_s, &tmap_do, it.s.q0 + it.qb * kBM, it.h, it.s.slice, q_full);
+        ++items;
+        for (int s = 0; s < 2 * it.nc; ++s) {  // K0 V0 K1 V1 ...
+          int first, valid;
+          it.chunk(s >> 1, first, valid);
+          const uint32_t slot = ld % C::kSlots, phase = (ld / C::kSlots) & 1, bit = 1u << slot;
+          if (!mbar_wait(&empty[slot], phase ^ 1, ctl, kErrBwdWait)) { ok = false; break; }
+          const bool clear = !(s & 1) && valid % 16 != 0;
+          uint64_t *bar = clear ? &raw[slot] : &full[slot];
+          raw_last = clear ? raw_last | bit : raw_last & ~bit;
+          if (clear) raw_par ^= bit;
+          mbar_arrive_expect_tx(bar, C::kTile);
+          load_tile<D>(slots + slot * C::kTile, (s & 1) ? &tmap_v : &tmap_k, it.s.k0 + first, it.h / p.group, it.s.slice, bar);
+          ++ld;
+        }
+      }
+      if (!ok) {
+        const uint32_t start = ld > (uint32_t)C::kSlots ? ld - C::kSlots : 0;
+        for (uint32_t i = start; i < ld; ++i) {
+          const uint32_t slot = i % C::kSlots;
+          if (raw_last >> slot & 1) drain_wait(&raw[slot], (raw_par >> slot & 1) ^ 1);
+          else drain_wait(&full[slot], (i / C::kSlots) & 1);
+        }
+        if (items > 0) drain_wait(q_full, (items - 1) & 1);
+      }
+    }
+  } else if (warp == R::kClearWarp) {
+    uint32_t ld = 0, raw_par = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      QueryItem it;
+      if (!query_item(p, item, it)) continue;
+      for (int j = 0; j < it.nc && ok; ++j) {
+        int first, valid;
+        it.chunk(j, first, valid);
+        if (valid % 16 == 0) continue;
+        const uint32_t slot = (ld + 2 * j) % C::kSlots;
+        ok = mbar_wait_w(&raw[slot], raw_par >> slot & 1, ctl, kErrBwdWait);
+        raw_par ^= 1u << slot;
+        if (!ok) break;
+        clear_rows<D>(slots + slot * C::kTile, valid, (valid + 15) & ~15, lane);
+        if (lane == 0) mbar_arrive(&full[slot]);
+      }
+      ld += 2 * it.nc;
+    }
+  } else if (warp == R::kMmaWarp) {
+    constexpr uint32_t idesc_ss = idesc_for<T>(kBM, kBM, false, false);
+    constexpr uint32_t idesc_dq = idesc_for<T>(kBM, D, false, true);
+    const uint64_t qd = smem_desc_sw128(smem_u32(q_s), 16, 1024), dod = smem_desc_sw128(smem_u32(do_s), 16, 1024);
+    const uint64_t sk0 = smem_desc_sw128(smem_u32(slots), 16, 1024);         // K-major K / V
+    const uint64_t sm0 = smem_desc_sw128(smem_u32(slots), kTilePanel, 1024);  // MN-major K
+    uint32_t ld = 0, items = 0, ds_waits = 0, r_waits = 0;
+    bool ok = true, issued = false;
+    auto issue_s = [&](uint32_t lk) -> bool {
+      const uint32_t lv = lk + 1, ks = lk % C::kSlots, vs = lv % C::kSlots;
+      if (!mbar_wait_w(&full[ks], (lk / C::kSlots) & 1, ctl, kErrBwdWait) ||
+          !mbar_wait_w(&full[vs], (lv / C::kSlots) & 1, ctl, kErrBwdWait))
+        return false;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
+        mma_ss_w(tmem + C::kTmS, qd + off, sk0 + ((ks * C::kTile) >> 4) + off, idesc_ss, kk > 0 ? 1u : 0u);
+      }
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
+        mma_ss_w(tmem + C::kTmDP, dod + off, sk0 + ((vs * C::kTile) >> 4) + off, idesc_ss, kk > 0 ? 1u : 0u);
+      }
+      mma_commit_w(s_full);
+      mma_commit_w(&empty[vs]);  // V is read by dP only
+      return true;
+    };
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      QueryItem it;
+      if (!query_item(p, item, it) || it.nc == 0) continue;
+      if (!mbar_wait_w(q_full, items & 1, ctl, kErrBwdWait)) { ok = false; break; }
+      tc_fence_after();
+      if (!issue_s(ld)) { ok = false; break; }
+      issued = true;
+      if (it.nc == 1) mma_commit_w(q_free);
+      for (int j = 0; j < it.nc && ok; ++j) {
+        const uint32_t lk = ld + 2 * j;
+        if (j + 1 < it.nc) {
+          if (!mbar_wait_w(s_read, r_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
+          ++r_waits;
+          tc_fence_after();
+          if (!issue_s(lk + 2)) { ok = false; break; }
+          if (j + 2 == it.nc) mma_commit_w(q_free);
+        }
+        if (!mbar_wait_w(ds_ready, ds_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
+        ++ds_waits;
+        if (j == 0 && items > 0 && !mbar_wait_w(acc_free, (items - 1) & 1, ctl, kErrBwdWait)) { ok = false; break; }
+        tc_fence_after();
+        int first, valid;
+        it.chunk(j, first, valid);
+        const int steps = (valid + 15) / 16;
+        const uint32_t ks = lk % C::kSlots;
+#pragma unroll
+        for (int kk = 0; kk < kBM / 16; ++kk)
+          if (kk < steps)
+            mma_ts_w(tmem + C::kTmDQ, tmem + C::kTmDS + kk * 8, sm0 + ((ks * C::kTile + kk * 16 * 128) >> 4), idesc_dq,
+                     (j > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_w(&empty[ks]);
+        mma_commit_w(ds_free);
+      }
+      if (!ok) break;
+      ld += 2 * it.nc;
+      mma_commit_w(acc_done);
+      ++items;
+    }
+    if (!ok && issued) {
+      mma_commit_w(drain);
+      drain_wait(drain, 0);
+    }
+  } else {
+    // elementwise: thread = query row; warpgroup e owns key columns [kCW e, kCW e + kCW)
+    const int e = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+    uint32_t s_waits = 0, f_waits = 0, items = 0, chunks = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      QueryItem it;
+      if (!query_item(p, item, it)) continue;
+      const int qrow = it.qb * kBM + row;
+      const bool row_valid = qrow < it.s.nq;
+      float lse2 = 0.f, dd = 0.f;
+      if (row_valid && it.nc > 0) {
+        const long long at = stat_row(p, it.s, it.h, qrow);
+        lse2 = p.lse[at] * kLog2e, dd = p.dd[at];
+      }
+      const float2 nlse2 = make_float2(-lse2, -lse2), ndd = make_float2(-dd, -dd);
+      const float2 fac2 = make_float2(fac, fac);
+      for (int j = 0; j < it.nc; ++j, ++chunks) {
+        int first, valid;
+        it.chunk(j, first, valid);
+        const bool whole = valid == kBM && first + kBM - 1 <= it.pos0 &&
+                           (first > it.pos0 + kBM - 1 - p.window || first + kBM <= p.sinks);
+        if (!mbar_wait_w(s_full, s_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
+        ++s_waits;
+        tc_fence_after();
+        uint32_t rs[kCW / 32][32], rd[kCW / 32][32];
+        const uint32_t base = tmem + lane_off + kCW * e;
+#pragma unroll
+        for (int hf = 0; hf < kCW / 32; ++hf) tmem_ld32(base + C::kTmS + 32 * hf, rs[hf]);
+#pragma unroll
+        for (int hf = 0; hf < kCW / 32; ++hf) tmem_ld32(base + C::kTmDP + 32 * hf, rd[hf]);
+        tmem_ld_wait();
+        if (j + 1 < it.nc) {
+          tc_fence_before();
+          warp_arrive(s_read, lane);
+        }
+        uint32_t pd[kCW / 32][16];
+#pragma unroll
+        for (int hf = 0; hf < kCW / 32; ++hf) {
+          const uint32_t bits =
+              whole ? 0xffffffffu
+                    : visible_bits(it.pos0 + row, first, valid, p.window, p.sinks, (kCW / 32) * e + hf);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 t = fma2(make_float2(__uint_as_float(rs[hf][2 * k]), __uint_as_float(rs[hf][2 * k + 1])), sl2, nlse2);
+            const float2 pr = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+            float2 dr = mul2(pr, add2(make_float2(__uint_as_float(rd[hf][2 * k]), __uint_as_float(rd[hf][2 * k + 1])), ndd));
+            if (kIsHalf<T>) dr = mul2(dr, fac2);
+            if (!whole) {
+              if (!(bits & (1u << (2 * k)))) dr.x = 0.f;
+              if (!(bits & (2u << (2 * k)))) dr.y = 0.f;
+            }
+            pd[hf][k] = Elem<T>::pack(dr.x, dr.y);
+          }
+        }
+        if (chunks > 0) {
+          if (!mbar_wait_w(ds_free, f_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
+          ++f_waits;
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int hf = 0; hf < kCW / 32; ++hf) tmem_st16(tmem + lane_off + C::kTmDS + (kCW / 2) * e + 16 * hf, pd[hf]);
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(ds_ready, lane);
+      }
+      if (!ok) break;
+      if (it.nc > 0) {
+        if (!mbar_wait_w(acc_done, items & 1, ctl, kErrBwdWait)) { ok = false; break; }
+        tc_fence_after();
+      }
+      constexpr int kOut = D / R::kGroups;  // dQ columns of a warpgroup
+      uint4 *dst = reinterpret_cast<uint4 *>(p.dq.p + 2 * (it.s.slice * p.dq.b + it.h * p.dq.h +
+                                                           (long long)(it.s.q0 + qrow) * p.dq.r + e * kOut));
+      const float mul = p.scale / fac;
+#pragma unroll
+      for (int c = 0; c < kOut / 16; ++c) {
+        uint32_t r[16];
+        if (it.nc > 0) {
+          tmem_ld16(tmem + lane_off + C::kTmDQ + e * kOut + c * 16, r);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = 0u;
+        }
+        if (row_valid) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = Elem<T>::pack(__uint_as_float(r[8 * v + 2 * i]) * mul, __uint_as_float(r[8 * v + 2 * i + 1]) * mul);
+            dst[c * 2 + v] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (it.nc > 0) {
+        tc_fence_before();
+        warp_arrive(acc_free, lane);
+        ++items;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == R::kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, class T>
+cudaError_t launch(const WinParams &p, const CUtensorMap *m, int num_sms, cudaStream_t stream) {
+  using K = DkvCfg<D>;
+  using Q = DqCfg<D>;
+  cudaError_t e = cudaFuncSetAttribute(window_dkdv_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(window_dq_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Q::kSmem);
+  if (e != cudaSuccess) return e;
+  const int nqb = (p.q_len + kBM - 1) / kBM, nkb = (p.kv_len + kBM - 1) / kBM, slices = p.batch * p.kv_heads;
+  if (nqb > 0) window_pre_kernel<D, T><<<dim3(nqb, p.heads, p.batch), 256, 0, stream>>>(p);
+  const int kv_items = (p.sink_blocks * p.sink_segs + (nkb - p.sink_blocks) * p.norm_segs) * slices;
+  if (kv_items > 0) {
+    window_dkdv_kernel<D, T><<<kv_items < num_sms ? kv_items : num_sms, K::R::kThreads, K::kSmem, stream>>>(
+        m[0], m[1], m[2], m[3], p, kv_items);
+    const int joined = p.norm_segs > 1 ? nkb : p.sink_segs > 1 ? p.sink_blocks : 0;
+    if (joined > 0) window_join_kernel<D, T><<<dim3(joined, slices), 256, 0, stream>>>(p);
+  }
+  const int q_items = nqb * p.batch * p.heads;
+  if (q_items > 0)
+    window_dq_kernel<D, T><<<q_items < num_sms ? q_items : num_sms, Q::R::kThreads, Q::kSmem, stream>>>(
+        m[0], m[1], m[2], m[3], p, q_items);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_backward(const WinParams &p, int type, const CUtensorMap *maps, int num_sms,
+                                   cudaStream_t stream) {
+  if (p.d == 128)
+    return type == STA_TYPE_BF16 ? launch<128, __nv_bfloat16>(p, maps, num_sms, stream)
+                                 : launch<128, __half>(p, maps, num_sms, stream);
+  return type == STA_TYPE_BF16 ? launch<64, __nv_bfloat16>(p, maps, num_sms, stream)
+                               : launch<64, __half>(p, maps, num_sms, stream);
+}
+
+}  // namespace sta

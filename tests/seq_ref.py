@@ -22,10 +22,10 @@ def unit(dtype):
     return torch.finfo(dtype).eps / 2
 
 
-def attention(q, k, v, mask, scale, do=None, dtype=torch.bfloat16, extra=0.0):
+def attention(q, k, v, mask, scale, do=None, dtype=torch.bfloat16, do_top=0.0):
     """One sequence: q [heads, nq, d], k, v [kv_heads, nk, d], mask [nq, nk].
-    Returns {name: (value, bound)} in fp64.  extra: relative error of K and V
-    values beyond their own type (none here)."""
+    Returns {name: (value, bound)} in fp64.  do_top: the largest row norm of dO
+    in the call, if not this sequence's."""
     g, u = q.shape[0] // k.shape[0], unit(dtype)
     tiny = torch.finfo(dtype).smallest_normal * u * 2  # half a step of the smallest numbers
     q, k, v = q.double(), k.double().repeat_interleave(g, 0), v.double().repeat_interleave(g, 0)
@@ -49,7 +49,10 @@ def attention(q, k, v, mask, scale, do=None, dtype=torch.bfloat16, extra=0.0):
     # the backward adds -LSE and -D to its products as two 16-bit numbers each: 2^-15 relative
     p_rel = e_s + e_l[..., None] + 2.0 ** -15 * torch.where(lse.isinf(), 0.0, lse.abs())[..., None]
     ds = p * (dp - dd)
-    ds_err = ds.abs() * (u + p_rel) + p * (dd_err + 2.0 ** -20 * dp_mag + 2.0 ** -15 * dd.abs()) + mask * tiny
+    # fp16: dS is held times 2^(2 - e), 2^e <= max |dO_i|, so half a step of the
+    # smallest numbers, 2^-25, stands for 2^-25 2^(e - 2) <= 2^-27 max |dO_i|
+    floor = tiny if dtype != torch.float16 else tiny + 2.0 ** -27 * max(do_top, float(do.norm(dim=-1).max()) if do.numel() else 0.0)
+    ds_err = ds.abs() * (u + p_rel) + p * (dd_err + 2.0 ** -20 * dp_mag + 2.0 ** -15 * dd.abs()) + mask * floor
     kv = lambda t: t.unflatten(0, (-1, g)).sum(1)  # noqa: E731
     pv = p * (u + p_rel) + mask * tiny
     dq, dk, dv = ds @ k * scale, kv(ds.mT @ q * scale), kv(p.mT @ do)

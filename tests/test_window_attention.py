@@ -31,7 +31,8 @@ def compare(q, k, v, do, window, sinks, scale=0.0, backward=True):
     grads = window_backward(qd, kd, vd, o, lse, dod, window, sinks, scale, check=True) if backward else ()
     mask = seq_ref.mask_of(q.shape[2], k.shape[2], window, sinks)
     for b in range(q.shape[0]):
-        want = seq_ref.attention(q[b], k[b], v[b], mask, scale or q.shape[3] ** -0.5, do[b] if backward else None, q.dtype)
+        want = seq_ref.attention(q[b], k[b], v[b], mask, scale or q.shape[3] ** -0.5, do[b] if backward else None, q.dtype,
+                                 float(do.double().norm(dim=-1).max()) if do.numel() else 0.0)
         for name, got in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads)):
             seq_ref.check(got[b], want[name], f"{name} of sequence {b}")
     return (o, lse, *grads)
@@ -137,7 +138,8 @@ def test_packed_sequences(dtype, d, lens_q, lens_k, window, sinks, bounds):
     for b in range(len(lens_q)):
         rq, rk = slice(int(cu_q[b]), int(cu_q[b + 1])), slice(int(cu_k[b]), int(cu_k[b + 1]))
         mask = seq_ref.mask_of(lens_q[b], lens_k[b], window, sinks)
-        want = seq_ref.attention(q[0, :, rq], k[0, :, rk], v[0, :, rk], mask, d ** -0.5, do[0, :, rq], dtype)
+        want = seq_ref.attention(q[0, :, rq], k[0, :, rk], v[0, :, rk], mask, d ** -0.5, do[0, :, rq], dtype,
+                                 float(do[0, :, :sum(lens_q)].double().norm(dim=-1).max()))
         for name, got, r in (("o", o, rq), ("lse", lse, rq), ("dq", dq, rq), ("dk", dk, rk), ("dv", dv, rk)):
             seq_ref.check(got[0, :, r], want[name], f"{name} of sequence {b}")
     for t, n in ((o, sum(lens_q)), (lse, sum(lens_q)), (dq, sum(lens_q)), (dk, sum(lens_k)), (dv, sum(lens_k))):
@@ -388,3 +390,23 @@ def test_binding_refusals_on_device():
         assert o.shape == e.shape and lse.shape == e.shape[:3]
         grads = window_backward(e, k, k, o, lse, e, 4)
         assert [g.shape for g in grads] == [e.shape, k.shape, k.shape] and not any(g.any() for g in grads)
+@pytest.mark.gpu
+def test_wait_timeout_is_reported_and_recoverable():
+    q, k, v, do = (t.cuda() for t in make(2, 2, 700, 700, 128, BF16))
+    o, lse = window_forward(q, k, v, 300, 4, check=True)
+    good = window_backward(q, k, v, o, lse, do, 300, 4, check=True)
+    try:
+        sta.sta_set_wait_limit_ns(0)
+        for call in (lambda: window_forward(q, k, v, 300, 4, check=True),
+                     lambda: window_backward(q, k, v, o, lse, do, 300, 4, check=True)):
+            with pytest.raises(sta.StaError) as e:
+                call()
+            assert e.value.status == 8
+    finally:
+        sta.sta_set_wait_limit_ns(2_000_000_000)
+    o2, lse2 = window_forward(q, k, v, 300, 4, check=True)
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    for a, b in zip(window_backward(q, k, v, o, lse, do, 300, 4, check=True), good):
+        assert torch.equal(a, b)
+
+
