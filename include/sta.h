@@ -378,19 +378,16 @@ sta_status sta_cache_read(const sta_cache *cache, int32_t batch, int32_t rows, c
                           int32_t out_type, const int32_t *page_table, int32_t table_pages, const int32_t *start,
                           const int32_t *count, void *stream, uint32_t flags);
 
-/* Workspace bytes of sta_cache_attention. */
-sta_status sta_cache_workspace_size(const sta_cache *cache, int32_t batch, int32_t heads, int32_t q_len,
-                                    int32_t table_pages, int32_t window, int32_t sinks, size_t *bytes);
-
 /* Attention of q_len new queries per sequence (their keys and values already
  * in the cache) over the cache: the forward of sta_window_forward with
  * Nk = lengths[b] (device int32, cut to [0, table_pages * page_size]) and
  * Nq = q_len.  q, o: type `type`; lse fp32 [batch][heads][q_len], nullable.
- * Meant for few queries: every 8 query rows of a key head read its keys once. */
+ * Meant for few queries: every 16 query rows of a key head (heads / kv_heads *
+ * q_len of them) read its keys once.  Needs no workspace. */
 sta_status sta_cache_attention(const sta_cache *cache, int32_t batch, int32_t heads, int32_t q_len, int32_t window,
                                int32_t sinks, float scale, int32_t type, const sta_rows *q, const sta_rows *o,
                                float *lse, const int32_t *page_table, int32_t table_pages, const int32_t *lengths,
-                               void *workspace, size_t workspace_bytes, void *stream, uint32_t flags);
+                               void *stream, uint32_t flags);
 
 /* Static description of a status code. */
 const char *sta_status_string(sta_status status);

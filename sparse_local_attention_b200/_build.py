@@ -10,7 +10,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsta.so")
 SOURCES = ["sta_api.cpp", "sta_permute.cu", "sta_fwd.cu", "sta_bwd.cu", "sta_noalloc.cu",
-           "seq_api.cpp", "seq_attn.cu", "win_fwd.cu", "win_bwd.cu",
+           "seq_api.cpp", "split_attn.cu", "win_fwd.cu", "win_bwd.cu",
            "cache.cu"]
 HEADERS = ["sm100_ptx.cuh", "sta_kernels.h", "sta_common.cuh", "seq_kernels.h", "seq_common.cuh",
            "seq_tile.cuh"]

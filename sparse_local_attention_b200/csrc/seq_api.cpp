@@ -59,6 +59,9 @@ size_t stat_rows(const sta_window_problem *p) {
   return dense > packed ? dense : packed;
 }
 
+// Query rows of a key head up to which the keys are split over the GPU.
+constexpr long long kFewRows = 32;
+
 size_t window_fwd_bytes(const sta_window_problem *) { return kStatusBytes; }
 
 // How the backward's key blocks are cut into parts, and its workspace.  A part
@@ -260,6 +263,10 @@ sta_status sta_window_forward(const sta_window_problem *p, const sta_rows *q, co
   w.q = rows_of(q), w.k = rows_of(k), w.v = rows_of(v), w.o = rows_of(o), w.lse = lse;
   if ((flags & STA_CALL_CHECK) && cudaMemsetAsync(ws, 0, sizeof(int), stream) != cudaSuccess) return STA_ERR_CUDA;
   if (p->q_len > 0) {
+    if ((long long)p->q_len * w.group <= kFewRows) {
+      if (sta::launch_window_split(w, p->type, stream) != cudaSuccess) return STA_ERR_CUDA;
+      return finish(ws, stream, flags);
+    }
     int sms = 0;
     CUtensorMap maps[3];
     if (!multiprocessors(&sms) || !q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
@@ -312,29 +319,20 @@ sta_status sta_cache_read(const sta_cache *c, int32_t batch, int32_t rows, const
   return move_call(false, c, batch, rows, k, v, out_type, table, table_pages, start, count, stream, flags);
 }
 
-sta_status sta_cache_workspace_size(const sta_cache *c, int32_t batch, int32_t heads, int32_t q_len,
-                                    int32_t table_pages, int32_t window, int32_t sinks, size_t *bytes) {
-  if (const sta_status st = check_cache(c, batch, table_pages)) return st;
-  if (!bytes || window < 0 || sinks < 0) return STA_ERR_INVALID_ARG;
-  if (heads < 1 || heads > 65535 || heads % c->kv_heads || q_len < 0 || q_len >= sta::kNoWindow / 2 ||
-      (long long)batch * heads * q_len >= kMaxRows)
-    return STA_ERR_SHAPE;
-  *bytes = kStatusBytes;
-  return STA_OK;
-}
-
 sta_status sta_cache_attention(const sta_cache *c, int32_t batch, int32_t heads, int32_t q_len, int32_t window,
                                int32_t sinks, float scale, int32_t type, const sta_rows *q, const sta_rows *o,
-                               float *lse, const int32_t *table, int32_t table_pages, const int32_t *lengths, void *ws,
-                               size_t ws_bytes, void *stream_, uint32_t flags) {
-  size_t need = 0;
-  if (const sta_status st = sta_cache_workspace_size(c, batch, heads, q_len, table_pages, window, sinks, &need)) return st;
+                               float *lse, const int32_t *table, int32_t table_pages, const int32_t *lengths,
+                               void *stream_, uint32_t flags) {
+  if (const sta_status st = check_cache(c, batch, table_pages)) return st;
+  if (heads < 1 || heads > 65535 || heads % c->kv_heads || q_len < 0 || (long long)batch * heads * q_len >= kMaxRows ||
+      (long long)q_len * (heads / c->kv_heads) > 16 * 65535)
+    return STA_ERR_SHAPE;
   if (!io_type_ok(type)) return STA_ERR_UNSUPPORTED;
-  if ((flags & ~STA_CALL_CHECK) || !(scale == scale) || std::isinf(scale)) return STA_ERR_INVALID_ARG;
+  if ((flags & ~STA_CALL_CHECK) || window < 0 || sinks < 0 || !(scale == scale) || std::isinf(scale))
+    return STA_ERR_INVALID_ARG;
   if (const sta_status st = check_cache_pointers(c, table, lengths)) return st;
   if (const sta_status st = check_rows(q, batch, heads, q_len)) return st;
   if (const sta_status st = check_rows(o, batch, heads, q_len)) return st;
-  if (const sta_status st = check_workspace(ws, ws_bytes, need)) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   sta::CacheAttn a{};
   a.c = cache_params(c, table, table_pages);

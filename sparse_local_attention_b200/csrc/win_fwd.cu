@@ -35,6 +35,10 @@ constexpr int kBM = kTileRows;
 constexpr int kThreads = 352;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kClearWarp = 10;
 
+// P = 2^(s - m) with m the maximum less kHead when it last moved: in fp16 P stays
+// below 2^15 and the smallest number stands for 2^-31 of the row's largest.
+template <class T> constexpr float kHead = std::is_same<T, __half>::value ? 7.f : 0.f;
+
 template <int D>
 struct Cfg {
   static constexpr uint32_t kTile = kBM * D * 2;
@@ -356,8 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int a = 0; a < 4; ++a) t4[a] = fmaxf(fmaxf(t16[4 * a], t16[4 * a + 1]), fmaxf(t16[4 * a + 2], t16[4 * a + 3]));
         const float mloc = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sl2;
-        const bool resc = mloc > m + 8.0f;  // also the first finite maximum
-        const float m_new = resc ? mloc : m;
+        const bool resc = mloc > m + (kHead<T> + 8.0f);  // also the first finite maximum
+        const float m_new = resc ? mloc - kHead<T> : m;
         const float alpha = resc ? ex2_approx(m - m_new) : 1.f;
         const bool warp_resc = __any_sync(0xffffffffu, resc) && seen > 0;
         m = m_new;

@@ -6,14 +6,13 @@ sta_cache_attention of include/sta.h, which state the semantics.
 from __future__ import annotations
 
 import ctypes
-import functools
 from typing import Optional
 
 import torch
 
 from .sta import STA_CALL_CHECK, _check, _ptr, lib
 from .window import (IO_TYPES, STA_TYPE_E4M3, STA_TYPE_INT8, _current_stream, _flat, _in_place, _input, _on, _output,
-                     _rows, _scratch)
+                     _rows)
 
 CACHE_TYPES = {torch.float8_e4m3fn: STA_TYPE_E4M3, torch.int8: STA_TYPE_INT8}
 
@@ -21,15 +20,6 @@ CACHE_TYPES = {torch.float8_e4m3fn: STA_TYPE_E4M3, torch.int8: STA_TYPE_INT8}
 class _Cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("pages", "kv_heads", "page_size", "block", "head_dim", "type")] + [
         (n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
-
-
-@functools.lru_cache(maxsize=256)
-def _attention_bytes(pages, kv_heads, page_size, block, head_dim, dtype, batch, heads, q_len, table_pages, window,
-                     sinks) -> int:
-    c, n = _Cache(pages, kv_heads, page_size, block, head_dim, dtype), ctypes.c_size_t()
-    _check(lib().sta_cache_workspace_size(ctypes.byref(c), batch, heads, q_len, table_pages, window, sinks,
-                                          ctypes.byref(n)), "sta_cache_workspace_size")
-    return n.value
 
 
 class KVCache:
@@ -75,8 +65,7 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, kv_heads, page_size, head_dim
         self.block, self.dtype, self.device = page_size // blocks, k.dtype, k.device
-        self._sizes = (pages, kv_heads, page_size, self.block, head_dim, CACHE_TYPES[k.dtype])
-        self._c = _Cache(*self._sizes, *(t.data_ptr() for t in (k, v, k_scale, v_scale)))
+        self._c = _Cache(pages, kv_heads, page_size, self.block, head_dim, CACHE_TYPES[k.dtype], *(t.data_ptr() for t in (k, v, k_scale, v_scale)))
 
     def _table(self, page_table, batch):
         if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
@@ -132,8 +121,7 @@ class KVCache:
 
     def attention(self, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor, window: int = 0,
                   sinks: int = 0, scale: float = 0.0, o: Optional[torch.Tensor] = None,
-                  lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None,
-                  check: bool = False, want_lse: bool = True):
+                  lse: Optional[torch.Tensor] = None, stream=None, check: bool = False, want_lse: bool = True):
         """(o, lse) of the last Nq positions of each sequence over its cached
         tokens: q [batch, heads, Nq, d], lengths int32 [batch] tokens in the
         cache, the queries' own among them.  The visible keys are those of
@@ -158,12 +146,10 @@ class KVCache:
                 lse = torch.empty(shape[:3], dtype=torch.float32, device=self.device)
             _flat(lse, "lse", shape[:3], torch.float32, self.device)
             if batch and nq:
-                need = _attention_bytes(*self._sizes, batch, heads, nq, page_table.shape[1], int(window), int(sinks))
-                ws = _scratch(workspace, need, self.device)
                 st = lib().sta_cache_attention(ctypes.byref(self._c), batch, heads, nq, int(window), int(sinks),
                                                float(scale), IO_TYPES[q.dtype], _rows(q), _rows(o), _ptr(lse),
-                                               _ptr(page_table), page_table.shape[1], _ptr(lengths), _ptr(ws),
-                                               ws.numel() * ws.element_size(), _current_stream(self.device),
+                                               _ptr(page_table), page_table.shape[1], _ptr(lengths),
+                                               _current_stream(self.device),
                                                STA_CALL_CHECK if check else 0)
                 _check(st, "sta_cache_attention")
         return o, lse

@@ -34,7 +34,7 @@ EXPORTED = ["sta_plan_create", "sta_plan_destroy", "sta_plan_workspace_size", "s
             "sta_status_string", "sta_set_wait_limit_ns", "sta_backward_noalloc", "sta_plan_launches",
             "sta_plan_host_workspace_size", "sta_forward_host", "sta_plan_work_items",
             "sta_window_workspace_size", "sta_window_forward", "sta_window_backward", "sta_cache_write",
-            "sta_cache_read", "sta_cache_workspace_size", "sta_cache_attention"]
+            "sta_cache_read", "sta_cache_attention"]
 STA_WORK_FORWARD, STA_WORK_FORWARD_HOST, STA_WORK_DKDV, STA_WORK_DQ = 0, 1, 2, 3
 
 
@@ -99,9 +99,8 @@ def lib() -> ctypes.CDLL:
     L.sta_window_backward.argtypes = [vp, *[_ROWS] * 4, vp, *[_ROWS] * 4, vp, vp, vp, sz, vp, u32]
     for name in ("sta_cache_write", "sta_cache_read"):
         getattr(L, name).argtypes = [vp, i32, i32, _ROWS, _ROWS, i32, vp, i32, vp, vp, vp, u32]
-    L.sta_cache_workspace_size.argtypes = [vp, i32, i32, i32, i32, i32, i32, szp]
     L.sta_cache_attention.argtypes = [vp, i32, i32, i32, i32, i32, ctypes.c_float, i32, _ROWS, _ROWS, vp, vp, i32, vp,
-                                      vp, sz, vp, u32]
+                                      vp, u32]
     L.sta_status_string.argtypes = [ctypes.c_int]
     L.sta_status_string.restype = ctypes.c_char_p
     L.sta_set_wait_limit_ns.argtypes = [ctypes.c_uint64]

@@ -22,10 +22,11 @@ def unit(dtype):
     return torch.finfo(dtype).eps / 2
 
 
-def attention(q, k, v, mask, scale, do=None, dtype=torch.bfloat16, do_top=0.0):
+def attention(q, k, v, mask, scale, do=None, dtype=torch.bfloat16, do_top=0.0, p_floor=0.0):
     """One sequence: q [heads, nq, d], k, v [kv_heads, nk, d], mask [nq, nk].
     Returns {name: (value, bound)} in fp64.  do_top: the largest row norm of dO
-    in the call, if not this sequence's."""
+    in the call, if not this sequence's.  p_floor: absolute error of a P beyond
+    its relative one."""
     g, u = q.shape[0] // k.shape[0], unit(dtype)
     tiny = torch.finfo(dtype).smallest_normal * u * 2  # half a step of the smallest numbers
     q, k, v = q.double(), k.double().repeat_interleave(g, 0), v.double().repeat_interleave(g, 0)
@@ -36,7 +37,7 @@ def attention(q, k, v, mask, scale, do=None, dtype=torch.bfloat16, do_top=0.0):
     p = torch.where(mask, torch.exp(x - torch.where(lse.isinf(), 0.0, lse)[..., None]), 0.0)
     o = p @ v
     e_l = (p * e_s).sum(-1) + 2.0 ** -22 * torch.where(lse.isinf(), 0.0, lse.abs()) + 2.0 ** -20
-    pe = p * (u + e_s + e_l[..., None]) + mask * tiny
+    pe = p * (u + e_s + e_l[..., None]) + mask * (tiny + p_floor)
     o_bound = pe @ v.abs() + u * o.abs() + tiny
     out = dict(o=(o, o_bound), lse=(lse, e_l))
     if do is None:
