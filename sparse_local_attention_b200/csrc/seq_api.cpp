@@ -267,10 +267,9 @@ sta_status sta_window_forward(const sta_window_problem *p, const sta_rows *q, co
       if (sta::launch_window_split(w, p->type, stream) != cudaSuccess) return STA_ERR_CUDA;
       return finish(ws, stream, flags);
     }
-    int sms = 0;
     CUtensorMap maps[3];
-    if (!multiprocessors(&sms) || !q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
-        !kv_map(&maps[2], v, p, cu_q) || sta::launch_window_tiles(w, p->type, maps, sms, stream) != cudaSuccess)
+    if (!q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
+        !kv_map(&maps[2], v, p, cu_q) || sta::launch_window_tiles(w, p->type, maps, stream) != cudaSuccess)
       return STA_ERR_CUDA;
   }
   return finish(ws, stream, flags);

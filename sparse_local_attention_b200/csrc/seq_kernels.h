@@ -76,7 +76,7 @@ struct CacheAttn {
 cudaError_t launch_cache_attention(const CacheAttn &a, int cache_type, int io_type, cudaStream_t stream);
 
 // Forward on 128-row tiles; maps: q, k, v.
-cudaError_t launch_window_tiles(const WinParams &p, int type, const CUtensorMap *maps, int num_sms, cudaStream_t stream);
+cudaError_t launch_window_tiles(const WinParams &p, int type, const CUtensorMap *maps, cudaStream_t stream);
 // Forward of a few query rows per key head, the keys split over the GPU.
 cudaError_t launch_window_split(const WinParams &p, int type, cudaStream_t stream);
 // Backward; maps: q, k, v, dO.

@@ -10,7 +10,7 @@
 //     are numbered block by block, the heads of the group within a block, and
 //     a work item is two consecutive units (A, B): every key chunk in shared
 //     memory serves 256 query rows, with any number of heads per key head.
-//     Persistent grid, one CTA per SM, the blocks with the most keys first.
+//     The blocks with the most keys come first, on whichever SM is free.
 //   * An item's keys are its sinks, then its window [lo, hi], each in chunks
 //     of 128 from its own first key on (TMA rows need no alignment), so no
 //     chunk holds keys below every row's window, and a chunk that one of the
@@ -48,7 +48,8 @@ struct Cfg {
   static constexpr int kLead = D == 128 ? 96 : 64;  // keys of the first part of P V
   // full[S] empty[S] raw[S] q_full q_free s_full[2] p_ready[2] pv_done[2] o_free[2] drain p_lead[2]
   static constexpr int kNumBars = 3 * kSlots + 13;
-  static constexpr uint32_t kSmem = (2 + kSlots) * kTile + kNumBars * 8 + 64 + 1024;
+  static constexpr uint32_t kInfo = 8 * 64;  // per softmax warp: what it keeps of its item
+  static constexpr uint32_t kSmem = (2 + kSlots) * kTile + kNumBars * 8 + 64 + kTicketBytes + 16 + kInfo + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -105,7 +106,7 @@ __device__ __forceinline__ Item decode(const WinParams &p, int item) {
 template <int D, class T>
 __global__ void __launch_bounds__(kThreads, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                      const __grid_constant__ CUtensorMap tmap_v, const WinParams p, const int n_items) {
+                      const __grid_constant__ CUtensorMap tmap_v, const WinParams p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -118,9 +119,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *drain = o_free + 2, *p_lead = drain + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const Tickets tickets = tickets_at(
+      reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(tmem_slot) + 64 + 15) & ~uintptr_t(15)));
+  volatile int *info_s = reinterpret_cast<volatile int *>(reinterpret_cast<uint8_t *>(tickets.answer) + kTicketBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    tickets_init(tickets, 10);  // softmax warps, MMA, clear
     for (int i = 0; i < 3 * C::kSlots; ++i) mbar_init(&bars[i], 1);
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
@@ -151,8 +156,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmap_k);
       tma_prefetch_desc(&tmap_v);
       uint32_t ld = 0, items = 0, raw_par = 0, raw_last = 0;  // per slot: parity of raw, last load went to raw
+      uint32_t asked = 0, taken = 0;
       bool ok = true;
-      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      int item = blockIdx.x;
+      for (; item >= 0 && ok; item = ok ? ticket_take(tickets, taken, ok, ctl, kErrWaitProducer) : 0) {
+        if (!ticket_ask(tickets, asked, ctl, kErrWaitProducer)) { ok = false; break; }
+        ++asked;
         const Item it = decode(p, item);
         if (it.nc == 0) continue;
         if (!mbar_wait(q_free, (items & 1) ^ 1, ctl, kErrWaitProducer)) { ok = false; break; }
@@ -184,12 +193,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           else drain_wait(&full[slot], (i / C::kSlots) & 1);
         }
         if (items > 0) drain_wait(q_full, (items - 1) & 1);
+        tickets_discard(tickets, asked, taken, item < 0);
       }
     }
   } else if (warp == kClearWarp) {
-    uint32_t ld = 0, raw_par = 0;
+    uint32_t ld = 0, raw_par = 0, taken = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+    for (int item = blockIdx.x; item >= 0 && ok; item = ok ? ticket_next(tickets, taken, ok, ctl, kErrWaitProducer, lane) : -1) {
       const Item it = decode(p, item);
       for (int j = 0; j < it.nc && ok; ++j) {
         int first, valid;
@@ -211,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t qdesc0 = smem_desc_sw128(smem_u32(q_smem), 16, 1024);
     const uint64_t kdesc0 = smem_desc_sw128(slots_addr, 16, 1024);
     const uint64_t vdesc0 = smem_desc_sw128(slots_addr, kTilePanel, 1024);
-    uint32_t ld = 0, items = 0;
+    uint32_t ld = 0, items = 0, taken = 0;
     uint32_t p_waits[2] = {0, 0}, o_waits[2] = {0, 0}, used[2] = {0, 0};
     bool ok = true, issued = false;
     auto mma_s = [&](int x, uint32_t slot) {
@@ -244,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       return true;
     };
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+    for (int item = blockIdx.x; item >= 0 && ok; item = ok ? ticket_next(tickets, taken, ok, ctl, kErrWaitMma, lane) : -1) {
       const Item it = decode(p, item);
       if (it.nc == 0) continue;
       if (!mbar_wait_w(q_full, items & 1, ctl, kErrWaitMma)) { ok = false; break; }
@@ -306,109 +316,148 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_off + 128 * x, o_tm = tmem + lane_off + C::kTmO + x * D;
     const float sl2 = p.scale_log2;
-    uint32_t s_waits = 0;
+    uint32_t s_waits = 0, taken = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      const Item it = decode(p, item);
-      if (!pick(it.has, x)) continue;
-      const int pos0 = pick(it.pos0, x), qrow = pick(it.qb, x) * kBM + row;
-      const bool row_valid = qrow < it.s.nq;
+    // What the passes over an item's chunks need of it lies in shared memory,
+    // a copy per warp: beside a row of 128 scores registers are short.
+    volatile int *info = info_s + 16 * warp;
+    enum { kSinkChunks, kChunks, kBase, kLast, kSinkKeys, kLo, kHi, kPos0 };
+    for (int item = blockIdx.x; item >= 0 && ok; item = ok ? ticket_next(tickets, taken, ok, ctl, kErrWaitSoftmax, lane) : -1) {
+      {
+        const Item it = decode(p, item);
+        if (!pick(it.has, x)) continue;
+        __syncwarp();
+        if (lane == 0) {
+          info[kSinkChunks] = it.ns, info[kChunks] = it.nc, info[kBase] = it.base, info[kLast] = it.last;
+          info[kSinkKeys] = it.nsink, info[kLo] = pick(it.lo, x), info[kHi] = pick(it.hi, x), info[kPos0] = pick(it.pos0, x);
+        }
+        __syncwarp();
+      }
       float m = -INFINITY, l = 0.f;
-      int seen = 0;
-      for (int j = 0; j < it.nc; ++j) {
+      bool seen = false;
+      for (int j = 0; j < info[kChunks]; ++j) {
         int first, valid;
-        it.chunk(j, first, valid);
-        if (!sees(it, x, first, valid, p.sinks)) continue;
+        {
+          const int ns = info[kSinkChunks];
+          first = j < ns ? j * kBM : info[kBase] + (j - ns) * kBM;
+          valid = min(kBM, (j < ns ? info[kSinkKeys] : info[kLast] + 1) - first);
+        }
+        if (!(first <= info[kHi] && (first + valid > info[kLo] || first < p.sinks))) continue;
         if (!mbar_wait_w(&s_full[x], s_waits & 1, ctl, kErrWaitSoftmax)) { ok = false; break; }
         ++s_waits;
         tc_fence_after();
         // O_X holds every chunk before this one: S was issued after their P V
-        float s[kBM];
+        // whole: every row of the unit sees all 128 keys
+        const int pos0 = info[kPos0];
+        const bool whole = valid == kBM && first + kBM - 1 <= pos0 &&
+                           (first > pos0 + kBM - 1 - p.window || first + kBM <= p.sinks);
+        auto mask = [&](uint32_t(&r)[32], int w) {
+          if (whole) return;
+          const uint32_t bits = visible_bits(pos0 + row, first, valid, p.window, p.sinks, w);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(bits & (1u << i))) r[i] = 0xff800000u;  // -inf
+        };
+        // The row maximum takes all 128 scores; the second half is then read
+        // from tensor memory again, a quarter at a time, while P of the quarter
+        // before is formed: held throughout, the scores would not fit.
+        uint32_t r0[32], r1[32];
+        float mloc;
         {
-          uint32_t r0[32], r1[32], r2[32], r3[32];
+          uint32_t r2[32], r3[32];
           tmem_ld32(s_tm, r0);
           tmem_ld32(s_tm + 32, r1);
           tmem_ld32(s_tm + 64, r2);
           tmem_ld32(s_tm + 96, r3);
           tmem_ld_wait();
+          reg_fence32(r0);
+          reg_fence32(r1);
+          reg_fence32(r2);
+          reg_fence32(r3);
+          mask(r0, 0);
+          mask(r1, 1);
+          mask(r2, 2);
+          mask(r3, 3);
+          float t[4];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            s[i] = __uint_as_float(r0[i]);
-            s[32 + i] = __uint_as_float(r1[i]);
-            s[64 + i] = __uint_as_float(r2[i]);
-            s[96 + i] = __uint_as_float(r3[i]);
+          for (int a = 0; a < 4; ++a) {
+            auto at = [&](int i) { return __uint_as_float(i < 8 ? r0[8 * a + i] : i < 16 ? r1[8 * a + i - 8] : i < 24 ? r2[8 * a + i - 16] : r3[8 * a + i - 24]); };
+            t[a] = max3(at(0), at(1), at(2));
+#pragma unroll
+            for (int i = 3; i < 31; i += 2) t[a] = max3(t[a], at(i), at(i + 1));
+            t[a] = fmaxf(t[a], at(31));
           }
+          mloc = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * sl2;
         }
-        // whole: every row of the unit sees all 128 keys
-        const bool whole = valid == kBM && first + kBM - 1 <= pos0 &&
-                           (first > pos0 + kBM - 1 - p.window || first + kBM <= p.sinks);
-        if (!whole) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t bits = visible_bits(pos0 + row, first, valid, p.window, p.sinks, w);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(bits & (1u << i))) s[32 * w + i] = -INFINITY;
-          }
-        }
-        float t16[16];
-#pragma unroll
-        for (int a = 0; a < 16; ++a)
-          t16[a] = max3(max3(s[8 * a], s[8 * a + 1], s[8 * a + 2]), max3(s[8 * a + 3], s[8 * a + 4], s[8 * a + 5]),
-                        fmaxf(s[8 * a + 6], s[8 * a + 7]));
-        float t4[4];
-#pragma unroll
-        for (int a = 0; a < 4; ++a) t4[a] = fmaxf(fmaxf(t16[4 * a], t16[4 * a + 1]), fmaxf(t16[4 * a + 2], t16[4 * a + 3]));
-        const float mloc = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sl2;
         const bool resc = mloc > m + (kHead<T> + 8.0f);  // also the first finite maximum
         const float m_new = resc ? mloc - kHead<T> : m;
         const float alpha = resc ? ex2_approx(m - m_new) : 1.f;
-        const bool warp_resc = __any_sync(0xffffffffu, resc) && seen > 0;
+        const bool warp_resc = __any_sync(0xffffffffu, resc) && seen;
         m = m_new;
         const float ms = m == -INFINITY ? 0.f : m;  // a row without a visible key so far: P = 0
-        float ls[8];
+        const float2 sl2x2 = make_float2(sl2, sl2), nms = make_float2(-ms, -ms);
+        float2 ls[4];
 #pragma unroll
-        for (int a = 0; a < 8; ++a) ls[a] = 0.f;
-#pragma unroll
-        for (int c = 0; c < kBM / 32; ++c) {
+        for (int a = 0; a < 4; ++a) ls[a] = make_float2(0.f, 0.f);
+        // P of 32 keys from their scores: written over S, added to the row sum
+        auto form = [&](const uint32_t(&r)[32], int c) {
           uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float p0 = ex2_approx(fmaf(s[32 * c + i], sl2, -ms));
-            const float p1 = ex2_approx(fmaf(s[32 * c + i + 1], sl2, -ms));
-            ls[(i / 2) & 7] += p0 + p1;
-            pk[i / 2] = Elem<T>::pack(p0, p1);
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = fma2(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), sl2x2, nms);
+            const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            ls[i & 3] = add2(ls[i & 3], e);
+            pk[i] = Elem<T>::pack(e.x, e.y);
           }
           tmem_st16(s_tm + c * 16, pk);
-          if (c == 1 && warp_resc) {
+        };
+        auto lead = [&]() {
+          tmem_st_wait();
+          tc_fence_before();
+          warp_arrive(&p_lead[x], lane);
+        };
+        form(r0, 0);
+        uint32_t r2[32];
+        tmem_ld32(s_tm + 64, r2);
+        form(r1, 1);
+        if (warp_resc) {
 #pragma unroll 1
-            for (int oc = 0; oc < D / 16; ++oc) {
-              uint32_t r[16];
-              tmem_ld16(o_tm + oc * 16, r);
-              tmem_ld_wait();
+          for (int oc = 0; oc < D / 16; ++oc) {
+            uint32_t r[16];
+            tmem_ld16(o_tm + oc * 16, r);
+            tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-              tmem_st16(o_tm + oc * 16, r);
-            }
-          }
-          if (c == C::kLead / 32 - 1) {
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(&p_lead[x], lane);
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+            tmem_st16(o_tm + oc * 16, r);
           }
         }
-        l = l * alpha + (((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7])));
+        if constexpr (C::kLead == 64) lead();
+        uint32_t r3[32];
+        tmem_ld32(s_tm + 96, r3);
+        tmem_ld_wait();
+        reg_fence32(r2);
+        reg_fence32(r3);
+        mask(r2, 2);
+        form(r2, 2);
+        if constexpr (C::kLead == 96) lead();
+        mask(r3, 3);
+        form(r3, 3);
+        const float2 sum = add2(add2(ls[0], ls[1]), add2(ls[2], ls[3]));
+        l = l * alpha + (sum.x + sum.y);
         tmem_st_wait();
         tc_fence_before();
         warp_arrive(&p_ready[x], lane);
-        ++seen;
+        seen = true;
       }
       if (!ok) break;
-      if (seen > 0) {
+      if (seen) {
         // one P V per chunk so far: the last one's phase
         if (!mbar_wait_w(&pv_done[x], (s_waits - 1) & 1, ctl, kErrWaitEpilogue)) { ok = false; break; }
         tc_fence_after();
       }
+      const Item it = decode(p, item);
+      const int qrow = pick(it.qb, x) * kBM + row;
+      const bool row_valid = qrow < it.s.nq;
       const bool none = l == 0.f;
       const float inv_l = none ? 0.f : 1.f / l;
       uint4 *dst = reinterpret_cast<uint4 *>(p.o.p + 2 * ((long long)it.s.slice * p.o.b + (long long)pick(it.h, x) * p.o.h +
@@ -416,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t r[32];
-        if (seen > 0) {
+        if (seen) {
           tmem_ld32(o_tm + c * 32, r);
           tmem_ld_wait();
         }
@@ -433,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (seen > 0) {
+      if (seen) {
         tc_fence_before();
         warp_arrive(&o_free[x], lane);
       }
@@ -452,25 +501,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, class T>
-cudaError_t launch(const WinParams &p, const CUtensorMap *maps, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const WinParams &p, const CUtensorMap *maps, cudaStream_t stream) {
   using C = Cfg<D>;
   const cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
   const long long nqb = (p.q_len + kBM - 1) / kBM;
   const long long items = (nqb * p.group + 1) / 2 * p.batch * p.kv_heads;
-  const int grid = (int)(items < num_sms ? items : num_sms);
-  window_fwd_kernel<D, T><<<grid, kThreads, C::kSmem, stream>>>(maps[0], maps[1], maps[2], p, (int)items);
+  window_fwd_kernel<D, T><<<(unsigned)items, kThreads, C::kSmem, stream>>>(maps[0], maps[1], maps[2], p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_window_tiles(const WinParams &p, int type, const CUtensorMap *maps, int num_sms, cudaStream_t stream) {
+cudaError_t launch_window_tiles(const WinParams &p, int type, const CUtensorMap *maps, cudaStream_t stream) {
   if (p.d == 128)
-    return type == STA_TYPE_BF16 ? launch<128, __nv_bfloat16>(p, maps, num_sms, stream)
-                                 : launch<128, __half>(p, maps, num_sms, stream);
-  return type == STA_TYPE_BF16 ? launch<64, __nv_bfloat16>(p, maps, num_sms, stream)
-                               : launch<64, __half>(p, maps, num_sms, stream);
+    return type == STA_TYPE_BF16 ? launch<128, __nv_bfloat16>(p, maps, stream)
+                                 : launch<128, __half>(p, maps, stream);
+  return type == STA_TYPE_BF16 ? launch<64, __nv_bfloat16>(p, maps, stream)
+                               : launch<64, __half>(p, maps, stream);
 }
 
 }  // namespace sta
