@@ -64,90 +64,118 @@ __device__ __forceinline__ uint32_t visible_bits(int pos, int base, int valid, i
 // Each kernel below is launched with one CTA per work item, but a running CTA
 // takes over items whose CTAs have not started yet (cluster launch control), so
 // items of uneven cost spread over the SMs while the pipelines of one CTA run
-// from item to item without a restart.  The producer warp asks for the next
-// item when it starts one; every role reads the answer when it is done with
-// its own.  Two answers are in flight at most.
-struct Tickets {
-  uint4 *answer;  // [2], shared memory
-  uint64_t *full, *empty;  // [2] each; empty: one arrival per consumer warp
+// from item to item without a restart.  The producer thread asks for the next
+// item when it starts one, and leaves what the other roles need of an item in
+// a ring of two, ahead of them.  Item::stop marks the end.
+template <class Item>
+struct ItemRing {
+  Item *items;              // [2]
+  uint64_t *full, *empty;   // [2] each; empty: one arrival per consumer warp
+  uint4 *answer;
+  uint64_t *answered;
+  static constexpr uint32_t kBytes = 16 + 5 * 8 + 2 * sizeof(Item) + 15;
+
+  __device__ __forceinline__ explicit ItemRing(void *smem) {
+    answer = reinterpret_cast<uint4 *>((reinterpret_cast<uintptr_t>(smem) + 15) & ~uintptr_t(15));
+    full = reinterpret_cast<uint64_t *>(answer + 1);
+    empty = full + 2, answered = full + 4;
+    items = reinterpret_cast<Item *>(full + 5);
+  }
+  __device__ __forceinline__ void init(int consumers) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], consumers);
+    }
+    mbar_init(answered, 1);
+  }
+
+  // ---- the producer thread
+  __device__ __forceinline__ bool put(uint32_t n, const Item &it, const WaitCtl &ctl, int code) {
+    if (!mbar_wait(&empty[n & 1], ((n >> 1) & 1) ^ 1, ctl, code)) return false;
+    items[n & 1] = it;
+    mbar_arrive(&full[n & 1]);
+    return true;
+  }
+  // ask for the item after the n-th (not after an answer of none)
+  __device__ __forceinline__ void ask() {
+    fence_proxy_async_cta();  // the answer before has been read
+    mbar_arrive_expect_tx(answered, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(answered))
+                 : "memory");
+  }
+  __device__ __forceinline__ int read() const {
+    uint32_t some, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(some), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return some ? (int)x : -1;
+  }
+  // the item after the n-th, or -1: there is none left
+  __device__ __forceinline__ bool take(uint32_t n, int &item, const WaitCtl &ctl, int code) {
+    if (!mbar_wait(answered, n & 1, ctl, code)) return false;
+    item = read();
+    return true;
+  }
+  // After an abort in the n-th item (`asked`: its successor has been asked for):
+  // take the items that are left, so that no CTA starts on them only to wait in
+  // vain.
+  __device__ __forceinline__ void discard(uint32_t n, bool asked) {
+    while (true) {
+      if (!asked) ask();
+      asked = false;
+      if (!drain_wait(answered, n & 1) || read() < 0) return;
+      ++n;
+    }
+  }
+
+  // ---- a consumer warp
+  // The n-th item, or none: the end, or a wait that ran out (ok = false).
+  __device__ __forceinline__ const Item *get(uint32_t n, bool &ok, const WaitCtl &ctl, int code) const {
+    if (!mbar_wait_w(&full[n & 1], (n >> 1) & 1, ctl, code)) {
+      ok = false;
+      return nullptr;
+    }
+    const Item *it = &items[n & 1];
+    return it->stop ? nullptr : it;
+  }
+  __device__ __forceinline__ void release(uint32_t n, int lane) const {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[n & 1]);
+  }
 };
-constexpr uint32_t kTicketBytes = 2 * 16 + 4 * 8;
 
-__device__ __forceinline__ Tickets tickets_at(void *smem16) {
-  uint4 *a = static_cast<uint4 *>(smem16);
-  uint64_t *b = reinterpret_cast<uint64_t *>(a + 2);
-  return Tickets{a, b, b + 2};
-}
-__device__ __forceinline__ void tickets_init(const Tickets &t, int consumers) {
-  for (int i = 0; i < 2; ++i) {
-    mbar_init(&t.full[i], 1);
-    mbar_init(&t.empty[i], consumers);
-  }
-}
-
-__device__ __forceinline__ void ticket_cancel(const Tickets &t, uint32_t k) {
-  mbar_arrive_expect_tx(&t.full[k & 1], 16);
-  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                   smem_u32(&t.answer[k & 1])),
-               "r"(smem_u32(&t.full[k & 1]))
-               : "memory");
-}
-
-// Ask for the k-th answer (the producer thread; not after an answer of none).
-__device__ __forceinline__ bool ticket_ask(const Tickets &t, uint32_t k, const WaitCtl &ctl, int code) {
-  if (!mbar_wait(&t.empty[k & 1], ((k >> 1) & 1) ^ 1, ctl, code)) return false;
-  ticket_cancel(t, k);
-  return true;
-}
-
-// The item in the k-th answer, or -1: there is none left.
-__device__ __forceinline__ int ticket_read(const Tickets &t, uint32_t k) {
-  uint32_t some, x;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
-      "ld.shared.b128 h, [%2];\n\t"
-      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t"
-      "mov.u32 %1, 0;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
-      : "=r"(some), "=r"(x)
-      : "r"(smem_u32(&t.answer[k & 1]))
-      : "memory");
-  fence_proxy_async_cta();  // the next answer is written by the async proxy
-  return some ? (int)x : -1;
-}
-
-// The k-th answer for a whole consumer warp (-1: none, or a wait ran out).
-__device__ __forceinline__ int ticket_next(const Tickets &t, uint32_t &k, bool &ok, const WaitCtl &ctl, int code, int lane) {
-  if (!mbar_wait_w(&t.full[k & 1], (k >> 1) & 1, ctl, code)) {
-    ok = false;
-    return -1;
-  }
-  const int item = ticket_read(t, k);
-  __syncwarp();
-  if (lane == 0) mbar_arrive(&t.empty[k & 1]);
-  ++k;
-  return item;
-}
-
-// The k-th answer for the producer thread, which is not counted as a consumer.
-__device__ __forceinline__ int ticket_take(const Tickets &t, uint32_t &k, bool &ok, const WaitCtl &ctl, int code) {
-  if (!mbar_wait(&t.full[k & 1], (k >> 1) & 1, ctl, code)) {
-    ok = false;
-    return -1;
-  }
-  return ticket_read(t, k++);
-}
-
-// After an abort (the producer thread; `asked` answers asked for, `taken`
-// read): take the items that are left, so that no CTA starts on them only to
-// wait in vain.  The consumers have left, so their arrivals are not waited for.
-__device__ __forceinline__ void tickets_discard(const Tickets &t, uint32_t asked, uint32_t taken, bool none) {
-  while (!none) {
-    if (asked == taken) ticket_cancel(t, asked++);
-    if (!drain_wait(&t.full[taken & 1], (taken >> 1) & 1)) return;
-    none = ticket_read(t, taken++) < 0;
-  }
+// Four 16-byte pieces of this lane's row, columns 64 bytes wide, stored so that
+// four lanes write a row's 64 bytes together (a 4 x 4 exchange among them): a
+// lane for a row would touch 32 lines with every store.  `first`: the row of the
+// quad's first lane at those columns; rows `pitch` bytes apart, `rows` of the
+// quad there.
+__device__ __forceinline__ void store_quad(uint4 (&w)[4], char *first, long long pitch, int rows, int lane) {
+  auto swap = [&](uint4 &a, uint4 &b, int bit) {
+    const bool up = lane & bit;
+    uint4 give = up ? a : b;
+    give.x = __shfl_xor_sync(0xffffffffu, give.x, bit);
+    give.y = __shfl_xor_sync(0xffffffffu, give.y, bit);
+    give.z = __shfl_xor_sync(0xffffffffu, give.z, bit);
+    give.w = __shfl_xor_sync(0xffffffffu, give.w, bit);
+    if (up) a = give;
+    else b = give;
+  };
+  swap(w[0], w[1], 1);
+  swap(w[2], w[3], 1);
+  swap(w[0], w[2], 2);
+  swap(w[1], w[3], 2);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < rows) *reinterpret_cast<uint4 *>(first + k * pitch + 16 * (lane & 3)) = w[k];
 }
 
 }  // namespace sta

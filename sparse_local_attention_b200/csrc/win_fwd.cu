@@ -35,25 +35,8 @@ constexpr int kBM = kTileRows;
 constexpr int kThreads = 352;
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kClearWarp = 10;
 
-// P = 2^(s - m) with m the maximum less kHead when it last moved: in fp16 P stays
-// below 2^15 and the smallest number stands for 2^-31 of the row's largest.
-template <class T> constexpr float kHead = std::is_same<T, __half>::value ? 7.f : 0.f;
-
-template <int D>
-struct Cfg {
-  static constexpr uint32_t kTile = kBM * D * 2;
-  static constexpr int kSlots = D == 128 ? 4 : 8;  // ring of K and V chunks
-  static constexpr uint32_t kTmO = 256;            // O_X at kTmO + X * D; S_X at 128 * X
-  static constexpr uint32_t kTmCols = 512;
-  static constexpr int kLead = D == 128 ? 96 : 64;  // keys of the first part of P V
-  // full[S] empty[S] raw[S] q_full q_free s_full[2] p_ready[2] pv_done[2] o_free[2] drain p_lead[2]
-  static constexpr int kNumBars = 3 * kSlots + 13;
-  static constexpr uint32_t kInfo = 8 * 64;  // per softmax warp: what it keeps of its item
-  static constexpr uint32_t kSmem = (2 + kSlots) * kTile + kNumBars * 8 + 64 + kTicketBytes + 16 + kInfo + 1024;
-  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-};
-
 struct Item {
+  bool stop;
   Sequence s;
   int hk;
   int h[2], qb[2];   // query head and query block of A and B
@@ -67,17 +50,32 @@ struct Item {
   }
 };
 
-// a[x] without indexing a register array by a run-time x
-template <class V>
-__device__ __forceinline__ V pick(const V (&a)[2], int x) { return x ? a[1] : a[0]; }
+// P = 2^(s - m) with m the maximum less kHead when it last moved: in fp16 P stays
+// below 2^15 and the smallest number stands for 2^-31 of the row's largest.
+template <class T> constexpr float kHead = std::is_same<T, __half>::value ? 7.f : 0.f;
+
+template <int D>
+struct Cfg {
+  static constexpr uint32_t kTile = kBM * D * 2;
+  static constexpr int kSlots = D == 128 ? 4 : 8;  // ring of K and V chunks
+  static constexpr uint32_t kTmO = 256;            // O_X at kTmO + X * D; S_X at 128 * X
+  static constexpr uint32_t kTmCols = 512;
+  static constexpr int kLead = D == 128 ? 96 : 64;  // keys of the first part of P V
+  // full[S] empty[S] raw[S] q_full q_free s_full[2] p_ready[2] pv_done[2] o_free[2] drain p_lead[2]
+  static constexpr int kNumBars = 3 * kSlots + 13;
+  static constexpr uint32_t kSmem = (2 + kSlots) * kTile + kNumBars * 8 + 64 + ItemRing<Item>::kBytes + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
 
 // Whether unit x sees a key of a chunk (hi is below 0 for a unit that is not there).
 __device__ __forceinline__ bool sees(const Item &it, int x, int first, int valid, int sinks) {
-  return first <= pick(it.hi, x) && (first + valid > pick(it.lo, x) || first < sinks);
+  return first <= it.hi[x] && (first + valid > it.lo[x] || first < sinks);
 }
 
 __device__ __forceinline__ Item decode(const WinParams &p, int item) {
   Item it;
+  it.stop = item < 0;
+  if (it.stop) return it;
   const int slices = p.batch * p.kv_heads, nqb = (p.q_len + kBM - 1) / kBM;
   const int pairs = (nqb * p.group + 1) / 2;
   const int pair = pairs - 1 - item / slices, slice = item % slices;  // the last blocks have the most keys
@@ -119,13 +117,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *drain = o_free + 2, *p_lead = drain + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  const Tickets tickets = tickets_at(
-      reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(tmem_slot) + 64 + 15) & ~uintptr_t(15)));
-  volatile int *info_s = reinterpret_cast<volatile int *>(reinterpret_cast<uint8_t *>(tickets.answer) + kTicketBytes);
+  ItemRing<Item> ring(tmem_slot + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    tickets_init(tickets, 10);  // softmax warps, MMA, clear
+    ring.init(10);  // softmax warps, MMA, clear
     for (int i = 0; i < 3 * C::kSlots; ++i) mbar_init(&bars[i], 1);
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
@@ -156,14 +152,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmap_k);
       tma_prefetch_desc(&tmap_v);
       uint32_t ld = 0, items = 0, raw_par = 0, raw_last = 0;  // per slot: parity of raw, last load went to raw
-      uint32_t asked = 0, taken = 0;
-      bool ok = true;
+      uint32_t n = 0;
       int item = blockIdx.x;
-      for (; item >= 0 && ok; item = ok ? ticket_take(tickets, taken, ok, ctl, kErrWaitProducer) : 0) {
-        if (!ticket_ask(tickets, asked, ctl, kErrWaitProducer)) { ok = false; break; }
-        ++asked;
+      bool ok = true, asked = false;
+      while (true) {
         const Item it = decode(p, item);
-        if (it.nc == 0) continue;
+        if (!ring.put(n, it, ctl, kErrWaitProducer)) { ok = false; break; }
+        if (it.stop) break;
+        ring.ask();
+        asked = true;
+        if (it.nc == 0) {
+          if (!ring.take(n++, item, ctl, kErrWaitProducer)) { ok = false; break; }
+          asked = false;
+          continue;
+        }
         if (!mbar_wait(q_free, (items & 1) ^ 1, ctl, kErrWaitProducer)) { ok = false; break; }
         mbar_arrive_expect_tx(q_full, (it.has[1] ? 2 : 1) * C::kTile);
 #pragma unroll
@@ -183,6 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_tile<D>(slots + slot * C::kTile, (s & 1) ? &tmap_v : &tmap_k, it.s.k0 + first, it.hk, it.s.slice, bar);
           ++ld;
         }
+        if (!ok || !ring.take(n++, item, ctl, kErrWaitProducer)) { ok = false; break; }
+        asked = false;
       }
       if (!ok) {
         // let the copies already issued land before the CTA exits
@@ -193,14 +197,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           else drain_wait(&full[slot], (i / C::kSlots) & 1);
         }
         if (items > 0) drain_wait(q_full, (items - 1) & 1);
-        tickets_discard(tickets, asked, taken, item < 0);
+        if (item >= 0) ring.discard(n, asked);
       }
     }
   } else if (warp == kClearWarp) {
-    uint32_t ld = 0, raw_par = 0, taken = 0;
+    uint32_t ld = 0, raw_par = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item >= 0 && ok; item = ok ? ticket_next(tickets, taken, ok, ctl, kErrWaitProducer, lane) : -1) {
-      const Item it = decode(p, item);
+    for (uint32_t n = 0;; ++n) {
+      const Item *at = ring.get(n, ok, ctl, kErrWaitProducer);
+      if (!at) break;
+      const Item &it = *at;
       for (int j = 0; j < it.nc && ok; ++j) {
         int first, valid;
         it.chunk(j, first, valid);
@@ -212,7 +218,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         clear_rows<D>(slots + slot * C::kTile, valid, (valid + 15) & ~15, lane);
         if (lane == 0) mbar_arrive(&full[slot]);
       }
+      if (!ok) break;
       ld += 2 * it.nc;
+      ring.release(n, lane);
     }
   } else if (warp == kMmaWarp) {
     constexpr uint32_t idesc_qk = idesc_for<T>(kBM, kBM, false, false);
@@ -221,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t qdesc0 = smem_desc_sw128(smem_u32(q_smem), 16, 1024);
     const uint64_t kdesc0 = smem_desc_sw128(slots_addr, 16, 1024);
     const uint64_t vdesc0 = smem_desc_sw128(slots_addr, kTilePanel, 1024);
-    uint32_t ld = 0, items = 0, taken = 0;
+    uint32_t ld = 0, items = 0;
     uint32_t p_waits[2] = {0, 0}, o_waits[2] = {0, 0}, used[2] = {0, 0};
     bool ok = true, issued = false;
     auto mma_s = [&](int x, uint32_t slot) {
@@ -254,9 +262,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       return true;
     };
-    for (int item = blockIdx.x; item >= 0 && ok; item = ok ? ticket_next(tickets, taken, ok, ctl, kErrWaitMma, lane) : -1) {
-      const Item it = decode(p, item);
-      if (it.nc == 0) continue;
+    for (uint32_t n = 0;; ++n) {
+      const Item *at = ring.get(n, ok, ctl, kErrWaitMma);
+      if (!at) break;
+      const Item it = *at;
+      if (it.nc == 0) {
+        ring.release(n, lane);
+        continue;
+      }
       if (!mbar_wait_w(q_full, items & 1, ctl, kErrWaitMma)) { ok = false; break; }
       tc_fence_after();
       ++items;
@@ -275,9 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < it.nc && ok; ++j) {
         const uint32_t vj = k0 + 2 * j + 1, kn = vj + 1;
         const bool more = j + 1 < it.nc;
-        if (!wait_slot(vj) || (more && !wait_slot(kn))) { ok = false; break; }
         const int steps = (valid + 15) / 16;
-        if (more) it.chunk(j + 1, first, valid);
+        it.chunk(j + 1, first, valid);
+        const bool next[2] = {more && sees(it, 0, first, valid, p.sinks), more && sees(it, 1, first, valid, p.sinks)};
+        if (!wait_slot(vj) || (more && !wait_slot(kn))) { ok = false; break; }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (act[x]) {
@@ -294,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!mma_pv(x, vj % C::kSlots, !begun[x], ph, steps)) { ok = false; break; }
             begun[x] = true;
           }
-          act[x] = more && sees(it, x, first, valid, p.sinks);
+          act[x] = next[x];
           if (act[x]) mma_s(x, kn % C::kSlots);
         }
         if (!ok) break;
@@ -302,7 +316,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (more) mma_commit_w(&empty[kn % C::kSlots]);
         if (j + 2 == it.nc) mma_commit_w(q_free);
       }
+      if (!ok) break;
       ld = k0 + 2 * it.nc;
+      ring.release(n, lane);
 #pragma unroll
       for (int x = 0; x < 2; ++x) used[x] += begun[x] ? 1 : 0;
     }
@@ -316,41 +332,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lane_off + 128 * x, o_tm = tmem + lane_off + C::kTmO + x * D;
     const float sl2 = p.scale_log2;
-    uint32_t s_waits = 0, taken = 0;
+    uint32_t s_waits = 0;
     bool ok = true;
-    // What the passes over an item's chunks need of it lies in shared memory,
-    // a copy per warp: beside a row of 128 scores registers are short.
-    volatile int *info = info_s + 16 * warp;
-    enum { kSinkChunks, kChunks, kBase, kLast, kSinkKeys, kLo, kHi, kPos0 };
-    for (int item = blockIdx.x; item >= 0 && ok; item = ok ? ticket_next(tickets, taken, ok, ctl, kErrWaitSoftmax, lane) : -1) {
-      {
-        const Item it = decode(p, item);
-        if (!pick(it.has, x)) continue;
-        __syncwarp();
-        if (lane == 0) {
-          info[kSinkChunks] = it.ns, info[kChunks] = it.nc, info[kBase] = it.base, info[kLast] = it.last;
-          info[kSinkKeys] = it.nsink, info[kLo] = pick(it.lo, x), info[kHi] = pick(it.hi, x), info[kPos0] = pick(it.pos0, x);
-        }
-        __syncwarp();
+    for (uint32_t n = 0;; ++n) {
+      const Item *at = ring.get(n, ok, ctl, kErrWaitSoftmax);
+      if (!at) break;
+      const Item &it = *at;  // stays in shared memory: beside a row of scores registers are short
+      if (!it.has[x]) {
+        ring.release(n, lane);
+        continue;
       }
       float m = -INFINITY, l = 0.f;
       bool seen = false;
-      for (int j = 0; j < info[kChunks]; ++j) {
+      for (int j = 0; j < it.nc; ++j) {
         int first, valid;
-        {
-          const int ns = info[kSinkChunks];
-          first = j < ns ? j * kBM : info[kBase] + (j - ns) * kBM;
-          valid = min(kBM, (j < ns ? info[kSinkKeys] : info[kLast] + 1) - first);
-        }
-        if (!(first <= info[kHi] && (first + valid > info[kLo] || first < p.sinks))) continue;
+        it.chunk(j, first, valid);
+        if (!sees(it, x, first, valid, p.sinks)) continue;
+        // whole: every row of the unit sees all 128 keys
+        const int pos0 = it.pos0[x];
+        const bool whole = valid == kBM && first + kBM - 1 <= pos0 &&
+                           (first > pos0 + kBM - 1 - p.window || first + kBM <= p.sinks);
         if (!mbar_wait_w(&s_full[x], s_waits & 1, ctl, kErrWaitSoftmax)) { ok = false; break; }
         ++s_waits;
         tc_fence_after();
         // O_X holds every chunk before this one: S was issued after their P V
-        // whole: every row of the unit sees all 128 keys
-        const int pos0 = info[kPos0];
-        const bool whole = valid == kBM && first + kBM - 1 <= pos0 &&
-                           (first > pos0 + kBM - 1 - p.window || first + kBM <= p.sinks);
         auto mask = [&](uint32_t(&r)[32], int w) {
           if (whole) return;
           const uint32_t bits = visible_bits(pos0 + row, first, valid, p.window, p.sinks, w);
@@ -365,29 +370,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mloc;
         {
           uint32_t r2[32], r3[32];
-          tmem_ld32(s_tm, r0);
-          tmem_ld32(s_tm + 32, r1);
+          auto top = [](float t, const uint32_t(&r)[32]) {
+            float a = max3(t, __uint_as_float(r[0]), __uint_as_float(r[1])), b = max3(__uint_as_float(r[2]), __uint_as_float(r[3]), __uint_as_float(r[4]));
+#pragma unroll
+            for (int i = 5; i < 29; i += 4) {
+              a = max3(a, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+              b = max3(b, __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+            }
+            a = max3(a, __uint_as_float(r[29]), __uint_as_float(r[30]));
+            return max3(a, b, __uint_as_float(r[31]));
+          };
           tmem_ld32(s_tm + 64, r2);
           tmem_ld32(s_tm + 96, r3);
           tmem_ld_wait();
-          reg_fence32(r0);
-          reg_fence32(r1);
           reg_fence32(r2);
           reg_fence32(r3);
-          mask(r0, 0);
-          mask(r1, 1);
+          tmem_ld32(s_tm, r0);
           mask(r2, 2);
+          float t = top(-INFINITY, r2);
+          tmem_ld32(s_tm + 32, r1);
           mask(r3, 3);
-          float t[4];
-#pragma unroll
-          for (int a = 0; a < 4; ++a) {
-            auto at = [&](int i) { return __uint_as_float(i < 8 ? r0[8 * a + i] : i < 16 ? r1[8 * a + i - 8] : i < 24 ? r2[8 * a + i - 16] : r3[8 * a + i - 24]); };
-            t[a] = max3(at(0), at(1), at(2));
-#pragma unroll
-            for (int i = 3; i < 31; i += 2) t[a] = max3(t[a], at(i), at(i + 1));
-            t[a] = fmaxf(t[a], at(31));
-          }
-          mloc = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * sl2;
+          t = top(t, r3);
+          tmem_ld_wait();
+          reg_fence32(r0);
+          reg_fence32(r1);
+          mask(r0, 0);
+          t = top(t, r0);
+          mask(r1, 1);
+          mloc = top(t, r1) * sl2;
         }
         const bool resc = mloc > m + (kHead<T> + 8.0f);  // also the first finite maximum
         const float m_new = resc ? mloc - kHead<T> : m;
@@ -417,9 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           warp_arrive(&p_lead[x], lane);
         };
         form(r0, 0);
+        form(r1, 1);
         uint32_t r2[32];
         tmem_ld32(s_tm + 64, r2);
-        form(r1, 1);
         if (warp_resc) {
 #pragma unroll 1
           for (int oc = 0; oc < D / 16; ++oc) {
@@ -455,39 +465,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait_w(&pv_done[x], (s_waits - 1) & 1, ctl, kErrWaitEpilogue)) { ok = false; break; }
         tc_fence_after();
       }
-      const Item it = decode(p, item);
-      const int qrow = pick(it.qb, x) * kBM + row;
+      const int qrow = it.qb[x] * kBM + row;
       const bool row_valid = qrow < it.s.nq;
       const bool none = l == 0.f;
       const float inv_l = none ? 0.f : 1.f / l;
-      uint4 *dst = reinterpret_cast<uint4 *>(p.o.p + 2 * ((long long)it.s.slice * p.o.b + (long long)pick(it.h, x) * p.o.h +
-                                                         (long long)(it.s.q0 + qrow) * p.o.r));
+      // the quad's first row, and how many of its rows there are
+      char *dst = p.o.p + 2 * ((long long)it.s.slice * p.o.b + (long long)it.h[x] * p.o.h +
+                               (long long)(it.s.q0 + (qrow & ~3)) * p.o.r);
+      const int quad_rows = it.s.nq - (qrow & ~3);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t r[32];
         if (seen) {
           tmem_ld32(o_tm + c * 32, r);
           tmem_ld_wait();
+          reg_fence32(r);
         }
-        if (row_valid) {
+        uint4 w[4];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = none ? 0u
-                          : Elem<T>::pack(__uint_as_float(r[8 * v + 2 * e]) * inv_l,
-                                          __uint_as_float(r[8 * v + 2 * e + 1]) * inv_l);
-            dst[c * 4 + v] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+        for (int v = 0; v < 4; ++v) {
+          auto pair = [&](int e) {
+            return none ? 0u : Elem<T>::pack(__uint_as_float(r[8 * v + 2 * e]) * inv_l, __uint_as_float(r[8 * v + 2 * e + 1]) * inv_l);
+          };
+          w[v] = make_uint4(pair(0), pair(1), pair(2), pair(3));
         }
+        store_quad(w, dst + 64 * c, 2 * p.o.r, quad_rows, lane);
       }
       if (seen) {
         tc_fence_before();
         warp_arrive(&o_free[x], lane);
       }
       if (row_valid && p.lse)
-        p.lse[stat_row(p, it.s, pick(it.h, x), qrow)] = none ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+        p.lse[stat_row(p, it.s, it.h[x], qrow)] = none ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+      ring.release(n, lane);
     }
   }
 
