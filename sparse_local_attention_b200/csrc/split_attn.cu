@@ -7,12 +7,12 @@
 // (group x q_len of them, kRows per block) are the N side of warp-wide
 // products of 16 keys:
 //   S^T[key][row] = K Q^T,   O^T[d][row] += V^T P^T
-// so that K and V go from global memory straight into the A operand's
-// registers, in an order of d and of the keys under which each lane's 16-byte
-// loads are what it multiplies: nothing is staged in shared memory and no warp
-// waits for another one until the join.  8-bit codes widen to fp16, which holds
-// them all; a 16-key step lies in one scale block, so its scales are two
-// numbers per warp.  The query rows are scaled by a power of two each, so that
+// in an order of d and of the keys under which a lane's 16-byte pieces of K and V
+// are what it multiplies.  Each warp copies its own steps into a ring of its own
+// in shared memory (asynchronous copies, several steps ahead: what is in flight
+// is not held in registers, and hidden keys arrive as zeros), so no warp waits
+// for another one until the join.  8-bit codes widen to fp16, which holds them
+// all; a 16-key step lies in one scale block, so its scales are two numbers.  The query rows are scaled by a power of two each, so that
 // fp16 holds them as well as bf16 did.  Sums, statistics and O are fp32, P is
 // rounded to the operand type.
 #include <cooperative_groups.h>
@@ -29,6 +29,7 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps, kStep = 16;  // keys per step
 // P = 2^(x - m) with m set to the maximum less kHead, and moved when a score
 // exceeds m by kHead + 8: P stays below 2^15 and the smallest fp16 stands for 2^-31.
 constexpr float kHead = 7.f;
+constexpr int kMaxSplits = 16;  // blocks of a cluster
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -70,26 +71,37 @@ template <> struct Code16<STA_TYPE_INT8> {
   }
 };
 
-template <int kWords>
-__device__ __forceinline__ void load_words(uint32_t *dst, const void *src) {
-  if constexpr (kWords == 4) {
-    const uint4 w = __ldg(static_cast<const uint4 *>(src));
-    dst[0] = w.x, dst[1] = w.y, dst[2] = w.z, dst[3] = w.w;
-  } else {
-    const uint2 w = __ldg(static_cast<const uint2 *>(src));
-    dst[0] = w.x, dst[1] = w.y;
-  }
+// 16 (or 4) bytes from global to shared memory, zeros where !there
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
 
 // The keys that some query row of a block sees: others are not read, so that
 // whatever they hold never meets P = 0.
 struct Seen {
   int end, low, sinks;  // below end, and from low on or below sinks
   __device__ __forceinline__ bool operator()(int key) const { return key < end && (key >= low || key < sinks); }
+  // all 16 keys of a step
+  __device__ __forceinline__ bool whole(int k0) const {
+    return k0 + kStep <= end && (k0 >= low || k0 + kStep <= sinks);
+  }
 };
 
-// Lane (g, c) = (lane / 4, lane % 4) holds, of 16 keys: K rows g and g + 8,
+// Lane (g, c) = (lane / 4, lane % 4) multiplies, of 16 keys: K rows g and g + 8,
 // a quarter of d each; V rows 2c, 2c + 1, 2c + 8, 2c + 9, an eighth of d each.
+// A step's rows lie in shared memory with their 16-byte pieces exchanged such
+// that the lanes of one access touch all banks (8-byte rows of V: half of them).
+struct Source {
+  const char *k, *v;  // first key
+  long long k_pitch, v_pitch;
+  const float *k_scale, *v_scale;
+};
 
 // The 8-bit cache.
 template <int D, int kType, class T>
@@ -99,10 +111,7 @@ struct CacheKeys {
   static constexpr bool kScaled = true;
   CacheAttn a;
   int b, hk, nk, nq;
-  struct Raw {
-    uint32_t k[2][D / 16], v[4][D / 32];
-    float ks, vs;
-  };
+  static constexpr int kRowBytes = D;
   __device__ __forceinline__ void open(int slice) {
     b = slice / a.c.kv_heads, hk = slice % a.c.kv_heads, nq = a.q_len;
     nk = min(max(__ldg(a.lengths + b), 0), a.c.table_pages * a.c.page_size);
@@ -114,44 +123,37 @@ struct CacheKeys {
   __device__ __forceinline__ float *lse_at(int h, int i) const {
     return a.lse ? a.lse + ((long long)b * a.heads + h) * a.q_len + i : nullptr;
   }
-  // the page of a step, looked up a step before its loads
-  __device__ __forceinline__ int place(int step) const { return page_of(a.c, b, step * kStep); }
-  __device__ __forceinline__ bool there(int page) const { return page >= 0; }
-  __device__ __forceinline__ void load(Raw &r, int page, int step, const Seen &seen, int g, int c) const {
-    const int k0 = step * kStep, at = k0 % a.c.page_size;
-    const bool here = page >= 0;
-    const long long row = ((long long)page * a.c.kv_heads + hk) * a.c.page_size + at;
-    const long long sc = ((long long)page * a.c.kv_heads + hk) * (a.c.page_size / a.c.block) + at / a.c.block;
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int u = 0; u < D / 64; ++u) {
-        if (here && seen(k0 + g + 8 * x)) load_words<4>(&r.k[x][4 * u], a.c.k + (row + g + 8 * x) * D + 16 * c + 64 * u);
-        else r.k[x][4 * u] = r.k[x][4 * u + 1] = r.k[x][4 * u + 2] = r.k[x][4 * u + 3] = 0u;
-      }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int key = 2 * c + (x & 1) + 8 * (x >> 1);
-      if (here && seen(k0 + key)) load_words<D / 32>(r.v[x], a.c.v + (row + key) * D + D / 8 * g);
-      else
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) r.v[x][j] = 0u;
-    }
-    r.ks = here ? __ldg(a.c.k_scale + sc) : 0.f;
-    r.vs = here ? __ldg(a.c.v_scale + sc) : 0.f;
+  // Where a step's keys lie, looked up a step before their loads.
+  struct Place {
+    int page, at;  // page (-1: absent), first key within it
+  };
+  __device__ __forceinline__ Place place(int step) const {
+    const int per = a.c.page_size / kStep;  // uniform
+    int i = (int)(__int2float_rz(step) * a.page_inv), r = step - i * per;
+    while (r < 0) --i, r += per;
+    while (r >= per) ++i, r -= per;
+    const int page = __ldg(a.c.table + (long long)b * a.c.table_pages + i);
+    return Place{(unsigned)page < (unsigned)a.c.pages ? page : -1, r * kStep};
   }
-  // A operand of the s-th 16 columns of d
-  static __device__ __forceinline__ void k_frag(const Raw &r, int s, uint32_t (&f)[4]) {
-    Code16<kType>::widen(Code16<kType>::prepare(r.k[0][s]), f[0], f[2]);
-    Code16<kType>::widen(Code16<kType>::prepare(r.k[1][s]), f[1], f[3]);
+  __device__ __forceinline__ bool there(const Place &p) const { return p.page >= 0; }
+  __device__ __forceinline__ Source source(const Place &p, int) const {
+    const long long ph = (long long)p.page * a.c.kv_heads + hk, row = (ph * a.c.page_size + p.at) * D;
+    const long long sc = ph * a.blocks + (p.at >> a.block_shift);
+    return Source{reinterpret_cast<const char *>(a.c.k + row), reinterpret_cast<const char *>(a.c.v + row), D, D,
+                  a.c.k_scale + sc, a.c.v_scale + sc};
+  }
+  // A operand of the s-th 16 columns of d, from 64 bytes' pieces of rows g and g + 8
+  static constexpr int kPerPiece = 4;
+  static __device__ __forceinline__ void k_frag(const uint32_t (&w)[2][4], int i, uint32_t (&f)[4]) {
+    Code16<kType>::widen(Code16<kType>::prepare(w[0][i]), f[0], f[2]);
+    Code16<kType>::widen(Code16<kType>::prepare(w[1][i]), f[1], f[3]);
   }
   static __device__ __forceinline__ int k_col(int s, int c) { return 64 * (s / 4) + 16 * c + 4 * (s % 4); }
   // A operand of the t-th 16 rows of V^T
-  static __device__ __forceinline__ void v_frag(const Raw &r, int t, uint32_t (&f)[4]) {
-    const int j = t / 2;
+  static __device__ __forceinline__ void v_frag(const uint32_t (&w)[4][kRowBytes / 32], int t, uint32_t (&f)[4]) {
     const uint32_t sel = t % 2 ? 0x7362 : 0x5140;
-    Code16<kType>::widen(Code16<kType>::prepare(__byte_perm(r.v[0][j], r.v[1][j], sel)), f[0], f[1]);
-    Code16<kType>::widen(Code16<kType>::prepare(__byte_perm(r.v[2][j], r.v[3][j], sel)), f[2], f[3]);
+    Code16<kType>::widen(Code16<kType>::prepare(__byte_perm(w[0][t / 2], w[1][t / 2], sel)), f[0], f[1]);
+    Code16<kType>::widen(Code16<kType>::prepare(__byte_perm(w[2][t / 2], w[3][t / 2], sel)), f[2], f[3]);
   }
   static __device__ __forceinline__ int v_col(int t, int g) { return D / 8 * g + 2 * t; }
 };
@@ -165,9 +167,7 @@ struct RowKeys {
   WinParams p;
   Sequence s;
   int hk, nk, nq;
-  struct Raw {
-    uint32_t k[2][D / 8], v[4][D / 16];
-  };
+  static constexpr int kRowBytes = 2 * D;
   __device__ __forceinline__ void open(int slice) {
     hk = slice % p.kv_heads;
     s = sequence(p, slice / p.kv_heads);
@@ -180,40 +180,50 @@ struct RowKeys {
     return p.o.p + 2 * (s.slice * p.o.b + h * p.o.h + (long long)(s.q0 + i) * p.o.r);
   }
   __device__ __forceinline__ float *lse_at(int h, int i) const { return p.lse ? p.lse + stat_row(p, s, h, i) : nullptr; }
-  __device__ __forceinline__ int place(int) const { return 0; }
-  __device__ __forceinline__ bool there(int) const { return true; }
-  __device__ __forceinline__ void load(Raw &r, int, int step, const Seen &seen, int g, int c) const {
-    const int k0 = step * kStep;
-    const long long row = s.k0 + k0;
-    const char *k = p.k.p + 2 * (s.slice * p.k.b + hk * p.k.h + row * p.k.r);
-    const char *v = p.v.p + 2 * (s.slice * p.v.b + hk * p.v.h + row * p.v.r);
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int u = 0; u < D / 32; ++u) {
-        if (seen(k0 + g + 8 * x)) load_words<4>(&r.k[x][4 * u], k + 2 * (g + 8 * x) * p.k.r + 16 * c + 64 * u);
-        else r.k[x][4 * u] = r.k[x][4 * u + 1] = r.k[x][4 * u + 2] = r.k[x][4 * u + 3] = 0u;
-      }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int key = 2 * c + (x & 1) + 8 * (x >> 1);
-#pragma unroll
-      for (int u = 0; u < D / 64; ++u) {
-        if (seen(k0 + key)) load_words<4>(&r.v[x][4 * u], v + 2 * key * p.v.r + 16 * g + 128 * u);
-        else r.v[x][4 * u] = r.v[x][4 * u + 1] = r.v[x][4 * u + 2] = r.v[x][4 * u + 3] = 0u;
-      }
-    }
+  struct Place {};
+  __device__ __forceinline__ Place place(int) const { return Place{}; }
+  __device__ __forceinline__ bool there(const Place &) const { return true; }
+  __device__ __forceinline__ Source source(const Place &, int step) const {
+    const long long row = s.k0 + step * kStep;
+    return Source{p.k.p + 2 * (s.slice * p.k.b + hk * p.k.h + row * p.k.r), p.v.p + 2 * (s.slice * p.v.b + hk * p.v.h + row * p.v.r),
+                  2 * p.k.r, 2 * p.v.r, nullptr, nullptr};
   }
-  static __device__ __forceinline__ void k_frag(const Raw &r, int s, uint32_t (&f)[4]) {
-    f[0] = r.k[0][2 * s], f[2] = r.k[0][2 * s + 1], f[1] = r.k[1][2 * s], f[3] = r.k[1][2 * s + 1];
+  static constexpr int kPerPiece = 2;
+  static __device__ __forceinline__ void k_frag(const uint32_t (&w)[2][4], int i, uint32_t (&f)[4]) {
+    f[0] = w[0][2 * i], f[2] = w[0][2 * i + 1], f[1] = w[1][2 * i], f[3] = w[1][2 * i + 1];
   }
   static __device__ __forceinline__ int k_col(int s, int c) { return 32 * (s / 2) + 8 * c + 4 * (s % 2); }
-  static __device__ __forceinline__ void v_frag(const Raw &r, int t, uint32_t (&f)[4]) {
-    f[0] = __byte_perm(r.v[0][t], r.v[1][t], 0x5410), f[1] = __byte_perm(r.v[0][t], r.v[1][t], 0x7632);
-    f[2] = __byte_perm(r.v[2][t], r.v[3][t], 0x5410), f[3] = __byte_perm(r.v[2][t], r.v[3][t], 0x7632);
+  static __device__ __forceinline__ void v_frag(const uint32_t (&w)[4][kRowBytes / 32], int t, uint32_t (&f)[4]) {
+    f[0] = __byte_perm(w[0][t], w[1][t], 0x5410), f[1] = __byte_perm(w[0][t], w[1][t], 0x7632);
+    f[2] = __byte_perm(w[2][t], w[3][t], 0x5410), f[3] = __byte_perm(w[2][t], w[3][t], 0x7632);
   }
   static __device__ __forceinline__ int v_col(int t, int g) { return 64 * (t / 4) + 8 * g + 2 * (t % 4); }
 };
+
+template <int D, int NT, class Keys>
+struct SplitCfg {
+  static constexpr int kRows = 8 * NT, kPitch = D + 4;
+  static constexpr int kHalf = kStep * Keys::kRowBytes;  // K (or V) of a step
+  static constexpr int kStage = 2 * kHalf + 16;          // and its two scales
+  // CTAs per SM, and steps of a warp's ring: as many as shared memory holds
+  static constexpr int kCtas = Keys::kRowBytes == 256 || (NT == 2 && D == 128) ? 1 : 2;
+  static constexpr int kStages = (kCtas == 2 ? 100 : 200) * 1024 / (kWarps * kStage) > 6 ? 6 : (kCtas == 2 ? 100 : 200) * 1024 / (kWarps * kStage);
+  static_assert(kStages >= 2, "a step ahead");
+  // the join's sums lie over the rings
+  static constexpr int kSums = kWarps * kRows * kPitch * 4, kRings = kWarps * kStages * kStage;
+  static constexpr int kStats = 4 * kRows * 2 * (kWarps + 1 + kMaxSplits);
+  static constexpr int kSmem = (kSums > kRings ? kSums : kRings) + kStats;
+};
+
+// Where piece `col` (16 bytes) of row `row` lies.
+template <int kRowBytes>
+__device__ __forceinline__ int k_place(int row, int col) {
+  return row * kRowBytes + 16 * (kRowBytes >= 128 ? col ^ ((row & 1) << 2) : col);
+}
+template <int kRowBytes>
+__device__ __forceinline__ int v_place(int row, int col) {
+  return row * kRowBytes + 16 * (kRowBytes >= 128 ? col ^ (row & 6) : col ^ (row & 2));
+}
 
 struct SplitShape {
   int splits, group, window, sinks;
@@ -223,15 +233,17 @@ struct SplitShape {
 // NT groups of 8 query rows.  Grid: (splits x slices, row blocks), a cluster
 // per slice.
 template <int D, int NT, class Keys>
-__global__ void __launch_bounds__(kThreads) split_attn_kernel(const Keys keys_in, const SplitShape shape) {
+__global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas) split_attn_kernel(const Keys keys_in, const SplitShape shape) {
   using T = typename Keys::Io;
   using Op = typename Keys::Op;
-  constexpr int kRows = 8 * NT, kPitch = D + 4;
-  extern __shared__ float smem[];
-  float *o_s = smem;                             // [kWarps][kRows][kPitch]
-  float *m_s = o_s + kWarps * kRows * kPitch;    // [kWarps][kRows]
+  using C = SplitCfg<D, NT, Keys>;
+  constexpr int kRows = C::kRows, kPitch = C::kPitch, kRow = Keys::kRowBytes, kAhead = C::kStages - 1;
+  extern __shared__ __align__(16) float smem[];
+  float *o_s = smem;                             // [kWarps][kRows][kPitch], over the rings
+  float *m_s = reinterpret_cast<float *>(reinterpret_cast<char *>(smem) + (C::kSmem - C::kStats));  // [kWarps][kRows]
   float *l_s = m_s + kWarps * kRows;             // [kWarps][kRows]
   float *cta_m = l_s + kWarps * kRows, *cta_l = cta_m + kRows;
+  float *all_m = cta_l + kRows, *all_l = all_m + kMaxSplits * kRows;  // [splits][kRows]
   Keys keys = keys_in;
   const int rank = blockIdx.x % shape.splits;
   keys.open(blockIdx.x / shape.splits);
@@ -254,6 +266,50 @@ __global__ void __launch_bounds__(kThreads) split_attn_kernel(const Keys keys_in
   const int end = (int)((long long)n_steps * (rank + 1) / shape.splits);
   auto step_of = [&](int i) { return i < sink_steps ? i : base_step + i - sink_steps; };
 
+  float o[NT][D / 16][4], m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
+  }
+
+  char *ring = reinterpret_cast<char *>(smem) + warp * C::kStages * C::kStage;
+  const uint32_t ring_at = smem_u32(ring);
+  uint32_t here_bits = 0;  // stages whose keys are there
+  typename Keys::Place next{};
+  // the copies of the step at i into a stage (a group of them, empty past the end)
+  auto fetch = [&](int i, int stage) {
+    if (i < end) {
+      const int k0 = step_of(i) * kStep;
+      if (keys.there(next)) {
+        const Source src = keys.source(next, step_of(i));
+        const uint32_t at = ring_at + stage * C::kStage;
+        const bool whole = seen.whole(k0);
+#pragma unroll
+        for (int j = 0; j < kStep * kRow / 512; ++j) {
+          const int piece = lane + 32 * j, row = piece / (kRow / 16), col = piece % (kRow / 16);
+          const bool there = whole || seen(k0 + row);
+          // a row that is not there is not addressed either
+          copy16(at + k_place<kRow>(row, col), there ? src.k + row * src.k_pitch + 16 * col : src.k, there);
+          copy16(at + C::kHalf + v_place<kRow>(row, col), there ? src.v + row * src.v_pitch + 16 * col : src.v, there);
+        }
+        if (Keys::kScaled && lane < 2) copy4(at + 2 * C::kHalf + 4 * lane, lane ? src.v_scale : src.k_scale);
+        here_bits |= 1u << stage;
+      } else {
+        here_bits &= ~(1u << stage);
+      }
+      if (i + kWarps < end) next = keys.place(step_of(i + kWarps));
+    }
+    copies_commit();
+  };
+  int i = begin + warp, ahead = i, stage = 0, into = 0;
+  if (i < end) next = keys.place(step_of(i));
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) {
+    fetch(ahead, into++);
+    ahead += kWarps;
+  }
   // Q as the B operand: lane (g, c) holds row g, columns k_col(s, c) .. + 3
   uint32_t qf[NT][D / 16][2];
   float fac[NT][2];  // of this lane's score columns 2c, 2c + 1
@@ -300,42 +356,42 @@ __global__ void __launch_bounds__(kThreads) split_attn_kernel(const Keys keys_in
     }
   }
 
-  float o[NT][D / 16][4], m[NT][2], l[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-    for (int t = 0; t < D / 16; ++t) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
-  }
-
-  typename Keys::Raw cur, next;
-  int i = begin + warp, page = 0, page_next = 0;
-  if (i < end) {
-    page = keys.place(step_of(i));
-    keys.load(cur, page, step_of(i), seen, g, c);
-    if (i + kWarps < end) page_next = keys.place(step_of(i + kWarps));
-  }
   for (; i < end; i += kWarps) {
     const int step = step_of(i);
-    const bool here = keys.there(page);
-    if (i + kWarps < end) {
-      keys.load(next, page_next, step_of(i + kWarps), seen, g, c);
-      page = page_next;
-      if (i + 2 * kWarps < end) page_next = keys.place(step_of(i + 2 * kWarps));
-    }
+    fetch(ahead, into);  // into the stage read last
+    ahead += kWarps;
+    into = into + 1 == C::kStages ? 0 : into + 1;
+    copies_wait<kAhead>();
+    __syncwarp();
+    const bool here = here_bits >> stage & 1;
+    const char *k_s = ring + stage * C::kStage, *v_s = k_s + C::kHalf;
+    stage = stage + 1 == C::kStages ? 0 : stage + 1;
     if (here) {
       float x[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s) {
-        uint32_t a[4];
-        Keys::k_frag(cur, s, a);
+      for (int u = 0; u < kRow / 64; ++u) {
+        uint32_t w[2][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(x[nt], a, qf[nt][s][0], qf[nt][s][1], Op{});
+        for (int y = 0; y < 2; ++y) {
+          const uint4 q = *reinterpret_cast<const uint4 *>(k_s + k_place<kRow>(g + 8 * y, c + 4 * u));
+          w[y][0] = q.x, w[y][1] = q.y, w[y][2] = q.z, w[y][3] = q.w;
+        }
+#pragma unroll
+        for (int j = 0; j < Keys::kPerPiece; ++j) {
+          uint32_t a[4];
+          Keys::k_frag(w, j, a);
+          const int s = u * Keys::kPerPiece + j;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(x[nt], a, qf[nt][s][0], qf[nt][s][1], Op{});
+        }
       }
-      float ks = 1.f;
-      if constexpr (Keys::kScaled) ks = cur.ks;
+      float ks = 1.f, vs = 1.f;
+      if constexpr (Keys::kScaled) {
+        const float2 f = *reinterpret_cast<const float2 *>(k_s + 2 * C::kHalf);
+        ks = f.x, vs = f.y;
+      }
       // whole: every row sees the 16 keys (rows that are not there are not read)
       const int k0 = step * kStep;
       const bool whole = k0 + kStep - 1 <= first_pos && k0 + kStep <= keys.nk &&
@@ -381,25 +437,42 @@ __global__ void __launch_bounds__(kThreads) split_attn_kernel(const Keys keys_in
         pb[nt][0] = transpose8(Elem<Op>::pack(x[nt][0], x[nt][1]));
         pb[nt][1] = transpose8(Elem<Op>::pack(x[nt][2], x[nt][3]));
       }
+      uint32_t w[4][kRow / 32];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int row = 2 * c + (y & 1) + 8 * (y >> 1);
+        if constexpr (kRow == 64) {
+          const uint2 q = *reinterpret_cast<const uint2 *>(v_s + v_place<kRow>(row, g / 2) + 8 * (g & 1));
+          w[y][0] = q.x, w[y][1] = q.y;
+        } else {
+#pragma unroll
+          for (int u = 0; u < kRow / 128; ++u) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(v_s + v_place<kRow>(row, g + 8 * u));
+            w[y][4 * u] = q.x, w[y][4 * u + 1] = q.y, w[y][4 * u + 2] = q.z, w[y][4 * u + 3] = q.w;
+          }
+        }
+      }
 #pragma unroll
       for (int t = 0; t < D / 16; ++t) {
         uint32_t a[4];
-        Keys::v_frag(cur, t, a);
+        Keys::v_frag(w, t, a);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           if constexpr (Keys::kScaled) {
             float y[4] = {0.f, 0.f, 0.f, 0.f};
             mma16816(y, a, pb[nt][0], pb[nt][1], Op{});
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][t][e] = fmaf(y[e], cur.vs, o[nt][t][e]);
+            for (int e = 0; e < 4; ++e) o[nt][t][e] = fmaf(y[e], vs, o[nt][t][e]);
           } else {
             mma16816(o[nt][t], a, pb[nt][0], pb[nt][1], Op{});
           }
         }
       }
     }
-    cur = next;
+    __syncwarp();  // the stage may be copied over
   }
+  copies_wait<0>();
+  __syncthreads();  // the sums take the rings' place
 
   // join the warps
 #pragma unroll
@@ -447,21 +520,30 @@ __global__ void __launch_bounds__(kThreads) split_attn_kernel(const Keys keys_in
     }
     *at = sum;
   }
-  // join the cluster: each block finishes its share of the columns
+  // join the cluster: each block finishes its share of the columns, with every
+  // block's statistics copied first
   cg::cluster_group cluster = cg::this_cluster();
-  if (shape.splits > 1) cluster.sync();
-  else __syncthreads();
-  for (int q = threadIdx.x + rank * kThreads; q < kQuads; q += shape.splits * kThreads) {
+  const int splits = shape.splits;
+  if (splits > 1) {
+    cluster.sync();
+    for (int x = threadIdx.x; x < kRows * splits; x += kThreads) {
+      all_m[x] = *cluster.map_shared_rank(&cta_m[x % kRows], x / kRows);
+      all_l[x] = *cluster.map_shared_rank(&cta_l[x % kRows], x / kRows);
+    }
+  }
+  __syncthreads();
+  for (int q = threadIdx.x * splits + rank; q < kQuads; q += splits * kThreads) {
     const int r = q / (D / 4), col = q % (D / 4) * 4;
     if (r >= rows) continue;
     float top = -INFINITY, sum = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (shape.splits > 1) {
-      for (int s = 0; s < shape.splits; ++s) top = fmaxf(top, *cluster.map_shared_rank(&cta_m[r], s));
-      for (int s = 0; s < shape.splits; ++s) {
-        const float f = weight(*cluster.map_shared_rank(&cta_m[r], s), top);
-        sum += *cluster.map_shared_rank(&cta_l[r], s) * f;
-        const float4 z = *reinterpret_cast<float4 *>(cluster.map_shared_rank(&o_s[r * kPitch + col], s));
+    if (splits > 1) {
+      for (int x = 0; x < splits; ++x) top = fmaxf(top, all_m[x * kRows + r]);
+#pragma unroll 4
+      for (int x = 0; x < splits; ++x) {
+        const float f = weight(all_m[x * kRows + r], top);
+        const float4 z = *reinterpret_cast<float4 *>(cluster.map_shared_rank(&o_s[r * kPitch + col], x));
+        sum = fmaf(all_l[x * kRows + r], f, sum);
         y.x = fmaf(z.x, f, y.x), y.y = fmaf(z.y, f, y.y), y.z = fmaf(z.z, f, y.z), y.w = fmaf(z.w, f, y.w);
       }
     } else {
@@ -476,18 +558,19 @@ __global__ void __launch_bounds__(kThreads) split_attn_kernel(const Keys keys_in
     if (col == 0)
       if (float *lse = keys.lse_at(h, qi)) *lse = none ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994530942f;
   }
-  if (shape.splits > 1) cluster.sync();  // no block leaves while others read its part
+  if (splits > 1) cluster.sync();  // no block leaves while others read its part
 }
 
-constexpr size_t split_smem(int d, int nt) {
-  return sizeof(float) * (kWarps * 8 * nt * (d + 4) + 2 * kWarps * 8 * nt + 2 * 8 * nt);
-}
-
-// Blocks per slice: enough for two per SM, but at least two steps for each warp.
-int splits_for(long long units, long long most_keys) {
-  const long long steps = (most_keys + kStep - 1) / kStep;
+// Blocks per slice (units: slices and row blocks).  As many as fill the GPU
+// once, with a step for each warp; beyond that, while sequences of uneven
+// length would leave SMs idle at the end, up to three times the GPU, with 16
+// steps for each warp.
+int splits_for(long long units, long long most_keys, int ctas) {
+  const long long steps = (most_keys + kStep - 1) / kStep, room = 148ll * ctas;
   int s = 1;
-  while (s < 16 && units * s < 2 * 148 && steps >= 2ll * s * kWarps * 2) s *= 2;
+  while (s < kMaxSplits && ((units * 2 * s <= room && steps >= 2ll * s * kWarps) ||
+                            (units * s < 3 * room && steps >= 2ll * s * kWarps * 16)))
+    s *= 2;
   return s;
 }
 
@@ -495,8 +578,8 @@ template <int D, int NT, class Keys>
 cudaError_t launch(const Keys &keys, SplitShape shape, long long slices, int rows, long long most_keys, cudaStream_t stream) {
   auto *kernel = split_attn_kernel<D, NT, Keys>;
   const int blocks = (rows + 8 * NT - 1) / (8 * NT);
-  shape.splits = splits_for(slices * blocks, most_keys);
-  const size_t smem = split_smem(D, NT);
+  shape.splits = splits_for(slices * blocks, most_keys, SplitCfg<D, NT, Keys>::kCtas);
+  constexpr size_t smem = SplitCfg<D, NT, Keys>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
