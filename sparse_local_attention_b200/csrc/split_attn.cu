@@ -29,6 +29,9 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps, kStep = 16;  // keys per step
 // P = 2^(x - m) with m set to the maximum less kHead, and moved when a score
 // exceeds m by kHead + 8: P stays below 2^15 and the smallest fp16 stands for 2^-31.
 constexpr float kHead = 7.f;
+// m of a row without a key so far, far below any score
+constexpr float kNoMax = -1e30f;
+constexpr float kLeastScale = 1.1754943508222875e-38f;  // 2^-126
 constexpr int kMaxSplits = 16;  // blocks of a cluster
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
@@ -267,9 +270,10 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas) split_
   auto step_of = [&](int i) { return i < sink_steps ? i : base_step + i - sink_steps; };
 
   float o[NT][D / 16][4], m[NT][2], l[NT][2];
+  float v_top = kLeastScale, v_inv = 1.f / kLeastScale;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+    m[nt][0] = m[nt][1] = kNoMax, l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
     for (int t = 0; t < D / 16; ++t) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
   }
@@ -285,14 +289,24 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas) split_
       if (keys.there(next)) {
         const Source src = keys.source(next, step_of(i));
         const uint32_t at = ring_at + stage * C::kStage;
-        const bool whole = seen.whole(k0);
+        // a lane's pieces: kRow / 16 to a row, kPass rows apart
+        constexpr int kPieces = kRow / 16, kPass = 32 / kPieces;
+        const int row0 = lane / kPieces, col = lane % kPieces;
+        const char *k = src.k + row0 * src.k_pitch + 16 * col, *v = src.v + row0 * src.v_pitch + 16 * col;
+        if (seen.whole(k0)) {
 #pragma unroll
-        for (int j = 0; j < kStep * kRow / 512; ++j) {
-          const int piece = lane + 32 * j, row = piece / (kRow / 16), col = piece % (kRow / 16);
-          const bool there = whole || seen(k0 + row);
-          // a row that is not there is not addressed either
-          copy16(at + k_place<kRow>(row, col), there ? src.k + row * src.k_pitch + 16 * col : src.k, there);
-          copy16(at + C::kHalf + v_place<kRow>(row, col), there ? src.v + row * src.v_pitch + 16 * col : src.v, there);
+          for (int j = 0; j < kStep / kPass; ++j) {
+            copy16(at + k_place<kRow>(row0 + kPass * j, col), k + kPass * j * src.k_pitch, true);
+            copy16(at + C::kHalf + v_place<kRow>(row0 + kPass * j, col), v + kPass * j * src.v_pitch, true);
+          }
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < kStep / kPass; ++j) {
+            const bool there = seen(k0 + row0 + kPass * j);
+            // a row that is not there is not addressed either
+            copy16(at + k_place<kRow>(row0 + kPass * j, col), there ? k + kPass * j * src.k_pitch : src.k, there);
+            copy16(at + C::kHalf + v_place<kRow>(row0 + kPass * j, col), there ? v + kPass * j * src.v_pitch : src.v, there);
+          }
         }
         if (Keys::kScaled && lane < 2) copy4(at + 2 * C::kHalf + 4 * lane, lane ? src.v_scale : src.k_scale);
         here_bits |= 1u << stage;
@@ -398,16 +412,18 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas) split_
                          (k0 > last_pos - shape.window || k0 + kStep <= shape.sinks);
       bool grows = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        const float f[2] = {fac[nt][0] * ks, fac[nt][1] * ks};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[nt][e] *= fac[nt][e & 1] * ks;
+          x[nt][e] *= f[e & 1];
           if (!whole) {
             const int key = k0 + g + 8 * (e >> 1);
             if (key >= keys.nk || !visible(pos[nt][e & 1], key, shape.window, shape.sinks)) x[nt][e] = -INFINITY;
           }
           grows = grows || x[nt][e] > m[nt][e & 1] + (kHead + 8.f);
         }
+      }
       if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -418,21 +434,38 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas) split_
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
             top = fmaxf(top - kHead, m[nt][e]);
-            const float alpha = top == m[nt][e] ? 1.f : ex2_approx(m[nt][e] - top);
+            const float alpha = ex2_approx(m[nt][e] - top);
             m[nt][e] = top;
             l[nt][e] *= alpha;
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) o[nt][t][e] *= alpha, o[nt][t][2 + e] *= alpha;
           }
       }
+      float pv = 1.f;
+      if constexpr (Keys::kScaled) {
+        // O is held over v_top, the largest scale of values so far (a power of
+        // two), and P takes the step's own scale over it: at most 1
+        if (vs > v_top) {
+          const float top = __int_as_float(min((__float_as_int(vs) >> 23) + 1, 254) << 23);
+          const float down = v_top * (1.f / top);
+          v_top = top, v_inv = 1.f / top;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][t][e] *= down;
+        }
+        pv = vs * v_inv;
+      }
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float mm = m[nt][e & 1];
-          x[nt][e] = ex2_approx(x[nt][e] - (mm == -INFINITY ? 0.f : mm));
+          x[nt][e] = ex2_approx(x[nt][e] - m[nt][e & 1]);
           l[nt][e & 1] += x[nt][e];
+          if constexpr (Keys::kScaled) x[nt][e] *= pv;
         }
         pb[nt][0] = transpose8(Elem<Op>::pack(x[nt][0], x[nt][1]));
         pb[nt][1] = transpose8(Elem<Op>::pack(x[nt][2], x[nt][3]));
@@ -457,16 +490,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas) split_
         uint32_t a[4];
         Keys::v_frag(w, t, a);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (Keys::kScaled) {
-            float y[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(y, a, pb[nt][0], pb[nt][1], Op{});
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][t][e] = fmaf(y[e], vs, o[nt][t][e]);
-          } else {
-            mma16816(o[nt][t], a, pb[nt][0], pb[nt][1], Op{});
-          }
-        }
+        for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][t], a, pb[nt][0], pb[nt][1], Op{});
       }
     }
     __syncwarp();  // the stage may be copied over
@@ -487,16 +511,17 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas) split_
       }
     }
   __syncthreads();
-  auto weight = [](float part, float top) { return part == -INFINITY ? 0.f : ex2_approx(part - top); };
+  auto weight = [](float part, float top) { return ex2_approx(part - top); };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 8 * nt + 2 * c + e;
-      float top = -INFINITY;
+      float top = kNoMax;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w * kRows + r]);
-      const float f = weight(m[nt][e], top);
+      float f = weight(m[nt][e], top);
+      if constexpr (Keys::kScaled) f *= v_top;
 #pragma unroll
       for (int t = 0; t < D / 16; ++t)
         *reinterpret_cast<float2 *>(&o_s[(warp * kRows + r) * kPitch + Keys::v_col(t, g)]) =
@@ -535,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas) split_
   for (int q = threadIdx.x * splits + rank; q < kQuads; q += splits * kThreads) {
     const int r = q / (D / 4), col = q % (D / 4) * 4;
     if (r >= rows) continue;
-    float top = -INFINITY, sum = 0.f;
+    float top = kNoMax, sum = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     if (splits > 1) {
       for (int x = 0; x < splits; ++x) top = fmaxf(top, all_m[x * kRows + r]);
