@@ -373,7 +373,9 @@ sta_status sta_cache_write(const sta_cache *cache, int32_t batch, int32_t rows, 
 
 /* Read tokens back: rows [0, count[b]) of k and v (type out_type) receive the
  * values of tokens start[b], start[b] + 1, ... of sequence b, rounded to
- * nearest.  Rows past count[b], and of absent pages, are not written. */
+ * nearest.  Rows past count[b], and of absent pages, are not written, or
+ * written as zeros with STA_READ_ZERO in flags. */
+#define STA_READ_ZERO 0x2u
 sta_status sta_cache_read(const sta_cache *cache, int32_t batch, int32_t rows, const sta_rows *k, const sta_rows *v,
                           int32_t out_type, const int32_t *page_table, int32_t table_pages, const int32_t *start,
                           const int32_t *count, void *stream, uint32_t flags);

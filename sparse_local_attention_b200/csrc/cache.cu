@@ -131,21 +131,27 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheMove m) {
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   const long long row = i / kPer;
   const int part = (int)(i % kPer), start = __ldg(m.start + b);
-  if (start < 0 || row >= clamp_count(m, b)) return;
-  if (start + row >= (long long)c.table_pages * c.page_size) return;
-  const int pos = start + (int)row, page = page_of(c, b, pos);
-  if (page < 0) return;
-  const int in_page = pos % c.page_size;
-  const long long ph = (long long)page * c.kv_heads + h;
-  const uint4 w = *reinterpret_cast<const uint4 *>((is_v ? c.v : c.k) + (ph * c.page_size + in_page) * D + 16 * part);
-  const float s = (is_v ? c.v_scale : c.k_scale)[ph * (c.page_size / c.block) + in_page / c.block];
-  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-  uint32_t out[8];
+  if (row >= m.rows) return;
+  int page = -1, pos = 0;
+  if (start >= 0 && row < clamp_count(m, b) && start + row < (long long)c.table_pages * c.page_size) {
+    pos = start + (int)row;
+    page = page_of(c, b, pos);
+  }
+  uint32_t out[8] = {};
+  if (page >= 0) {
+    const int in_page = pos % c.page_size;
+    const long long ph = (long long)page * c.kv_heads + h;
+    const uint4 w = *reinterpret_cast<const uint4 *>((is_v ? c.v : c.k) + (ph * c.page_size + in_page) * D + 16 * part);
+    const float s = (is_v ? c.v_scale : c.k_scale)[ph * (c.page_size / c.block) + in_page / c.block];
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = Code<kType>::unpack(in[e] & 0xffffu), g = Code<kType>::unpack(in[e] >> 16);
-    out[2 * e] = Elem<T>::pack(f.x * s, f.y * s);
-    out[2 * e + 1] = Elem<T>::pack(g.x * s, g.y * s);
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = Code<kType>::unpack(in[e] & 0xffffu), g = Code<kType>::unpack(in[e] >> 16);
+      out[2 * e] = Elem<T>::pack(f.x * s, f.y * s);
+      out[2 * e + 1] = Elem<T>::pack(g.x * s, g.y * s);
+    }
+  } else if (!m.zero) {
+    return;
   }
   const Rows &x = is_v ? m.v : m.k;
   uint4 *dst = reinterpret_cast<uint4 *>(x.p + 2 * ((long long)b * x.b + (long long)h * x.h + row * x.r + 16 * part));

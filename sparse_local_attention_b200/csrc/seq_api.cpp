@@ -225,13 +225,14 @@ sta_status move_call(bool write, const sta_cache *c, int32_t batch, int32_t rows
   if (const sta_status st = check_cache(c, batch, table_pages)) return st;
   if (rows < 0 || (long long)batch * c->kv_heads * rows >= kMaxRows) return STA_ERR_SHAPE;
   if (!io_type_ok(type)) return STA_ERR_UNSUPPORTED;
-  if (flags & ~STA_CALL_CHECK) return STA_ERR_INVALID_ARG;
+  if (flags & ~(STA_CALL_CHECK | (write ? 0u : STA_READ_ZERO))) return STA_ERR_INVALID_ARG;
   if (const sta_status st = check_cache_pointers(c, table, start)) return st;
   if (const sta_status st = check_rows(k, batch, c->kv_heads, rows)) return st;
   if (const sta_status st = check_rows(v, batch, c->kv_heads, rows)) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (rows > 0) {
-    const sta::CacheMove m{cache_params(c, table, table_pages), batch, rows, rows_of(k), rows_of(v), start, count};
+    const sta::CacheMove m{cache_params(c, table, table_pages), batch, rows, rows_of(k), rows_of(v), start, count,
+                           (flags & STA_READ_ZERO) != 0};
     const cudaError_t e = write ? sta::launch_cache_write(m, c->type, type, stream)
                                 : sta::launch_cache_read(m, c->type, type, stream);
     if (e != cudaSuccess) return STA_ERR_CUDA;

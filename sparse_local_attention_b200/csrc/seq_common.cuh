@@ -5,11 +5,26 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <atomic>
 #include <cstdint>
 
 #include "seq_kernels.h"
 
 namespace sta {
+
+// Raise a kernel's limit of dynamic shared memory, once per device.  `done` is
+// the caller's record of the devices it has been raised on.
+template <class Kernel>
+cudaError_t allow_shared(Kernel *kernel, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // fp32 <-> the 16-bit types, two at a time; lo in bits 0..15.
 template <class T> struct Elem;

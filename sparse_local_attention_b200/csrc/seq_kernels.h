@@ -59,6 +59,7 @@ struct CacheMove {
   int batch, rows;
   Rows k, v;
   const int32_t *start, *count;
+  bool zero;  // reading: rows without a token become zeros
 };
 
 cudaError_t launch_cache_write(const CacheMove &m, int cache_type, int io_type, cudaStream_t stream);

@@ -599,15 +599,29 @@ int splits_for(long long units, long long most_keys, int ctas) {
   return s;
 }
 
+// Clusters of 16 blocks, once per device.
+template <class Kernel>
+cudaError_t allow_wide_clusters(Kernel *kernel, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 template <int D, int NT, class Keys>
 cudaError_t launch(const Keys &keys, SplitShape shape, long long slices, int rows, long long most_keys, cudaStream_t stream) {
   auto *kernel = split_attn_kernel<D, NT, Keys>;
   const int blocks = (rows + 8 * NT - 1) / (8 * NT);
   shape.splits = splits_for(slices * blocks, most_keys, SplitCfg<D, NT, Keys>::kCtas);
   constexpr size_t smem = SplitCfg<D, NT, Keys>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> done{0}, wide{0};
+  if (const cudaError_t e = allow_shared(kernel, (int)smem, done)) return e;
+  if (shape.splits > 8)
+    if (const cudaError_t e = allow_wide_clusters(kernel, wide)) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(slices * shape.splits), blocks), cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem, cfg.stream = stream;

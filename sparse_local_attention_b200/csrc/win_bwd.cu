@@ -964,10 +964,9 @@ template <int D, class T>
 cudaError_t launch(const WinParams &p, const CUtensorMap *m, int num_sms, cudaStream_t stream) {
   using K = DkvCfg<D>;
   using Q = DqCfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(window_dkdv_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)K::kSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(window_dq_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Q::kSmem);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> done_kv{0}, done_q{0};
+  if (const cudaError_t e = allow_shared(window_dkdv_kernel<D, T>, (int)K::kSmem, done_kv)) return e;
+  if (const cudaError_t e = allow_shared(window_dq_kernel<D, T>, (int)Q::kSmem, done_q)) return e;
   const int nqb = (p.q_len + kBM - 1) / kBM, nkb = (p.kv_len + kBM - 1) / kBM, slices = p.batch * p.kv_heads;
   if (nqb > 0) window_pre_kernel<D, T><<<dim3(nqb, p.heads, p.batch), 256, 0, stream>>>(p);
   const int kv_items = (p.sink_blocks * p.sink_segs + (nkb - p.sink_blocks) * p.norm_segs) * slices;

@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, class T>
 cudaError_t launch(const WinParams &p, const CUtensorMap *maps, cudaStream_t stream) {
   using C = Cfg<D>;
-  const cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> done{0};
+  if (const cudaError_t e = allow_shared(window_fwd_kernel<D, T>, (int)C::kSmem, done)) return e;
   const long long nqb = (p.q_len + kBM - 1) / kBM;
   const long long items = (nqb * p.group + 1) / 2 * p.batch * p.kv_heads;
   window_fwd_kernel<D, T><<<(unsigned)items, kThreads, C::kSmem, stream>>>(maps[0], maps[1], maps[2], p);

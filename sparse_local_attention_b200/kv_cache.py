@@ -10,10 +10,11 @@ from typing import Optional
 
 import torch
 
-from .sta import STA_CALL_CHECK, _check, _ptr, lib
-from .window import (IO_TYPES, STA_TYPE_E4M3, STA_TYPE_INT8, _current_stream, _flat, _in_place, _input, _on, _output,
-                     _rows)
+from .sta import STA_CALL_CHECK, _check, lib
+from .window import (IO_TYPES, STA_TYPE_E4M3, STA_TYPE_INT8, _at, _current_stream, _flat, _in_place, _input, _on,
+                     _output, _rows)
 
+STA_READ_ZERO = 0x2
 CACHE_TYPES = {torch.float8_e4m3fn: STA_TYPE_E4M3, torch.int8: STA_TYPE_INT8}
 
 
@@ -65,14 +66,15 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, kv_heads, page_size, head_dim
         self.block, self.dtype, self.device = page_size // blocks, k.dtype, k.device
-        self._c = _Cache(pages, kv_heads, page_size, self.block, head_dim, CACHE_TYPES[k.dtype], *(t.data_ptr() for t in (k, v, k_scale, v_scale)))
+        self._c = _Cache(pages, kv_heads, page_size, self.block, head_dim, CACHE_TYPES[k.dtype],
+                         *(t.data_ptr() for t in (k, v, k_scale, v_scale)))
 
     def _table(self, page_table, batch):
         if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
             raise ValueError("page_table: expected int32 [batch, table_pages]")
         return _flat(page_table, "page_table", (batch, page_table.shape[1]), torch.int32, self.device)
 
-    def _move(self, call, k, v, page_table, start, count, check):
+    def _move(self, call, k, v, page_table, start, count, flags):
         batch, _, rows, _ = k.shape
         self._table(page_table, batch)
         _flat(start, "start", (batch,), torch.int32, self.device)
@@ -81,8 +83,8 @@ class KVCache:
             raise ValueError("start: expected int32 [batch]")
         if batch and rows:
             st = getattr(lib(), call)(ctypes.byref(self._c), batch, rows, _rows(k), _rows(v), IO_TYPES[k.dtype],
-                                      _ptr(page_table), page_table.shape[1], _ptr(start), _ptr(count),
-                                      _current_stream(self.device), STA_CALL_CHECK if check else 0)
+                                      _at(page_table), page_table.shape[1], _at(start), _at(count),
+                                      _current_stream(self.device), flags)
             _check(st, call)
 
     def write(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, start: torch.Tensor,
@@ -99,7 +101,7 @@ class KVCache:
         with _on(self.device, stream):
             k = _input(k, "k", shape, k.dtype, self.device)
             v = _input(v, "v", shape, k.dtype, self.device)
-            self._move("sta_cache_write", k, v, page_table, start, count, check)
+            self._move("sta_cache_write", k, v, page_table, start, count, STA_CALL_CHECK if check else 0)
 
     def read(self, page_table: torch.Tensor, start: torch.Tensor, count: Optional[torch.Tensor], rows: int,
              dtype: torch.dtype = torch.bfloat16, k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
@@ -114,9 +116,11 @@ class KVCache:
             raise ValueError("page_table: expected int32 [batch, table_pages]")
         shape = (page_table.shape[0], self.kv_heads, int(rows), self.head_dim)
         with _on(self.device, stream):
-            k, v = (torch.zeros(shape, dtype=dtype, device=self.device) if t is None
+            flags = (STA_CALL_CHECK if check else 0) | (STA_READ_ZERO if k is None and v is None else 0)
+            new = torch.empty if flags & STA_READ_ZERO else torch.zeros
+            k, v = (new(shape, dtype=dtype, device=self.device) if t is None
                     else _output(t, name, shape, dtype, self.device) for t, name in ((k, "k"), (v, "v")))
-            self._move("sta_cache_read", k, v, page_table, start, count, check)
+            self._move("sta_cache_read", k, v, page_table, start, count, flags)
         return k, v
 
     def attention(self, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor, window: int = 0,
@@ -147,8 +151,8 @@ class KVCache:
             _flat(lse, "lse", shape[:3], torch.float32, self.device)
             if batch and nq:
                 st = lib().sta_cache_attention(ctypes.byref(self._c), batch, heads, nq, int(window), int(sinks),
-                                               float(scale), IO_TYPES[q.dtype], _rows(q), _rows(o), _ptr(lse),
-                                               _ptr(page_table), page_table.shape[1], _ptr(lengths),
+                                               float(scale), IO_TYPES[q.dtype], _rows(q), _rows(o), _at(lse),
+                                               _at(page_table), page_table.shape[1], _at(lengths),
                                                _current_stream(self.device),
                                                STA_CALL_CHECK if check else 0)
                 _check(st, "sta_cache_attention")

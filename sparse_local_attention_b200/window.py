@@ -16,7 +16,7 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from .sta import STA_CALL_CHECK, _check, _ptr, _Rows, lib
+from .sta import STA_CALL_CHECK, _check, _Rows, lib
 
 STA_TYPE_BF16, STA_TYPE_FP16, STA_TYPE_E4M3, STA_TYPE_INT8 = 0, 1, 2, 3
 IO_TYPES = {torch.bfloat16: STA_TYPE_BF16, torch.float16: STA_TYPE_FP16}
@@ -36,16 +36,19 @@ def _in_place(t: torch.Tensor) -> bool:
     """Whether the kernels can address the tensor's rows where they are:
     contiguous rows, 16-byte aligned, at positive strides that are multiples
     of 8 elements (a stride of an extent of one is not used)."""
-    if t.stride(3) != 1 or t.data_ptr() % 16:
+    b, h, r, e = t.stride()
+    if e != 1 or t.data_ptr() & 15:
         return False
-    return all(n <= 1 or (s > 0 and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()[:3]))
+    if b > 0 and h > 0 and r > 0 and not (b | h | r) & 7:
+        return True
+    return all(n <= 1 or (s > 0 and s % 8 == 0) for n, s in zip(t.shape, (b, h, r)))
 
 
 def _input(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
     """An input of [batch, heads, rows, d]: read in place if its strides allow it, else copied."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_cuda:
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on {device}, got {t.dtype} {tuple(t.shape)} on "
                          f"{t.device}")
     return t if _in_place(t) else t.clone(memory_format=torch.contiguous_format)
@@ -63,7 +66,7 @@ def _flat(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> Optiona
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t
@@ -86,13 +89,20 @@ def _switched(device, stream):
 def _on(device, stream):
     """Context of a call: the tensors' device is current, and so is `stream` if
     one is given, so that what the call allocates belongs to it."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
+    if stream is None and torch._C._cuda_getDevice() == device.index:
+        return _HERE
     return _switched(device, stream)
 
 
-def _current_stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+_HERE = contextlib.nullcontext()
+
+
+def _current_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _scratch(workspace: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
@@ -103,12 +113,10 @@ def _scratch(workspace: Optional[torch.Tensor], nbytes: int, device) -> torch.Te
     return workspace
 
 
-def _new(like: torch.Tensor, packed: bool) -> torch.Tensor:
-    """An output laid out as `like`; packed: zero, since rows outside every sequence are not written."""
+def _new(like: torch.Tensor) -> torch.Tensor:
+    """An output laid out as `like`."""
     t = torch.empty_like(like)
-    if not _in_place(t):
-        t = torch.empty_like(like, memory_format=torch.contiguous_format)
-    return t.zero_() if packed else t
+    return t if _in_place(t) else torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 @functools.lru_cache(maxsize=256)
@@ -161,7 +169,9 @@ class _Call:
 
 def _forward(c: _Call, o=None, lse=None, workspace=None, check=False, want_lse=True):
     if o is None:
-        o = _new(c.q, c.packed)
+        o = _new(c.q)
+        if c.packed:  # rows outside every sequence are not written
+            o.zero_()
     else:
         _output(o, "o", c.q_shape, c.dtype, c.device)
     if lse is None and want_lse:
@@ -176,8 +186,8 @@ def _forward(c: _Call, o=None, lse=None, workspace=None, check=False, want_lse=T
                 lse.fill_(float("-inf"))
             return o, lse
         ws = _scratch(workspace, c.fwd_bytes, c.device)
-        st = lib().sta_window_forward(ctypes.byref(c.problem), _rows(c.q), _rows(c.k), _rows(c.v), _rows(o), _ptr(lse),
-                                      _ptr(c.cu_q), _ptr(c.cu_kv), _ptr(ws), ws.numel() * ws.element_size(),
+        st = lib().sta_window_forward(ctypes.byref(c.problem), _rows(c.q), _rows(c.k), _rows(c.v), _rows(o), _at(lse),
+                                      _at(c.cu_q), _at(c.cu_kv), ws.data_ptr(), ws.nbytes,
                                       _current_stream(c.device), STA_CALL_CHECK if check else 0)
         _check(st, "sta_window_forward")
     return o, lse
@@ -187,18 +197,21 @@ def _backward(c: _Call, o, lse, dout, dq=None, dk=None, dv=None, workspace=None,
     o = _input(o, "o", c.q_shape, c.dtype, c.device)
     dout = _input(dout, "dout", c.q_shape, c.dtype, c.device)
     _flat(lse, "lse", c.q_shape[:3], torch.float32, c.device)
-    given = []
+    outs, new = [], []
     for t, like, shape, name in ((dq, c.q, c.q_shape, "dq"), (dk, c.k, c.kv_shape, "dk"), (dv, c.v, c.kv_shape, "dv")):
-        given.append(_new(like, c.packed) if t is None else _output(t, name, shape, c.dtype, c.device))
-    dq, dk, dv = given
+        outs.append(_new(like) if t is None else _output(t, name, shape, c.dtype, c.device))
+        if t is None:
+            new.append(outs[-1])
+    dq, dk, dv = outs
     if c.empty or 0 in c.kv_shape:
-        for t in given:
-            t.zero_()
+        torch._foreach_zero_(outs)
         return dq, dk, dv
+    if c.packed and new:  # rows outside every sequence are not written
+        torch._foreach_zero_(new)
     ws = _scratch(workspace, c.bwd_bytes, c.device)
-    st = lib().sta_window_backward(ctypes.byref(c.problem), _rows(c.q), _rows(c.k), _rows(c.v), _rows(o), _ptr(lse),
-                                   _rows(dout), _rows(dq), _rows(dk), _rows(dv), _ptr(c.cu_q), _ptr(c.cu_kv),
-                                   _ptr(ws), ws.numel() * ws.element_size(), _current_stream(c.device),
+    st = lib().sta_window_backward(ctypes.byref(c.problem), _rows(c.q), _rows(c.k), _rows(c.v), _rows(o), _at(lse),
+                                   _rows(dout), _rows(dq), _rows(dk), _rows(dv), _at(c.cu_q), _at(c.cu_kv),
+                                   ws.data_ptr(), ws.nbytes, _current_stream(c.device),
                                    STA_CALL_CHECK if check else 0)
     _check(st, "sta_window_backward")
     return dq, dk, dv
