@@ -26,6 +26,13 @@ template <> struct Code<STA_TYPE_E4M3> {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
   }
+  // four finite values of at most the largest code (but for a rounding)
+  static __device__ __forceinline__ uint32_t pack_finite(float a, float b, float c, float d) {
+    uint16_t x, y;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(x) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(d), "f"(c));
+    return uint32_t(x) | (uint32_t(y) << 16);
+  }
   static __device__ __forceinline__ float2 unpack(uint32_t w) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
@@ -39,6 +46,12 @@ template <> struct Code<STA_TYPE_INT8> {
     const int a = __float2int_rn(fminf(fmaxf(lo, -127.f), 127.f)), b = __float2int_rn(fminf(fmaxf(hi, -127.f), 127.f));
     return (lo == lo ? (uint32_t)a & 0xffu : 0u) | ((hi == hi ? (uint32_t)b & 0xffu : 0u) << 8);
   }
+  // Adding 1.5 * 2^23 rounds to the nearest even integer, whose two's complement
+  // is the sum's low byte.
+  static __device__ __forceinline__ uint32_t pack_finite(float a, float b, float c, float d) {
+    auto bits = [](float x) { return __float_as_uint(__fadd_rn(x, 12582912.f)); };  // not fused with the product before
+    return __byte_perm(__byte_perm(bits(a), bits(b), 0x0040), __byte_perm(bits(c), bits(d), 0x0040), 0x5410);
+  }
   static __device__ __forceinline__ float2 unpack(uint32_t w) {
     return make_float2((float)(int8_t)(w & 0xffu), (float)(int8_t)((w >> 8) & 0xffu));
   }
@@ -48,8 +61,14 @@ __device__ __forceinline__ int clamp_count(const CacheMove &m, int b) {
   return m.count ? min(max(__ldg(m.count + b), 0), m.rows) : m.rows;
 }
 
-// One CTA per (block of tokens touched, key head, sequence and tensor).
-template <int D, int kType, class T>
+// Largest magnitude of packed pairs: without their sign, 16-bit floats order
+// like unsigned integers, with infinity and NaN on top.
+__device__ __forceinline__ uint32_t top_pair(uint32_t top, uint32_t w) { return __vmaxu2(top, w & 0x7fff7fffu); }
+template <class T> constexpr uint32_t kInfBits = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+
+// One CTA per (block of tokens touched, key head, sequence and tensor).  The new
+// rows stay in registers between the maximum and the codes: one pass over them.
+template <int D, int kBlock, int kType, class T>
 __global__ void __launch_bounds__(128) cache_write_kernel(const CacheMove m) {
   const CacheParams &c = m.c;
   const bool is_v = blockIdx.z & 1;
@@ -57,58 +76,71 @@ __global__ void __launch_bounds__(128) cache_write_kernel(const CacheMove m) {
   const int start = __ldg(m.start + b), count = clamp_count(m, b);
   if (start < 0 || count == 0) return;
   const long long end = (long long)start + count;
-  const long long first = ((long long)start / c.block + blockIdx.x) * c.block;  // first token of the block
-  if (first >= end || first + c.block > (long long)c.table_pages * c.page_size) return;
+  const long long first = ((long long)start / kBlock + blockIdx.x) * kBlock;  // first token of the block
+  if (first >= end || first + kBlock > (long long)c.table_pages * c.page_size) return;
   const int page = page_of(c, b, (int)first);
   if (page < 0) return;
-  const int in_page = (int)(first % c.page_size);
-  uint8_t *codes = (is_v ? c.v : c.k) + (((long long)page * c.kv_heads + h) * c.page_size + in_page) * D;
-  float *scale = (is_v ? c.v_scale : c.k_scale) + ((long long)page * c.kv_heads + h) * (c.page_size / c.block) +
-                 in_page / c.block;
+  const int in_page = (int)first % c.page_size;
+  const long long ph = (long long)page * c.kv_heads + h;
+  uint8_t *codes = (is_v ? c.v : c.k) + (ph * c.page_size + in_page) * D;
+  float *scale = (is_v ? c.v_scale : c.k_scale) + ph * (c.page_size / kBlock) + in_page / kBlock;
   const Rows &x = is_v ? m.v : m.k;
-  const int lo = (int)max(0ll, start - first), hi = (int)min((long long)c.block, end - first);  // new tokens of the block
+  const int lo = (int)max(0ll, start - first), hi = (int)min((long long)kBlock, end - first);  // new tokens of the block
   constexpr int kPer = D / 8;  // 16-byte pieces per row
-  constexpr int kMaxPieces = 128 * kPer / 128;
-  const char *src = x.p + 2 * ((long long)b * x.b + (long long)h * x.h + (first - start) * x.r);
-  uint4 held[kMaxPieces];
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxPieces; ++i) {
-    const int piece = threadIdx.x + 128 * i, row = lo + piece / kPer;
-    if (row < hi) {
-      held[i] = *reinterpret_cast<const uint4 *>(src + 2 * ((long long)row * x.r + piece % kPer * 8));
-      const uint32_t w[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = Elem<T>::unpack(w[e]);
-        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));  // fmaxf drops NaN
-      }
-    }
-  }
-  amax = fminf(amax, Elem<T>::kMax);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  __shared__ float part[4];
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+  constexpr int kPieces = kBlock * kPer / 128 > 0 ? kBlock * kPer / 128 : 1, kPass = 128 / kPer;
+  const int row0 = lo + threadIdx.x / kPer, col = threadIdx.x % kPer * 8;
+  const char *src = x.p + 2 * ((long long)b * x.b + (long long)h * x.h + (first - start + row0) * x.r + col);
   const float old = lo > 0 ? *scale : 0.f;
+  uint4 held[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    if (row0 + kPass * i < hi) held[i] = __ldg(reinterpret_cast<const uint4 *>(src + 2 * kPass * i * x.r));
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    if (row0 + kPass * i < hi) top = top_pair(top_pair(top_pair(top_pair(top, held[i].x), held[i].y), held[i].z), held[i].w);
+  top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+  __shared__ uint32_t part[4];
+  __shared__ float part_f[4];
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
   __syncthreads();  // every thread has read the old scale, too
-  amax = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+  top = max(max(part[0], part[1]), max(part[2], part[3]));
+  float amax = Elem<T>::unpack(top).x;
+  const bool plain = top < kInfBits<T>;
+  if (!plain) {
+    // infinities count as the type's largest value, NaN as nothing
+    amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (row0 + kPass * i < hi) {
+        const uint32_t w[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = Elem<T>::unpack(w[e]);
+          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));  // fmaxf drops NaN
+        }
+      }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    if ((threadIdx.x & 31) == 0) part_f[threadIdx.x >> 5] = amax;
+    __syncthreads();
+    amax = fminf(fmaxf(fmaxf(part_f[0], part_f[1]), fmaxf(part_f[2], part_f[3])), Elem<T>::kMax);
+  }
   const float s = fmaxf(old, fmaxf(amax / Code<kType>::kMax, kScaleFloor));
   const float inv = 1.f / s;
   if (threadIdx.x == 0) *scale = s;
 #pragma unroll
-  for (int i = 0; i < kMaxPieces; ++i) {
-    const int piece = threadIdx.x + 128 * i, row = lo + piece / kPer;
-    if (row < hi) {
+  for (int i = 0; i < kPieces; ++i) {
+    if (row0 + kPass * i < hi) {
       const uint32_t w[4] = {held[i].x, held[i].y, held[i].z, held[i].w};
-      uint32_t q[4];
+      uint32_t q[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = Elem<T>::unpack(w[e]);
-        q[e] = Code<kType>::pack(f.x * inv, f.y * inv);
+      for (int e = 0; e < 2; ++e) {
+        const float2 f = Elem<T>::unpack(w[2 * e]), z = Elem<T>::unpack(w[2 * e + 1]);
+        q[e] = plain ? Code<kType>::pack_finite(f.x * inv, f.y * inv, z.x * inv, z.y * inv)
+                     : Code<kType>::pack(f.x * inv, f.y * inv) | (Code<kType>::pack(z.x * inv, z.y * inv) << 16);
       }
-      *reinterpret_cast<uint2 *>(codes + row * D + piece % kPer * 8) =
-          make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+      *reinterpret_cast<uint2 *>(codes + (row0 + kPass * i) * D + col) = make_uint2(q[0], q[1]);
     }
   }
   if (lo > 0 && s > old) {
@@ -163,7 +195,12 @@ template <int D, int kType, class T>
 cudaError_t write_launch(const CacheMove &m, cudaStream_t stream) {
   // a run of `rows` tokens that starts anywhere touches at most this many blocks
   const dim3 grid((m.rows + m.c.block - 2) / m.c.block + 1, m.c.kv_heads, 2 * m.batch);
-  cache_write_kernel<D, kType, T><<<grid, 128, 0, stream>>>(m);
+  switch (m.c.block) {
+    case 16: cache_write_kernel<D, 16, kType, T><<<grid, 128, 0, stream>>>(m); break;
+    case 32: cache_write_kernel<D, 32, kType, T><<<grid, 128, 0, stream>>>(m); break;
+    case 64: cache_write_kernel<D, 64, kType, T><<<grid, 128, 0, stream>>>(m); break;
+    default: cache_write_kernel<D, 128, kType, T><<<grid, 128, 0, stream>>>(m);
+  }
   return cudaGetLastError();
 }
 template <int D, int kType, class T>
