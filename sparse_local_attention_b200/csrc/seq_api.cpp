@@ -178,10 +178,13 @@ bool kv_map(CUtensorMap *m, const sta_rows *x, const sta_window_problem *p, bool
   return tile_map(m, x, p->type, p->head_dim, packed ? p->kv_rows : p->kv_len, p->kv_heads, packed ? 1 : p->batch);
 }
 
-bool multiprocessors(int *n) {
+// Make the current device's context current for this thread, too: a thread that
+// has not used the device before (such as an autograd worker) has none, and
+// encoding a tensor map needs it.
+bool open_device(int *multiprocessors) {
   int dev = -1;
-  return cudaGetDevice(&dev) == cudaSuccess &&
-         cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess &&
+         cudaDeviceGetAttribute(multiprocessors, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
 }
 
 sta_status check_workspace(const void *ws, size_t have, size_t need) {
@@ -268,8 +271,9 @@ sta_status sta_window_forward(const sta_window_problem *p, const sta_rows *q, co
       if (sta::launch_window_split(w, p->type, stream) != cudaSuccess) return STA_ERR_CUDA;
       return finish(ws, stream, flags);
     }
+    int sms = 0;
     CUtensorMap maps[3];
-    if (!q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
+    if (!open_device(&sms) || !q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
         !kv_map(&maps[2], v, p, cu_q) || sta::launch_window_tiles(w, p->type, maps, stream) != cudaSuccess)
       return STA_ERR_CUDA;
   }
@@ -300,7 +304,7 @@ sta_status sta_window_backward(const sta_window_problem *p, const sta_rows *q, c
   if ((flags & STA_CALL_CHECK) && cudaMemsetAsync(ws, 0, sizeof(int), stream) != cudaSuccess) return STA_ERR_CUDA;
   int sms = 0;
   CUtensorMap maps[4];
-  if (!multiprocessors(&sms) || !q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
+  if (!open_device(&sms) || !q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
       !kv_map(&maps[2], v, p, cu_q) || !q_map(&maps[3], dout, p, cu_q) ||
       sta::launch_window_backward(w, p->type, maps, sms, stream) != cudaSuccess)
     return STA_ERR_CUDA;

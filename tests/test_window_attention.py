@@ -291,6 +291,32 @@ def test_graph_streams_and_concurrent_calls():
 
 
 @pytest.mark.gpu
+def test_first_call_of_a_thread():
+    """A thread whose first use of the device is one of these calls, as an autograd worker's may be."""
+    import threading
+    q, k, v, do = (t.cuda() for t in make(2, 1, 300, 300, 64, BF16))
+    o, lse = window_forward(q, k, v, 50, 2, check=True)
+    want = (o, *window_backward(q, k, v, o, lse, do, 50, 2, check=True))
+    o1, lse1, grads = torch.empty_like(o), torch.empty_like(lse), [torch.empty_like(t) for t in (q, k, v)]
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    calls = (lambda: window_forward(q, k, v, 50, 2, o=o1, lse=lse1, workspace=ws),
+             lambda: window_backward(q, k, v, o, lse, do, 50, 2, dq=grads[0], dk=grads[1], dv=grads[2], workspace=ws))
+    failed = []
+    for call in calls:
+        def first(call=call):
+            try:
+                call()
+            except Exception as e:  # noqa: BLE001
+                failed.append(e)
+        t = threading.Thread(target=first)
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed and all(torch.equal(a, b) for a, b in zip((o1, *grads), want))
+
+
+@pytest.mark.gpu
 def test_capture_of_leaves_with_a_live_eager_graph_is_refused():
     leaves = [t.cuda().requires_grad_() for t in make(2, 2, 64, 64, 64, BF16)[:3]]
     alive = sliding_window_attention(*leaves, 16, 2)
