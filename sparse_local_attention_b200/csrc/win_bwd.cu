@@ -164,29 +164,12 @@ __global__ void __launch_bounds__(256) window_pre_kernel(const WinParams p) {
 }
 
 // ----------------------------------------------------------------------- 2. dK, dV
-template <int D>
-struct DkvCfg {
-  static constexpr uint32_t kTile = kBM * D * 2;
-  static constexpr bool kSep = D == 64;  // P^T, dS^T in columns of their own
-  using R = Roles<kSep ? 4 : 2>;
-  static constexpr int kStages = D == 128 ? 2 : 5;
-  static constexpr uint32_t kStage = 2 * kTile + kAugBytes;  // Q, dO, the rows' panel
-  static constexpr uint32_t kSel = 2 * kAugBytes;            // selector panels of -LSE / scale and -D
-  // st_full[S] st_empty[S] raw[S] kv_full kv_free s_full s_read p_ready pd_free acc_done acc_free drain
-  static constexpr int kNumBars = 3 * kStages + 9;
-  static constexpr uint32_t kSmem = 2 * kTile + kStages * kStage + kSel + kNumBars * 8 + 64 + 1024;
-  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-  static constexpr uint32_t kTmS = 0, kTmDP = 128;
-  static constexpr uint32_t kTmP = kSep ? 256 : kTmS, kTmDS = kSep ? 320 : kTmDP;
-  static constexpr uint32_t kTmDV = kSep ? 384 : 256, kTmDK = kTmDV + D;
-  static_assert(kTmDK + D <= 512, "TMEM budget");
-};
-
 // A key block and the part [c0, c1) of its chunks; chunk c is rows [qa + 128
 // (c % per_head), ...) of head c / per_head of the group.
 struct KeyItem {
+  bool stop;
   Sequence s;
-  int b, hk, key0, rows;
+  int b, hk, key0, rows;  // rows: 0 for a part that is not there
   int qa, qe, per_head, c0, c1, segs;
   long long slot;  // of the part's sums, or -1: the block is one part
   __device__ __forceinline__ int first(int c) const { return qa + c % per_head * kBM; }
@@ -208,7 +191,10 @@ __device__ __forceinline__ void block_queries(const WinParams &p, KeyItem &it) {
 // Parts are numbered sink blocks first (sink_blocks of them with sink_segs
 // slots each), then the others (norm_segs each), key blocks ascending, the
 // sequences and key heads innermost.
-__device__ __forceinline__ bool key_item(const WinParams &p, int item, KeyItem &it) {
+__device__ __forceinline__ KeyItem key_item(const WinParams &p, int item) {
+  KeyItem it;
+  it.stop = item < 0;
+  if (it.stop) return it;
   const int slices = p.batch * p.kv_heads;
   const int slice = item % slices, unit = item / slices, sink_units = p.sink_blocks * p.sink_segs;
   int kb, seg;
@@ -221,18 +207,40 @@ __device__ __forceinline__ bool key_item(const WinParams &p, int item, KeyItem &
   it.s = sequence(p, it.b);
   it.key0 = kb * kBM;
   block_queries(p, it);
-  if (it.rows <= 0 || seg >= it.segs) return false;
-  const int total = it.per_head * p.group, per = (total + it.segs - 1) / it.segs;
+  if (seg >= it.segs) it.rows = 0;
+  const int total = it.rows > 0 ? it.per_head * p.group : 0, per = (total + it.segs - 1) / it.segs;
   it.c0 = min(total, seg * per), it.c1 = min(total, it.c0 + per);
   it.slot = it.segs > 1 ? item : -1;
-  return true;
+  return it;
 }
+
+// The two halves of a chunk (64 queries each) are worked on by a warpgroup each
+// and go through tensor memory on their own: while one half's P^T and dS^T are
+// formed, the products of the other one run.  S^T and dP^T of a half take 64
+// columns each and P^T and dS^T lie over the first 32 of them, which with dV and
+// dK at head dim 128 is all there is.
+template <int D>
+struct DkvCfg {
+  static constexpr uint32_t kTile = kBM * D * 2;
+  using R = Roles<2>;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr uint32_t kStage = 2 * kTile + kAugBytes;  // Q, dO, the rows' panel
+  static constexpr uint32_t kSel = 2 * kAugBytes;            // selector panels of -LSE / scale and -D
+  // st_full[S] st_empty[S] raw[S] kv_full kv_free s_full[2] p_ready[2] acc_done acc_free drain
+  static constexpr int kNumBars = 3 * kStages + 9;
+  static constexpr uint32_t kSmem =
+      2 * kTile + kStages * kStage + kSel + kNumBars * 8 + 64 + ItemRing<KeyItem>::kBytes + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+  static constexpr uint32_t kTmS = 0, kTmDP = 128;  // half x: + 64 x
+  static constexpr uint32_t kTmDV = 256, kTmDK = kTmDV + D;
+  static_assert(kTmDK + D <= 512, "TMEM budget");
+};
 
 template <int D, class T>
 __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
     window_dkdv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
-                       const WinParams p, const int n_items) {
+                       const WinParams p) {
   using C = DkvCfg<D>;
   using R = typename C::R;
   constexpr int kCW = R::kCols;
@@ -244,23 +252,23 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(sel_s + C::kSel);
   uint64_t *st_full = bars, *st_empty = bars + C::kStages, *raw = bars + 2 * C::kStages;
   uint64_t *kv_full = bars + 3 * C::kStages, *kv_free = kv_full + 1;
-  uint64_t *s_full = kv_full + 2;   // S^T, dP^T of a chunk are in TMEM
-  uint64_t *s_read = kv_full + 3;   // ... and have been read (columns of their own only)
-  uint64_t *p_ready = kv_full + 4;  // P^T, dS^T written
-  uint64_t *pd_free = kv_full + 5;  // the dV / dK products have read them (columns of their own only)
+  uint64_t *s_full = kv_full + 2;   // [2] S^T, dP^T of a half are in TMEM
+  uint64_t *p_ready = kv_full + 4;  // [2] its P^T, dS^T written
   uint64_t *acc_done = kv_full + 6, *acc_free = kv_full + 7, *drain = kv_full + 8;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  ItemRing<KeyItem> ring(tmem_slot + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    ring.init(R::kMathWarps + 2);
     for (int i = 0; i < 3 * C::kStages; ++i) mbar_init(&bars[i], 1);
     mbar_init(kv_full, 1);
     mbar_init(kv_free, 1);
-    mbar_init(s_full, 1);
-    mbar_init(s_read, R::kMathWarps);
-    mbar_init(p_ready, R::kMathWarps);
-    mbar_init(pd_free, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_ready[x], 4);
+    }
     mbar_init(acc_done, 1);
     mbar_init(acc_free, R::kMathWarps);
     mbar_init(drain, 1);
@@ -298,11 +306,20 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
       tma_prefetch_desc(&tmap_k);
       tma_prefetch_desc(&tmap_v);
       tma_prefetch_desc(&tmap_do);
-      uint32_t ld = 0, items = 0, raw_par = 0, raw_last = 0;
-      bool ok = true;
-      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-        KeyItem it;
-        if (!key_item(p, item, it) || it.c0 == it.c1) continue;
+      uint32_t ld = 0, items = 0, raw_par = 0, raw_last = 0, n = 0;
+      int item = blockIdx.x;
+      bool ok = true, asked = false;
+      while (true) {
+        const KeyItem it = key_item(p, item);
+        if (!ring.put(n, it, ctl, kErrBwdWait)) { ok = false; break; }
+        if (it.stop) break;
+        ring.ask();
+        asked = true;
+        if (it.c0 == it.c1) {
+          if (!ring.take(n++, item, ctl, kErrBwdWait)) { ok = false; break; }
+          asked = false;
+          continue;
+        }
         if (!mbar_wait(kv_free, (items & 1) ^ 1, ctl, kErrBwdWait)) { ok = false; break; }
         mbar_arrive_expect_tx(kv_full, 2 * C::kTile);
         load_tile<D>(k_s, &tmap_k, it.s.k0 + it.key0, it.hk, it.s.slice, kv_full);
@@ -323,6 +340,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
           bulk_load(sb + 2 * C::kTile, p.aug + (aug_row(p, it.s, it.b, h) + first) / 8 * 256, kAugBytes, bar);
           ++ld;
         }
+        if (!ok || !ring.take(n++, item, ctl, kErrBwdWait)) { ok = false; break; }
+        asked = false;
       }
       if (!ok) {
         const uint32_t start = ld > (uint32_t)C::kStages ? ld - C::kStages : 0;
@@ -332,14 +351,17 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
           else drain_wait(&st_full[st], (i / C::kStages) & 1);
         }
         if (items > 0) drain_wait(kv_full, (items - 1) & 1);
+        if (item >= 0) ring.discard(n, asked);
       }
     }
   } else if (warp == R::kClearWarp) {
     uint32_t ld = 0, raw_par = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      KeyItem it;
-      if (!key_item(p, item, it)) continue;
+    for (uint32_t n = 0;; ++n) {
+      const KeyItem *at = ring.get(n, ok, ctl, kErrBwdWait);
+      if (!at) break;
+      const KeyItem it = *at;
+      ring.release(n, lane);
       for (int c = it.c0; c < it.c1 && ok; ++c, ++ld) {
         const int valid = it.valid(c);
         if (valid % 16 == 0) continue;
@@ -352,9 +374,10 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
         clear_rows<D>(stages + st * C::kStage + C::kTile, valid, upto, lane);
         if (lane == 0) mbar_arrive(&st_full[st]);
       }
+      if (!ok) break;
     }
   } else if (warp == R::kMmaWarp) {
-    constexpr uint32_t idesc_ss = idesc_for<T>(kBM, kBM, false, false);
+    constexpr uint32_t idesc_ss = idesc_for<T>(kBM, 64, false, false);
     constexpr uint32_t idesc_acc = idesc_for<T>(kBM, D, false, true);
     const uint64_t kd = smem_desc_sw128(smem_u32(k_s), 16, 1024), vd = smem_desc_sw128(smem_u32(v_s), 16, 1024);
     const uint64_t sk0 = smem_desc_sw128(smem_u32(stages), 16, 1024);         // K-major Q / dO
@@ -362,72 +385,85 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
     const uint64_t sel_l = smem_desc_plain(smem_u32(sel_s), 128, 256);
     const uint64_t sel_d = smem_desc_plain(smem_u32(sel_s) + kAugBytes, 128, 256);
     const uint64_t aug0 = smem_desc_plain(smem_u32(stages + 2 * C::kTile), 128, 256);
-    uint32_t ld = 0, items = 0, p_waits = 0, r_waits = 0;
+    constexpr uint32_t kHalfRows = 64 * 128 >> 4, kHalfAug = kAugBytes / 2 >> 4;  // of descriptors, to the second half
+    uint32_t ld = 0, items = 0, p_waits[2] = {0, 0};
     bool ok = true, issued = false;
-    auto issue_s = [&](uint32_t st) {
-      const uint32_t so = (st * C::kStage) >> 4, dso = (st * C::kStage + C::kTile) >> 4;
+    // S^T = K Q^T - LSE / scale and dP^T = V dO^T - D for half x of the chunk in stage st
+    auto issue_s = [&](int x, uint32_t st) {
+      const uint32_t so = ((st * C::kStage) >> 4) + x * kHalfRows, dso = so + (C::kTile >> 4);
+      const uint64_t aug = aug0 + ((st * C::kStage) >> 4) + x * kHalfAug;
+      const uint32_t s_tm = tmem + C::kTmS + 64 * x, d_tm = tmem + C::kTmDP + 64 * x;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
-        mma_ss_w(tmem + C::kTmS, kd + off, sk0 + so + off, idesc_ss, kk > 0 ? 1u : 0u);
+        mma_ss_w(s_tm, kd + off, sk0 + so + off, idesc_ss, kk > 0 ? 1u : 0u);
       }
-      mma_ss_w(tmem + C::kTmS, sel_l, aug0 + so, idesc_ss, 1u);  // - LSE / scale per query column
+      mma_ss_w(s_tm, sel_l, aug, idesc_ss, 1u);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
-        mma_ss_w(tmem + C::kTmDP, vd + off, sk0 + dso + off, idesc_ss, kk > 0 ? 1u : 0u);
+        mma_ss_w(d_tm, vd + off, sk0 + dso + off, idesc_ss, kk > 0 ? 1u : 0u);
       }
-      mma_ss_w(tmem + C::kTmDP, sel_d, aug0 + so, idesc_ss, 1u);  // - D per query column
-      mma_commit_w(s_full);
+      mma_ss_w(d_tm, sel_d, aug, idesc_ss, 1u);
+      mma_commit_w(&s_full[x]);
     };
     auto wait_stage = [&](uint32_t l) -> bool {
       if (!mbar_wait_w(&st_full[l % C::kStages], (l / C::kStages) & 1, ctl, kErrBwdWait)) return false;
       tc_fence_after();
       return true;
     };
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      KeyItem it;
-      if (!key_item(p, item, it) || it.c0 == it.c1) continue;
+    for (uint32_t rn = 0;; ++rn) {
+      const KeyItem *at = ring.get(rn, ok, ctl, kErrBwdWait);
+      if (!at) break;
+      const KeyItem it = *at;
+      ring.release(rn, lane);
       const int n = it.c1 - it.c0;
+      if (n == 0) continue;
       if (!mbar_wait_w(kv_full, items & 1, ctl, kErrBwdWait)) { ok = false; break; }
       tc_fence_after();
       if (!wait_stage(ld)) { ok = false; break; }
-      issue_s(ld % C::kStages);
+      int valid = it.valid(it.c0);
+      issue_s(0, ld % C::kStages);
+      if (valid > 64) issue_s(1, ld % C::kStages);
+      if (n == 1) mma_commit_w(kv_free);
       issued = true;
+      bool first = true;
       for (int i = 0; i < n && ok; ++i) {
         const uint32_t cur = ld + i, st = cur % C::kStages;
-        if (C::kSep && i + 1 < n) {
-          // the next chunk's S^T / dP^T as soon as this chunk's have been read
-          if (!mbar_wait_w(s_read, r_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
-          ++r_waits;
-          tc_fence_after();
-          if (!wait_stage(cur + 1)) { ok = false; break; }
-          issue_s((cur + 1) % C::kStages);
-        }
-        if (!mbar_wait_w(p_ready, p_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
-        ++p_waits;
-        if (i == 0 && items > 0 && !mbar_wait_w(acc_free, (items - 1) & 1, ctl, kErrBwdWait)) { ok = false; break; }
-        tc_fence_after();
-        const int steps = (it.valid(it.c0 + i) + 15) / 16;
-        const uint32_t so = (st * C::kStage) >> 4, dso = (st * C::kStage + C::kTile) >> 4;
+        const int next = i + 1 < n ? it.valid(it.c0 + i + 1) : 0;
+        const uint32_t so = (st * C::kStage) >> 4, dso = so + (C::kTile >> 4);
+        bool there = false;  // the next chunk's stage has been waited for
 #pragma unroll
-        for (int kk = 0; kk < kBM / 16; ++kk)
-          if (kk < steps)
-            mma_ts_w(tmem + C::kTmDV, tmem + C::kTmP + kk * 8, sm0 + dso + ((kk * 16 * 128) >> 4), idesc_acc,
-                     (i > 0 || kk > 0) ? 1u : 0u);
+        for (int x = 0; x < 2; ++x) {
+          if (valid > 64 * x) {
+            if (!mbar_wait_w(&p_ready[x], p_waits[x] & 1, ctl, kErrBwdWait)) { ok = false; break; }
+            ++p_waits[x];
+            if (first && items > 0 && !mbar_wait_w(acc_free, (items - 1) & 1, ctl, kErrBwdWait)) { ok = false; break; }
+            tc_fence_after();
+            // dV += P^T dO, dK += dS^T Q over the half's valid rows
+            const int steps = min(4, (valid - 64 * x + 15) / 16);
 #pragma unroll
-        for (int kk = 0; kk < kBM / 16; ++kk)
-          if (kk < steps)
-            mma_ts_w(tmem + C::kTmDK, tmem + C::kTmDS + kk * 8, sm0 + so + ((kk * 16 * 128) >> 4), idesc_acc,
-                     (i > 0 || kk > 0) ? 1u : 0u);
-        mma_commit_w(&st_empty[st]);
-        if (C::kSep) mma_commit_w(pd_free);
-        if (i + 1 == n) mma_commit_w(kv_free);
-        if (!C::kSep && i + 1 < n) {
-          // P^T / dS^T lie in the S^T / dP^T columns: the next ones follow their readers in order
-          if (!wait_stage(cur + 1)) { ok = false; break; }
-          issue_s((cur + 1) % C::kStages);
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < steps)
+                mma_ts_w(tmem + C::kTmDV, tmem + C::kTmS + 64 * x + kk * 8, sm0 + dso + x * kHalfRows + ((kk * 16 * 128) >> 4),
+                         idesc_acc, first && kk == 0 ? 0u : 1u);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < steps)
+                mma_ts_w(tmem + C::kTmDK, tmem + C::kTmDP + 64 * x + kk * 8, sm0 + so + x * kHalfRows + ((kk * 16 * 128) >> 4),
+                         idesc_acc, first && kk == 0 ? 0u : 1u);
+            first = false;
+            if (x == 1 || valid <= 64) mma_commit_w(&st_empty[st]);
+          }
+          // the half's next S^T / dP^T take the place of the P^T / dS^T just read
+          if (next > 64 * x) {
+            if (!there && !wait_stage(cur + 1)) { ok = false; break; }
+            there = true;
+            issue_s(x, (cur + 1) % C::kStages);
+          }
         }
+        if (i + 2 == n) mma_commit_w(kv_free);  // K and V are no longer read
+        valid = next;
       }
       if (!ok) break;
       ld += n;
@@ -439,33 +475,39 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
       drain_wait(drain, 0);
     }
   } else {
-    // elementwise: thread = key row of the block; warpgroup e owns query columns [kCW e, kCW e + kCW)
-    const int e = warp >> 2, row = (warp & 3) * 32 + lane;
+    // elementwise: warpgroup x works on half x; thread = key row of the block
+    const int x = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), shift = make_float2(kPShift<T>, kPShift<T>);
     // dS = P (dP - D), with P's own factor taken out again
     const float ds_mul = kIsHalf<T> ? fac * exp2f(-kPShift<T>) : 1.f;
     const float2 dsm = make_float2(ds_mul, ds_mul);
-    uint32_t s_waits = 0, f_waits = 0, items = 0, chunks = 0;
+    const uint32_t s_tm = tmem + lane_off + C::kTmS + 64 * x, d_tm = tmem + lane_off + C::kTmDP + 64 * x;
+    uint32_t s_waits = 0, items = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      KeyItem it;
-      if (!key_item(p, item, it)) continue;
+    for (uint32_t n = 0;; ++n) {
+      const KeyItem *at = ring.get(n, ok, ctl, kErrBwdWait);
+      if (!at) break;
+      const KeyItem it = *at;
+      ring.release(n, lane);
       const int key = it.key0 + row, off = it.s.nk - it.s.nq;
-      for (int c = it.c0; c < it.c1; ++c, ++chunks) {
-        const int first = it.first(c), valid = it.valid(c), qpos = first + off;
-        // whole: all 128 queries see all 128 keys
-        const bool whole = valid == kBM && qpos >= it.key0 + kBM - 1 &&
-                           (qpos + kBM - 1 < it.key0 + p.window || it.key0 + kBM <= p.sinks);
-        const int c_lo = key - qpos - kCW * e;  // columns below do not see this key
-        const int c_hi = min(valid, key < p.sinks ? kBM : min(kBM, key - qpos + p.window)) - kCW * e;
-        bool okw = mbar_wait_w(s_full, s_waits & 1, ctl, kErrBwdWait);
+      for (int c = it.c0; c < it.c1; ++c) {
+        const int valid = it.valid(c) - 64 * x, qpos = it.first(c) + 64 * x + off;
+        if (valid <= 0) continue;
+        // whole: the half's 64 queries see all 128 keys
+        const bool whole = valid >= 64 && qpos >= it.key0 + kBM - 1 &&
+                           (qpos + 63 < it.key0 + p.window || it.key0 + kBM <= p.sinks);
+        const int c_lo = key - qpos;  // columns below do not see this key
+        const int c_hi = min(min(valid, 64), key < p.sinks ? 64 : key - qpos + p.window);
+        if (!mbar_wait_w(&s_full[x], s_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
         ++s_waits;
-        uint32_t pp[kCW / 32][16], pd[kCW / 32][16];
-        auto pds = [&](int q0, int n, const uint32_t *rs, const uint32_t *rd) {
-          const uint32_t bits = whole ? 0xffffffffu : bits_below(c_hi - q0) & ~bits_below(c_lo - q0);
+        tc_fence_after();
+        uint32_t pp[2][16], pd[2][16];
+        // 16 columns from q0 on, from their raw S^T and dP^T
+        auto form = [&](int q0, const uint32_t(&rs)[16], const uint32_t(&rd)[16]) {
+          const uint32_t bits = whole ? 0xffffu : bits_below(c_hi - q0) & ~bits_below(c_lo - q0);
 #pragma unroll
-          for (int k = 0; k < n; ++k) {
+          for (int k = 0; k < 8; ++k) {
             const int w = q0 / 2 + k;
             const float2 sv = make_float2(__uint_as_float(rs[2 * k]), __uint_as_float(rs[2 * k + 1]));
             const float2 t = kIsHalf<T> ? fma2(sv, sl2, shift) : mul2(sv, sl2);
@@ -480,88 +522,57 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
             pd[w >> 4][w & 15] = Elem<T>::pack(dr.x, dr.y);
           }
         };
-        const uint32_t base = tmem + lane_off + kCW * e;
-        if constexpr (C::kSep) {
-          if (okw) {
-            tc_fence_after();
-            uint32_t rs[32], rd[32];
-            tmem_ld32(base + C::kTmS, rs);
-            tmem_ld32(base + C::kTmDP, rd);
-            tmem_ld_wait();
-            reg_fence32(rs);
-            reg_fence32(rd);
-            if (c + 1 < it.c1) {
-              tc_fence_before();
-              warp_arrive(s_read, lane);
-            }
-            pds(0, 16, rs, rd);
-          }
-        } else {
+        {
           // four quarters of 16 columns, the next quarter's load in flight
-          if (okw) {
-            tc_fence_after();
-            const uint32_t sa = base + C::kTmS, da = base + C::kTmDP;
-            uint32_t s0[16], d0[16], s1[16], d1[16];
-            tmem_ld16(sa, s0);
-            tmem_ld16(da, d0);
-            tmem_ld_wait_regs(s0, d0);
-            tmem_ld16(sa + 16, s1);
-            tmem_ld16(da + 16, d1);
-            pds(0, 8, s0, d0);
-            tmem_ld_wait_regs(s1, d1);
-            tmem_ld16(sa + 32, s0);
-            tmem_ld16(da + 32, d0);
-            pds(16, 8, s1, d1);
-            tmem_ld_wait_regs(s0, d0);
-            tmem_ld16(sa + 48, s1);
-            tmem_ld16(da + 48, d1);
-            pds(32, 8, s0, d0);
-            tmem_ld_wait_regs(s1, d1);
-            pds(48, 8, s1, d1);
-          }
-          // both warpgroups have read their columns before either writes over the first half of them
-          okw = named_bar_and(1, 32 * R::kMathWarps, okw);
+          uint32_t s0[16], d0[16], s1[16], d1[16];
+          tmem_ld16(s_tm, s0);
+          tmem_ld16(d_tm, d0);
+          tmem_ld_wait_regs(s0, d0);
+          tmem_ld16(s_tm + 16, s1);
+          tmem_ld16(d_tm + 16, d1);
+          form(0, s0, d0);
+          tmem_ld_wait_regs(s1, d1);
+          tmem_ld16(s_tm + 32, s0);
+          tmem_ld16(d_tm + 32, d0);
+          form(16, s1, d1);
+          tmem_ld_wait_regs(s0, d0);
+          tmem_ld16(s_tm + 48, s1);
+          tmem_ld16(d_tm + 48, d1);
+          // the first 32 columns have been read by this lane, the only one that does
+          tmem_st16(s_tm, pp[0]);
+          tmem_st16(d_tm, pd[0]);
+          form(32, s0, d0);
+          tmem_ld_wait_regs(s1, d1);
+          form(48, s1, d1);
         }
-        if (!okw) { ok = false; break; }
-        if (C::kSep && chunks > 0) {
-          if (!mbar_wait_w(pd_free, f_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
-          ++f_waits;
-          tc_fence_after();
-        }
-        const uint32_t pbase = tmem + lane_off + (kCW / 2) * e;
-#pragma unroll
-        for (int hf = 0; hf < kCW / 32; ++hf) {
-          tmem_st16(pbase + C::kTmP + 16 * hf, pp[hf]);
-          tmem_st16(pbase + C::kTmDS + 16 * hf, pd[hf]);
-        }
+        tmem_st16(s_tm + 16, pp[1]);
+        tmem_st16(d_tm + 16, pd[1]);
         tmem_st_wait();
         tc_fence_before();
-        warp_arrive(p_ready, lane);
+        warp_arrive(&p_ready[x], lane);
       }
       if (!ok) break;
-      // epilogue: the first half of the warpgroups writes dV, the second half dK, kOut columns each
+      // epilogue: warpgroup 0 writes dV, 1 dK
+      if (it.rows <= 0) continue;
       const bool any = it.c0 < it.c1;
       if (any) {
-        bool oke = mbar_wait_w(acc_done, items & 1, ctl, kErrBwdWait);
-        if (!C::kSep) oke = named_bar_and(1, 32 * R::kMathWarps, oke);
-        if (!oke) { ok = false; break; }
+        if (!mbar_wait_w(acc_done, items & 1, ctl, kErrBwdWait)) { ok = false; break; }
         tc_fence_after();
       }
-      constexpr int kHalf = R::kGroups / 2, kOut = D / kHalf;
-      static_assert(kOut % 32 == 0, "whole 32-column TMEM loads");
-      const int which = e / kHalf, part = e % kHalf;
-      const uint32_t col = (which ? C::kTmDK : C::kTmDV) + part * kOut;
-      const float mul = which ? p.scale / fac : exp2f(-kPShift<T>);
-      const Rows &out = which ? p.dk : p.dv;
-      uint4 *dst = reinterpret_cast<uint4 *>(out.p + 2 * (it.s.slice * out.b + it.hk * out.h +
-                                                          (long long)(it.s.k0 + key) * out.r + part * kOut));
-      float4 *sums = reinterpret_cast<float4 *>(p.parts + ((it.slot * 2 + which) * kBM + row) * D + part * kOut);
+      const uint32_t col = x ? C::kTmDK : C::kTmDV;
+      const float mul = x ? p.scale / fac : exp2f(-kPShift<T>);
+      const Rows &out = x ? p.dk : p.dv;
+      char *dst = out.p + 2 * (it.s.slice * out.b + it.hk * out.h + (long long)(it.s.k0 + (key & ~3)) * out.r);
+      const int quad_rows = it.rows - (row & ~3);
+      // the parts' sums, four columns of all rows behind one another
+      float4 *sums = reinterpret_cast<float4 *>(p.parts) + (it.slot * 2 + x) * (kBM * D / 4) + row;
 #pragma unroll
-      for (int c = 0; c < kOut / 32; ++c) {
+      for (int c = 0; c < D / 32; ++c) {
         uint32_t r[32];
         if (any) {
           tmem_ld32(tmem + lane_off + col + c * 32, r);
           tmem_ld_wait();
+          reg_fence32(r);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) r[i] = 0u;
@@ -569,17 +580,18 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
         if (it.slot >= 0) {
 #pragma unroll
           for (int v = 0; v < 8; ++v)
-            sums[c * 8 + v] = make_float4(__uint_as_float(r[4 * v]) * mul, __uint_as_float(r[4 * v + 1]) * mul,
-                                          __uint_as_float(r[4 * v + 2]) * mul, __uint_as_float(r[4 * v + 3]) * mul);
-        } else if (row < it.rows) {
+            sums[(c * 8 + v) * kBM] = make_float4(__uint_as_float(r[4 * v]) * mul, __uint_as_float(r[4 * v + 1]) * mul,
+                                                  __uint_as_float(r[4 * v + 2]) * mul, __uint_as_float(r[4 * v + 3]) * mul);
+        } else {
+          uint4 w[4];
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = Elem<T>::pack(__uint_as_float(r[8 * v + 2 * i]) * mul, __uint_as_float(r[8 * v + 2 * i + 1]) * mul);
-            dst[c * 4 + v] = make_uint4(w[0], w[1], w[2], w[3]);
+            auto pair = [&](int i) {
+              return Elem<T>::pack(__uint_as_float(r[8 * v + 2 * i]) * mul, __uint_as_float(r[8 * v + 2 * i + 1]) * mul);
+            };
+            w[v] = make_uint4(pair(0), pair(1), pair(2), pair(3));
           }
+          store_quad(w, dst + 64 * c, 2 * out.r, quad_rows, lane);
         }
       }
       if (any) {
@@ -611,20 +623,20 @@ __global__ void __launch_bounds__(256) window_join_kernel(const WinParams p) {
   if (it.rows <= 0 || it.segs == 1) return;
   const bool sink = kb < p.sink_blocks;
   const int unit = sink ? kb * p.sink_segs : p.sink_blocks * p.sink_segs + (kb - p.sink_blocks) * p.norm_segs;
-  constexpr int kPer = D / 8;
+  constexpr int kPer = D / 4;
   for (int i = threadIdx.x; i < 2 * kBM * kPer; i += 256) {
-    const int which = i / (kBM * kPer), row = i / kPer % kBM, col = i % kPer * 8;
+    const int row = i % kBM, col = i / kBM % kPer, which = i / (kBM * kPer);
     if (row >= it.rows) continue;
-    float a[8] = {};
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int seg = 0; seg < it.segs; ++seg) {
       const long long slot = (long long)(unit + seg) * slices + slice;
-      const float4 *x = reinterpret_cast<const float4 *>(p.parts + ((slot * 2 + which) * kBM + row) * D + col);
-      const float4 u = x[0], v = x[1];
-      a[0] += u.x, a[1] += u.y, a[2] += u.z, a[3] += u.w, a[4] += v.x, a[5] += v.y, a[6] += v.z, a[7] += v.w;
+      const float4 u = reinterpret_cast<const float4 *>(p.parts)[((slot * 2 + which) * kPer + col) * kBM + row];
+      a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
     }
     const Rows &out = which ? p.dk : p.dv;
-    *reinterpret_cast<uint4 *>(out.p + 2 * (it.s.slice * out.b + it.hk * out.h + (long long)(it.s.k0 + it.key0 + row) * out.r + col)) =
-        make_uint4(Elem<T>::pack(a[0], a[1]), Elem<T>::pack(a[2], a[3]), Elem<T>::pack(a[4], a[5]), Elem<T>::pack(a[6], a[7]));
+    *reinterpret_cast<uint2 *>(out.p + 2 * (it.s.slice * out.b + it.hk * out.h + (long long)(it.s.k0 + it.key0 + row) * out.r + 4 * col)) =
+        make_uint2(Elem<T>::pack(a.x, a.y), Elem<T>::pack(a.z, a.w));
   }
 }
 
@@ -971,8 +983,7 @@ cudaError_t launch(const WinParams &p, const CUtensorMap *m, int num_sms, cudaSt
   if (nqb > 0) window_pre_kernel<D, T><<<dim3(nqb, p.heads, p.batch), 256, 0, stream>>>(p);
   const int kv_items = (p.sink_blocks * p.sink_segs + (nkb - p.sink_blocks) * p.norm_segs) * slices;
   if (kv_items > 0) {
-    window_dkdv_kernel<D, T><<<kv_items < num_sms ? kv_items : num_sms, K::R::kThreads, K::kSmem, stream>>>(
-        m[0], m[1], m[2], m[3], p, kv_items);
+    window_dkdv_kernel<D, T><<<kv_items, K::R::kThreads, K::kSmem, stream>>>(m[0], m[1], m[2], m[3], p);
     const int joined = p.norm_segs > 1 ? nkb : p.sink_segs > 1 ? p.sink_blocks : 0;
     if (joined > 0) window_join_kernel<D, T><<<dim3(joined, slices), 256, 0, stream>>>(p);
   }
