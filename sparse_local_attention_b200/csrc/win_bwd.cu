@@ -641,6 +641,21 @@ __global__ void __launch_bounds__(256) window_join_kernel(const WinParams p) {
 }
 
 // ----------------------------------------------------------------------- 3. dQ
+struct QueryItem {
+  bool stop;
+  Sequence s;
+  int h, qb, rows, pos0, base, last, nsink, ns, nc;  // rows: 0 for a block that is not there
+  __device__ __forceinline__ void chunk(int j, int &first, int &valid) const {
+    first = j < ns ? j * kBM : base + (j - ns) * kBM;
+    valid = min(kBM, (j < ns ? nsink : last + 1) - first);
+  }
+};
+
+// The warpgroups share each chunk of 128 keys (64 or 32 columns each); dS has
+// columns of its own, so the next chunk's S and dP are computed while dS is
+// formed.  (Halves of 64 keys, as in window_dkdv, were slower here: 867 against
+// 796 us at 8192 tokens, 24 heads, d 128, window 2048, dK and dV included: the
+// products of 64 columns run at 60% of the rate, and nothing waits for room.)
 template <int D>
 struct DqCfg {
   static constexpr uint32_t kTile = kBM * D * 2;
@@ -648,43 +663,36 @@ struct DqCfg {
   using R = Roles<D == 64 ? 4 : 2>;
   // full[S] empty[S] raw[S] q_full q_free s_full s_read ds_ready ds_free acc_done acc_free drain
   static constexpr int kNumBars = 3 * kSlots + 9;
-  static constexpr uint32_t kSmem = (2 + kSlots) * kTile + kNumBars * 8 + 64 + 1024;
+  static constexpr uint32_t kSmem = (2 + kSlots) * kTile + kNumBars * 8 + 64 + ItemRing<QueryItem>::kBytes + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t kTmS = 0, kTmDP = 128, kTmDS = 256, kTmDQ = 320;
   static_assert(kTmDQ + D <= 512, "TMEM budget");
 };
 
-struct QueryItem {
-  Sequence s;
-  int h, qb, pos0, base, last, nsink, ns, nc;
-  __device__ __forceinline__ void chunk(int j, int &first, int &valid) const {
-    first = j < ns ? j * kBM : base + (j - ns) * kBM;
-    valid = min(kBM, (j < ns ? nsink : last + 1) - first);
-  }
-};
-
-__device__ __forceinline__ bool query_item(const WinParams &p, int item, QueryItem &it) {
+__device__ __forceinline__ QueryItem query_item(const WinParams &p, int item) {
+  QueryItem it;
+  it.stop = item < 0;
+  if (it.stop) return it;
   const int slices = p.batch * p.heads, nqb = (p.q_len + kBM - 1) / kBM, slice = item % slices;
   it.qb = nqb - 1 - item / slices;  // the last blocks have the most keys
   it.h = slice % p.heads;
   it.s = sequence(p, slice / p.heads);
-  const int rows = min(kBM, it.s.nq - it.qb * kBM);
-  if (rows <= 0) return false;
+  it.rows = max(0, min(kBM, it.s.nq - it.qb * kBM));
   it.pos0 = it.qb * kBM + it.s.nk - it.s.nq;
-  it.last = min(it.s.nk - 1, it.pos0 + rows - 1);
+  it.last = it.rows > 0 ? min(it.s.nk - 1, it.pos0 + it.rows - 1) : -1;
   const int lo = max(0, it.pos0 - p.window + 1);
   it.base = p.sinks >= lo ? 0 : lo;
   it.nsink = min(p.sinks, it.base);
   it.ns = (it.nsink + kBM - 1) / kBM;
   it.nc = it.last >= 0 ? it.ns + (it.last - it.base + kBM) / kBM : 0;
-  return true;
+  return it;
 }
 
 template <int D, class T>
 __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_do,
-                     const WinParams p, const int n_items) {
+                     const WinParams p) {
   using C = DqCfg<D>;
   using R = typename C::R;
   constexpr int kCW = R::kCols;
@@ -701,9 +709,11 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
   uint64_t *acc_done = q_full + 6, *acc_free = q_full + 7, *drain = q_full + 8;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  ItemRing<QueryItem> ring(tmem_slot + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
+    ring.init(R::kMathWarps + 2);
     for (int i = 0; i < 3 * C::kSlots; ++i) mbar_init(&bars[i], 1);
     mbar_init(q_full, 1);
     mbar_init(q_free, 1);
@@ -734,11 +744,20 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
       tma_prefetch_desc(&tmap_k);
       tma_prefetch_desc(&tmap_v);
       tma_prefetch_desc(&tmap_do);
-      uint32_t ld = 0, items = 0, raw_par = 0, raw_last = 0;
-      bool ok = true;
-      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-        QueryItem it;
-        if (!query_item(p, item, it) || it.nc == 0) continue;
+      uint32_t ld = 0, items = 0, raw_par = 0, raw_last = 0, n = 0;
+      int item = blockIdx.x;
+      bool ok = true, asked = false;
+      while (true) {
+        const QueryItem it = query_item(p, item);
+        if (!ring.put(n, it, ctl, kErrBwdWait)) { ok = false; break; }
+        if (it.stop) break;
+        ring.ask();
+        asked = true;
+        if (it.nc == 0) {
+          if (!ring.take(n++, item, ctl, kErrBwdWait)) { ok = false; break; }
+          asked = false;
+          continue;
+        }
         if (!mbar_wait(q_free, (items & 1) ^ 1, ctl, kErrBwdWait)) { ok = false; break; }
         mbar_arrive_expect_tx(q_full, 2 * C::kTile);
         load_tile<D>(q_s, &tmap_q, it.s.q0 + it.qb * kBM, it.h, it.s.slice, q_full);
@@ -757,6 +776,8 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
           load_tile<D>(slots + slot * C::kTile, (s & 1) ? &tmap_v : &tmap_k, it.s.k0 + first, it.h / p.group, it.s.slice, bar);
           ++ld;
         }
+        if (!ok || !ring.take(n++, item, ctl, kErrBwdWait)) { ok = false; break; }
+        asked = false;
       }
       if (!ok) {
         const uint32_t start = ld > (uint32_t)C::kSlots ? ld - C::kSlots : 0;
@@ -766,14 +787,17 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
           else drain_wait(&full[slot], (i / C::kSlots) & 1);
         }
         if (items > 0) drain_wait(q_full, (items - 1) & 1);
+        if (item >= 0) ring.discard(n, asked);
       }
     }
   } else if (warp == R::kClearWarp) {
     uint32_t ld = 0, raw_par = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      QueryItem it;
-      if (!query_item(p, item, it)) continue;
+    for (uint32_t n = 0;; ++n) {
+      const QueryItem *at = ring.get(n, ok, ctl, kErrBwdWait);
+      if (!at) break;
+      const QueryItem it = *at;
+      ring.release(n, lane);
       for (int j = 0; j < it.nc && ok; ++j) {
         int first, valid;
         it.chunk(j, first, valid);
@@ -785,6 +809,7 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
         clear_rows<D>(slots + slot * C::kTile, valid, (valid + 15) & ~15, lane);
         if (lane == 0) mbar_arrive(&full[slot]);
       }
+      if (!ok) break;
       ld += 2 * it.nc;
     }
   } else if (warp == R::kMmaWarp) {
@@ -795,12 +820,16 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
     const uint64_t sm0 = smem_desc_sw128(smem_u32(slots), kTilePanel, 1024);  // MN-major K
     uint32_t ld = 0, items = 0, ds_waits = 0, r_waits = 0;
     bool ok = true, issued = false;
-    auto issue_s = [&](uint32_t lk) -> bool {
-      const uint32_t lv = lk + 1, ks = lk % C::kSlots, vs = lv % C::kSlots;
-      if (!mbar_wait_w(&full[ks], (lk / C::kSlots) & 1, ctl, kErrBwdWait) ||
-          !mbar_wait_w(&full[vs], (lv / C::kSlots) & 1, ctl, kErrBwdWait))
+    auto wait_pair = [&](uint32_t lk) -> bool {
+      if (!mbar_wait_w(&full[lk % C::kSlots], (lk / C::kSlots) & 1, ctl, kErrBwdWait) ||
+          !mbar_wait_w(&full[(lk + 1) % C::kSlots], ((lk + 1) / C::kSlots) & 1, ctl, kErrBwdWait))
         return false;
       tc_fence_after();
+      return true;
+    };
+    // S = Q K^T and dP = dO V^T for the chunk whose K is load lk and whose V is lk + 1
+    auto issue_s = [&](uint32_t lk) {
+      const uint32_t ks = lk % C::kSlots, vs = (lk + 1) % C::kSlots;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
@@ -813,33 +842,36 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
       }
       mma_commit_w(s_full);
       mma_commit_w(&empty[vs]);  // V is read by dP only
-      return true;
     };
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      QueryItem it;
-      if (!query_item(p, item, it) || it.nc == 0) continue;
+    for (uint32_t n = 0;; ++n) {
+      const QueryItem *at = ring.get(n, ok, ctl, kErrBwdWait);
+      if (!at) break;
+      const QueryItem it = *at;
+      ring.release(n, lane);
+      if (it.nc == 0) continue;
       if (!mbar_wait_w(q_full, items & 1, ctl, kErrBwdWait)) { ok = false; break; }
       tc_fence_after();
-      if (!issue_s(ld)) { ok = false; break; }
+      if (!wait_pair(ld)) { ok = false; break; }
+      issue_s(ld);
       issued = true;
       if (it.nc == 1) mma_commit_w(q_free);
       for (int j = 0; j < it.nc && ok; ++j) {
-        const uint32_t lk = ld + 2 * j;
+        const uint32_t lk = ld + 2 * j, ks = lk % C::kSlots;
+        int first, valid;
+        it.chunk(j, first, valid);
+        const int steps = (valid + 15) / 16;
         if (j + 1 < it.nc) {
-          if (!mbar_wait_w(s_read, r_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
+          // the next chunk's S / dP as soon as this chunk's have been read
+          if (!wait_pair(lk + 2) || !mbar_wait_w(s_read, r_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
           ++r_waits;
           tc_fence_after();
-          if (!issue_s(lk + 2)) { ok = false; break; }
-          if (j + 2 == it.nc) mma_commit_w(q_free);
+          issue_s(lk + 2);
+          if (j + 2 == it.nc) mma_commit_w(q_free);  // Q and dO are no longer read
         }
         if (!mbar_wait_w(ds_ready, ds_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
         ++ds_waits;
         if (j == 0 && items > 0 && !mbar_wait_w(acc_free, (items - 1) & 1, ctl, kErrBwdWait)) { ok = false; break; }
         tc_fence_after();
-        int first, valid;
-        it.chunk(j, first, valid);
-        const int steps = (valid + 15) / 16;
-        const uint32_t ks = lk % C::kSlots;
 #pragma unroll
         for (int kk = 0; kk < kBM / 16; ++kk)
           if (kk < steps)
@@ -861,22 +893,23 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
     // elementwise: thread = query row; warpgroup e owns key columns [kCW e, kCW e + kCW)
     const int e = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
-    const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
-    uint32_t s_waits = 0, f_waits = 0, items = 0, chunks = 0;
+    const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), fac2 = make_float2(fac, fac);
+    uint32_t s_waits = 0, items = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      QueryItem it;
-      if (!query_item(p, item, it)) continue;
+    for (uint32_t n = 0;; ++n) {
+      const QueryItem *at = ring.get(n, ok, ctl, kErrBwdWait);
+      if (!at) break;
+      const QueryItem it = *at;
+      ring.release(n, lane);
+      if (it.rows == 0) continue;
       const int qrow = it.qb * kBM + row;
-      const bool row_valid = qrow < it.s.nq;
       float lse2 = 0.f, dd = 0.f;
-      if (row_valid && it.nc > 0) {
-        const long long at = stat_row(p, it.s, it.h, qrow);
-        lse2 = p.lse[at] * kLog2e, dd = p.dd[at];
+      if (row < it.rows && it.nc > 0) {
+        const long long at_stat = stat_row(p, it.s, it.h, qrow);
+        lse2 = p.lse[at_stat] * kLog2e, dd = p.dd[at_stat];
       }
       const float2 nlse2 = make_float2(-lse2, -lse2), ndd = make_float2(-dd, -dd);
-      const float2 fac2 = make_float2(fac, fac);
-      for (int j = 0; j < it.nc; ++j, ++chunks) {
+      for (int j = 0; j < it.nc; ++j) {
         int first, valid;
         it.chunk(j, first, valid);
         const bool whole = valid == kBM && first + kBM - 1 <= it.pos0 &&
@@ -891,6 +924,11 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
 #pragma unroll
         for (int hf = 0; hf < kCW / 32; ++hf) tmem_ld32(base + C::kTmDP + 32 * hf, rd[hf]);
         tmem_ld_wait();
+#pragma unroll
+        for (int hf = 0; hf < kCW / 32; ++hf) {
+          reg_fence32(rs[hf]);
+          reg_fence32(rd[hf]);
+        }
         if (j + 1 < it.nc) {
           tc_fence_before();
           warp_arrive(s_read, lane);
@@ -899,8 +937,7 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
 #pragma unroll
         for (int hf = 0; hf < kCW / 32; ++hf) {
           const uint32_t bits =
-              whole ? 0xffffffffu
-                    : visible_bits(it.pos0 + row, first, valid, p.window, p.sinks, (kCW / 32) * e + hf);
+              whole ? 0xffffffffu : visible_bits(it.pos0 + row, first, valid, p.window, p.sinks, (kCW / 32) * e + hf);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const float2 t = fma2(make_float2(__uint_as_float(rs[hf][2 * k]), __uint_as_float(rs[hf][2 * k + 1])), sl2, nlse2);
@@ -914,9 +951,9 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
             pd[hf][k] = Elem<T>::pack(dr.x, dr.y);
           }
         }
-        if (chunks > 0) {
-          if (!mbar_wait_w(ds_free, f_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
-          ++f_waits;
+        if (s_waits > 1) {
+          // the dQ products of the chunk before have read its dS
+          if (!mbar_wait_w(ds_free, s_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
           tc_fence_after();
         }
 #pragma unroll
@@ -930,30 +967,31 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
         if (!mbar_wait_w(acc_done, items & 1, ctl, kErrBwdWait)) { ok = false; break; }
         tc_fence_after();
       }
-      constexpr int kOut = D / R::kGroups;  // dQ columns of a warpgroup
-      uint4 *dst = reinterpret_cast<uint4 *>(p.dq.p + 2 * (it.s.slice * p.dq.b + it.h * p.dq.h +
-                                                           (long long)(it.s.q0 + qrow) * p.dq.r + e * kOut));
+      // warpgroup e < D / 32 writes dQ's columns [32 e, 32 e + 32), then 32 kGroups further
       const float mul = p.scale / fac;
 #pragma unroll
-      for (int c = 0; c < kOut / 16; ++c) {
-        uint32_t r[16];
+      for (int c = 0; c < (D / 32 + R::kGroups - 1) / R::kGroups; ++c) {
+        const int col = 32 * (e + c * R::kGroups);
+        if (col >= D) break;
+        uint32_t r[32];
         if (it.nc > 0) {
-          tmem_ld16(tmem + lane_off + C::kTmDQ + e * kOut + c * 16, r);
+          tmem_ld32(tmem + lane_off + C::kTmDQ + col, r);
           tmem_ld_wait();
+          reg_fence32(r);
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) r[i] = 0u;
+          for (int i = 0; i < 32; ++i) r[i] = 0u;
         }
-        if (row_valid) {
+        uint4 w[4];
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = Elem<T>::pack(__uint_as_float(r[8 * v + 2 * i]) * mul, __uint_as_float(r[8 * v + 2 * i + 1]) * mul);
-            dst[c * 2 + v] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+        for (int v = 0; v < 4; ++v) {
+          auto pair = [&](int i) {
+            return Elem<T>::pack(__uint_as_float(r[8 * v + 2 * i]) * mul, __uint_as_float(r[8 * v + 2 * i + 1]) * mul);
+          };
+          w[v] = make_uint4(pair(0), pair(1), pair(2), pair(3));
         }
+        char *dst = p.dq.p + 2 * (it.s.slice * p.dq.b + it.h * p.dq.h + (long long)(it.s.q0 + (qrow & ~3)) * p.dq.r + col);
+        store_quad(w, dst, 2 * p.dq.r, it.rows - (row & ~3), lane);
       }
       if (it.nc > 0) {
         tc_fence_before();
@@ -989,8 +1027,7 @@ cudaError_t launch(const WinParams &p, const CUtensorMap *m, int num_sms, cudaSt
   }
   const int q_items = nqb * p.batch * p.heads;
   if (q_items > 0)
-    window_dq_kernel<D, T><<<q_items < num_sms ? q_items : num_sms, Q::R::kThreads, Q::kSmem, stream>>>(
-        m[0], m[1], m[2], m[3], p, q_items);
+    window_dq_kernel<D, T><<<q_items, Q::R::kThreads, Q::kSmem, stream>>>(m[0], m[1], m[2], m[3], p);
   return cudaGetLastError();
 }
 
