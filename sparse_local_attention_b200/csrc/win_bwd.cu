@@ -12,7 +12,7 @@
 //   2. window_dkdv: an item is a 128-row key block of a key head (or a part of
 //      its queries): K and V stay in shared memory; the 128-row chunks of the
 //      queries that see the block, head after head of the group, stream
-//      through a ring.  S^T = K Q^T and dP^T = V dO^T land in tensor memory,
+//      through rings.  S^T = K Q^T and dP^T = V dO^T land in tensor memory,
 //      the elementwise warps (thread = key row) turn them into P^T and dS^T,
 //      then dV += P^T dO and dK += dS^T Q accumulate in tensor memory.  Blocks
 //      that many queries see (sinks; long sequences of few heads) are cut into
@@ -214,26 +214,33 @@ __device__ __forceinline__ KeyItem key_item(const WinParams &p, int item) {
   return it;
 }
 
-// The two halves of a chunk (64 queries each) are worked on by a warpgroup each
-// and go through tensor memory on their own: while one half's P^T and dS^T are
-// formed, the products of the other one run.  S^T and dP^T of a half take 64
-// columns each and P^T and dS^T lie over the first 32 of them, which with dV and
-// dK at head dim 128 is all there is.
+// S^T, dP^T, dV and dK fill tensor memory at head dim 128, so P^T and dS^T lie
+// over the S^T and dP^T they come from, and each of the two takes its turn
+// while the other one's products run:
+//   tensor core:  dV(i)  S^T(i + 1)  dK(i)  dP^T(i + 1)  dV(i + 1) ...
+//   warps:        dS^T(i) -------->  P^T(i + 1) ------>  dS^T(i + 1) ...
+// A thread's columns lie over its own, so no warp waits for another one to
+// have read: the P^T of columns [kCols e, kCols (e + 1)) takes the first half
+// of them.
 template <int D>
 struct DkvCfg {
   static constexpr uint32_t kTile = kBM * D * 2;
-  using R = Roles<2>;
-  static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr uint32_t kStage = 2 * kTile + kAugBytes;  // Q, dO, the rows' panel
-  static constexpr uint32_t kSel = 2 * kAugBytes;            // selector panels of -LSE / scale and -D
-  // st_full[S] st_empty[S] raw[S] kv_full kv_free s_full[2] p_ready[2] acc_done acc_free drain
-  static constexpr int kNumBars = 3 * kStages + 9;
+  using R = Roles<D == 64 ? 4 : 2>;
+  static constexpr int kStages = D == 128 ? 2 : 4;    // of each ring
+  static constexpr uint32_t kQStage = kTile + kAugBytes;  // Q and the rows' panel
+  static constexpr uint32_t kSel = 2 * kAugBytes;         // selector panels of -LSE / scale and -D
+  // q_full[S] q_empty[S] q_raw[S] do_full[S] do_empty[S] do_raw[S]
+  // kv_full kv_free s_full dp_full p_ready ds_ready acc_done acc_free drain
+  static constexpr int kNumBars = 6 * kStages + 9;
   static constexpr uint32_t kSmem =
-      2 * kTile + kStages * kStage + kSel + kNumBars * 8 + 64 + ItemRing<KeyItem>::kBytes + 1024;
+      2 * kTile + kStages * (kQStage + kTile) + kSel + kNumBars * 8 + 64 + ItemRing<KeyItem>::kBytes + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-  static constexpr uint32_t kTmS = 0, kTmDP = 128;  // half x: + 64 x
-  static constexpr uint32_t kTmDV = 256, kTmDK = kTmDV + D;
+  static constexpr uint32_t kTmS = 0, kTmDP = 128, kTmDV = 256, kTmDK = kTmDV + D;
   static_assert(kTmDK + D <= 512, "TMEM budget");
+  // tensor-memory column of the kk-th 16 queries of P^T (or dS^T) within its 128
+  static __device__ __forceinline__ constexpr uint32_t p_col(int kk) {
+    return 16 * kk / R::kCols * R::kCols + 16 * kk % R::kCols / 2;
+  }
 };
 
 template <int D, class T>
@@ -247,13 +254,16 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *k_s = smem, *v_s = smem + C::kTile;
-  uint8_t *stages = smem + 2 * C::kTile;
-  uint8_t *sel_s = stages + C::kStages * C::kStage;
+  uint8_t *q_st = smem + 2 * C::kTile;  // [stage]{Q tile, panel}
+  uint8_t *do_st = q_st + C::kStages * C::kQStage;
+  uint8_t *sel_s = do_st + C::kStages * C::kTile;
   uint64_t *bars = reinterpret_cast<uint64_t *>(sel_s + C::kSel);
-  uint64_t *st_full = bars, *st_empty = bars + C::kStages, *raw = bars + 2 * C::kStages;
-  uint64_t *kv_full = bars + 3 * C::kStages, *kv_free = kv_full + 1;
-  uint64_t *s_full = kv_full + 2;   // [2] S^T, dP^T of a half are in TMEM
-  uint64_t *p_ready = kv_full + 4;  // [2] its P^T, dS^T written
+  // full, empty, raw of the Q ring, then of the dO ring
+  uint64_t *q_full = bars, *q_empty = bars + C::kStages, *q_raw = bars + 2 * C::kStages;
+  uint64_t *do_full = bars + 3 * C::kStages, *do_empty = bars + 4 * C::kStages, *do_raw = bars + 5 * C::kStages;
+  uint64_t *kv_full = bars + 6 * C::kStages, *kv_free = kv_full + 1;
+  uint64_t *s_full = kv_full + 2, *dp_full = kv_full + 3;    // S^T, dP^T of a chunk are in TMEM
+  uint64_t *p_ready = kv_full + 4, *ds_ready = kv_full + 5;  // P^T, dS^T written
   uint64_t *acc_done = kv_full + 6, *acc_free = kv_full + 7, *drain = kv_full + 8;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -262,16 +272,10 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
 
   if (threadIdx.x == 0) {
     ring.init(R::kMathWarps + 2);
-    for (int i = 0; i < 3 * C::kStages; ++i) mbar_init(&bars[i], 1);
-    mbar_init(kv_full, 1);
-    mbar_init(kv_free, 1);
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_ready[x], 4);
+    for (int i = 0; i < C::kNumBars; ++i) {
+      uint64_t *bar = bars + i;
+      mbar_init(bar, bar == p_ready || bar == ds_ready || bar == acc_free ? R::kMathWarps : 1);
     }
-    mbar_init(acc_done, 1);
-    mbar_init(acc_free, R::kMathWarps);
-    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -306,7 +310,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
       tma_prefetch_desc(&tmap_k);
       tma_prefetch_desc(&tmap_v);
       tma_prefetch_desc(&tmap_do);
-      uint32_t ld = 0, items = 0, raw_par = 0, raw_last = 0, n = 0;
+      uint32_t ld = 0, items = 0, n = 0;
+      uint32_t q_bits = 0, do_bits = 0, raw_par = 0, raw_last = 0;  // loads begun of each ring; per stage: parity of raw, last load went to raw
       int item = blockIdx.x;
       bool ok = true, asked = false;
       while (true) {
@@ -327,28 +332,36 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
         ++items;
         for (int c = it.c0; c < it.c1; ++c) {
           const uint32_t st = ld % C::kStages, ph = (ld / C::kStages) & 1, bit = 1u << st;
-          if (!mbar_wait(&st_empty[st], ph ^ 1, ctl, kErrBwdWait)) { ok = false; break; }
           const int h = it.hk * p.group + c / it.per_head, first = it.first(c);
           const bool clear = it.valid(c) % 16 != 0;
-          uint64_t *bar = clear ? &raw[st] : &st_full[st];
+          if (!mbar_wait(&q_empty[st], ph ^ 1, ctl, kErrBwdWait)) { ok = false; break; }
           raw_last = clear ? raw_last | bit : raw_last & ~bit;
           if (clear) raw_par ^= bit;
-          uint8_t *sb = stages + st * C::kStage;
-          mbar_arrive_expect_tx(bar, C::kStage);
-          load_tile<D>(sb, &tmap_q, it.s.q0 + first, h, it.s.slice, bar);
-          load_tile<D>(sb + C::kTile, &tmap_do, it.s.q0 + first, h, it.s.slice, bar);
-          bulk_load(sb + 2 * C::kTile, p.aug + (aug_row(p, it.s, it.b, h) + first) / 8 * 256, kAugBytes, bar);
+          uint64_t *bar = clear ? &q_raw[st] : &q_full[st];
+          mbar_arrive_expect_tx(bar, C::kQStage);
+          load_tile<D>(q_st + st * C::kQStage, &tmap_q, it.s.q0 + first, h, it.s.slice, bar);
+          bulk_load(q_st + st * C::kQStage + C::kTile, p.aug + (aug_row(p, it.s, it.b, h) + first) / 8 * 256, kAugBytes, bar);
+          ++q_bits;
+          if (!mbar_wait(&do_empty[st], ph ^ 1, ctl, kErrBwdWait)) { ok = false; break; }
+          bar = clear ? &do_raw[st] : &do_full[st];
+          mbar_arrive_expect_tx(bar, C::kTile);
+          load_tile<D>(do_st + st * C::kTile, &tmap_do, it.s.q0 + first, h, it.s.slice, bar);
+          ++do_bits;
           ++ld;
         }
         if (!ok || !ring.take(n++, item, ctl, kErrBwdWait)) { ok = false; break; }
         asked = false;
       }
       if (!ok) {
-        const uint32_t start = ld > (uint32_t)C::kStages ? ld - C::kStages : 0;
-        for (uint32_t i = start; i < ld; ++i) {
-          const uint32_t st = i % C::kStages;
-          if (raw_last >> st & 1) drain_wait(&raw[st], (raw_par >> st & 1) ^ 1);
-          else drain_wait(&st_full[st], (i / C::kStages) & 1);
+        // let the copies already issued land before the CTA exits
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t begun = r ? do_bits : q_bits, start = begun > (uint32_t)C::kStages ? begun - C::kStages : 0;
+          uint64_t *f = r ? do_full : q_full, *w = r ? do_raw : q_raw;
+          for (uint32_t i = start; i < begun; ++i) {
+            const uint32_t st = i % C::kStages;
+            if (raw_last >> st & 1) drain_wait(&w[st], (raw_par >> st & 1) ^ 1);
+            else drain_wait(&f[st], (i / C::kStages) & 1);
+          }
         }
         if (items > 0) drain_wait(kv_full, (items - 1) & 1);
         if (item >= 0) ring.discard(n, asked);
@@ -365,50 +378,52 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
       for (int c = it.c0; c < it.c1 && ok; ++c, ++ld) {
         const int valid = it.valid(c);
         if (valid % 16 == 0) continue;
-        const uint32_t st = ld % C::kStages;
-        ok = mbar_wait_w(&raw[st], raw_par >> st & 1, ctl, kErrBwdWait);
+        const uint32_t st = ld % C::kStages, par = raw_par >> st & 1;
+        const int upto = (valid + 15) & ~15;
+        ok = mbar_wait_w(&q_raw[st], par, ctl, kErrBwdWait);
+        if (!ok) break;
+        clear_rows<D>(q_st + st * C::kQStage, valid, upto, lane);
+        if (lane == 0) mbar_arrive(&q_full[st]);
+        ok = mbar_wait_w(&do_raw[st], par, ctl, kErrBwdWait);
         raw_par ^= 1u << st;
         if (!ok) break;
-        const int upto = (valid + 15) & ~15;
-        clear_rows<D>(stages + st * C::kStage, valid, upto, lane);
-        clear_rows<D>(stages + st * C::kStage + C::kTile, valid, upto, lane);
-        if (lane == 0) mbar_arrive(&st_full[st]);
+        clear_rows<D>(do_st + st * C::kTile, valid, upto, lane);
+        if (lane == 0) mbar_arrive(&do_full[st]);
       }
       if (!ok) break;
     }
   } else if (warp == R::kMmaWarp) {
-    constexpr uint32_t idesc_ss = idesc_for<T>(kBM, 64, false, false);
+    constexpr uint32_t idesc_ss = idesc_for<T>(kBM, kBM, false, false);
     constexpr uint32_t idesc_acc = idesc_for<T>(kBM, D, false, true);
     const uint64_t kd = smem_desc_sw128(smem_u32(k_s), 16, 1024), vd = smem_desc_sw128(smem_u32(v_s), 16, 1024);
-    const uint64_t sk0 = smem_desc_sw128(smem_u32(stages), 16, 1024);         // K-major Q / dO
-    const uint64_t sm0 = smem_desc_sw128(smem_u32(stages), kTilePanel, 1024);  // MN-major Q / dO
+    const uint64_t qk0 = smem_desc_sw128(smem_u32(q_st), 16, 1024), qm0 = smem_desc_sw128(smem_u32(q_st), kTilePanel, 1024);
+    const uint64_t gk0 = smem_desc_sw128(smem_u32(do_st), 16, 1024), gm0 = smem_desc_sw128(smem_u32(do_st), kTilePanel, 1024);
     const uint64_t sel_l = smem_desc_plain(smem_u32(sel_s), 128, 256);
     const uint64_t sel_d = smem_desc_plain(smem_u32(sel_s) + kAugBytes, 128, 256);
-    const uint64_t aug0 = smem_desc_plain(smem_u32(stages + 2 * C::kTile), 128, 256);
-    constexpr uint32_t kHalfRows = 64 * 128 >> 4, kHalfAug = kAugBytes / 2 >> 4;  // of descriptors, to the second half
-    uint32_t ld = 0, items = 0, p_waits[2] = {0, 0};
+    const uint64_t aug0 = smem_desc_plain(smem_u32(q_st + C::kTile), 128, 256);
+    uint32_t ld = 0, items = 0, waits = 0;
     bool ok = true, issued = false;
-    // S^T = K Q^T - LSE / scale and dP^T = V dO^T - D for half x of the chunk in stage st
-    auto issue_s = [&](int x, uint32_t st) {
-      const uint32_t so = ((st * C::kStage) >> 4) + x * kHalfRows, dso = so + (C::kTile >> 4);
-      const uint64_t aug = aug0 + ((st * C::kStage) >> 4) + x * kHalfAug;
-      const uint32_t s_tm = tmem + C::kTmS + 64 * x, d_tm = tmem + C::kTmDP + 64 * x;
+    auto issue_s = [&](uint32_t st) {  // S^T = K Q^T - LSE / scale
+      const uint32_t so = (st * C::kQStage) >> 4;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
-        mma_ss_w(s_tm, kd + off, sk0 + so + off, idesc_ss, kk > 0 ? 1u : 0u);
+        mma_ss_w(tmem + C::kTmS, kd + off, qk0 + so + off, idesc_ss, kk > 0 ? 1u : 0u);
       }
-      mma_ss_w(s_tm, sel_l, aug, idesc_ss, 1u);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
-        mma_ss_w(d_tm, vd + off, sk0 + dso + off, idesc_ss, kk > 0 ? 1u : 0u);
-      }
-      mma_ss_w(d_tm, sel_d, aug, idesc_ss, 1u);
-      mma_commit_w(&s_full[x]);
+      mma_ss_w(tmem + C::kTmS, sel_l, aug0 + so, idesc_ss, 1u);
+      mma_commit_w(s_full);
     };
-    auto wait_stage = [&](uint32_t l) -> bool {
-      if (!mbar_wait_w(&st_full[l % C::kStages], (l / C::kStages) & 1, ctl, kErrBwdWait)) return false;
+    auto issue_dp = [&](uint32_t st) {  // dP^T = V dO^T - D
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
+        mma_ss_w(tmem + C::kTmDP, vd + off, gk0 + ((st * C::kTile) >> 4) + off, idesc_ss, kk > 0 ? 1u : 0u);
+      }
+      mma_ss_w(tmem + C::kTmDP, sel_d, aug0 + ((st * C::kQStage) >> 4), idesc_ss, 1u);
+      mma_commit_w(dp_full);
+    };
+    auto wait_full = [&](uint64_t *full, uint32_t l) -> bool {
+      if (!mbar_wait_w(&full[l % C::kStages], (l / C::kStages) & 1, ctl, kErrBwdWait)) return false;
       tc_fence_after();
       return true;
     };
@@ -421,49 +436,40 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
       if (n == 0) continue;
       if (!mbar_wait_w(kv_full, items & 1, ctl, kErrBwdWait)) { ok = false; break; }
       tc_fence_after();
-      if (!wait_stage(ld)) { ok = false; break; }
-      int valid = it.valid(it.c0);
-      issue_s(0, ld % C::kStages);
-      if (valid > 64) issue_s(1, ld % C::kStages);
-      if (n == 1) mma_commit_w(kv_free);
+      if (!wait_full(q_full, ld)) { ok = false; break; }
+      issue_s(ld % C::kStages);
       issued = true;
-      bool first = true;
-      for (int i = 0; i < n && ok; ++i) {
-        const uint32_t cur = ld + i, st = cur % C::kStages;
-        const int next = i + 1 < n ? it.valid(it.c0 + i + 1) : 0;
-        const uint32_t so = (st * C::kStage) >> 4, dso = so + (C::kTile >> 4);
-        bool there = false;  // the next chunk's stage has been waited for
+      if (!wait_full(do_full, ld)) { ok = false; break; }
+      issue_dp(ld % C::kStages);
+      if (n == 1) mma_commit_w(kv_free);
+      for (int i = 0; i < n && ok; ++i, ++waits) {
+        const uint32_t cur = ld + i, st = cur % C::kStages, st1 = (cur + 1) % C::kStages;
+        const bool more = i + 1 < n;
+        const int steps = (it.valid(it.c0 + i) + 15) / 16;
+        if (more && !wait_full(q_full, cur + 1)) { ok = false; break; }
+        if (!mbar_wait_w(p_ready, waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
+        if (i == 0 && items > 0 && !mbar_wait_w(acc_free, (items - 1) & 1, ctl, kErrBwdWait)) { ok = false; break; }
+        tc_fence_after();
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (valid > 64 * x) {
-            if (!mbar_wait_w(&p_ready[x], p_waits[x] & 1, ctl, kErrBwdWait)) { ok = false; break; }
-            ++p_waits[x];
-            if (first && items > 0 && !mbar_wait_w(acc_free, (items - 1) & 1, ctl, kErrBwdWait)) { ok = false; break; }
-            tc_fence_after();
-            // dV += P^T dO, dK += dS^T Q over the half's valid rows
-            const int steps = min(4, (valid - 64 * x + 15) / 16);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              if (kk < steps)
-                mma_ts_w(tmem + C::kTmDV, tmem + C::kTmS + 64 * x + kk * 8, sm0 + dso + x * kHalfRows + ((kk * 16 * 128) >> 4),
-                         idesc_acc, first && kk == 0 ? 0u : 1u);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              if (kk < steps)
-                mma_ts_w(tmem + C::kTmDK, tmem + C::kTmDP + 64 * x + kk * 8, sm0 + so + x * kHalfRows + ((kk * 16 * 128) >> 4),
-                         idesc_acc, first && kk == 0 ? 0u : 1u);
-            first = false;
-            if (x == 1 || valid <= 64) mma_commit_w(&st_empty[st]);
-          }
-          // the half's next S^T / dP^T take the place of the P^T / dS^T just read
-          if (next > 64 * x) {
-            if (!there && !wait_stage(cur + 1)) { ok = false; break; }
-            there = true;
-            issue_s(x, (cur + 1) % C::kStages);
-          }
+        for (int kk = 0; kk < kBM / 16; ++kk)
+          if (kk < steps)
+            mma_ts_w(tmem + C::kTmDV, tmem + C::kTmS + C::p_col(kk), gm0 + ((st * C::kTile + kk * 16 * 128) >> 4), idesc_acc,
+                     (i > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_w(&do_empty[st]);
+        if (more) {
+          issue_s(st1);  // over the P^T just read
+          if (!wait_full(do_full, cur + 1)) { ok = false; break; }
         }
+        if (!mbar_wait_w(ds_ready, waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kBM / 16; ++kk)
+          if (kk < steps)
+            mma_ts_w(tmem + C::kTmDK, tmem + C::kTmDP + C::p_col(kk), qm0 + ((st * C::kQStage + kk * 16 * 128) >> 4), idesc_acc,
+                     (i > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_w(&q_empty[st]);
+        if (more) issue_dp(st1);  // over the dS^T just read
         if (i + 2 == n) mma_commit_w(kv_free);  // K and V are no longer read
-        valid = next;
       }
       if (!ok) break;
       ld += n;
@@ -475,15 +481,15 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
       drain_wait(drain, 0);
     }
   } else {
-    // elementwise: warpgroup x works on half x; thread = key row of the block
-    const int x = warp >> 2, row = (warp & 3) * 32 + lane;
+    // elementwise: thread = key row; warpgroup e owns query columns [kCW e, kCW e + kCW) of each chunk
+    const int e = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2), shift = make_float2(kPShift<T>, kPShift<T>);
     // dS = P (dP - D), with P's own factor taken out again
     const float ds_mul = kIsHalf<T> ? fac * exp2f(-kPShift<T>) : 1.f;
     const float2 dsm = make_float2(ds_mul, ds_mul);
-    const uint32_t s_tm = tmem + lane_off + C::kTmS + 64 * x, d_tm = tmem + lane_off + C::kTmDP + 64 * x;
-    uint32_t s_waits = 0, items = 0;
+    const uint32_t s_tm = tmem + lane_off + C::kTmS + kCW * e, d_tm = tmem + lane_off + C::kTmDP + kCW * e;
+    uint32_t waits = 0, items = 0;
     bool ok = true;
     for (uint32_t n = 0;; ++n) {
       const KeyItem *at = ring.get(n, ok, ctl, kErrBwdWait);
@@ -491,83 +497,91 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
       const KeyItem it = *at;
       ring.release(n, lane);
       const int key = it.key0 + row, off = it.s.nk - it.s.nq;
-      for (int c = it.c0; c < it.c1; ++c) {
-        const int valid = it.valid(c) - 64 * x, qpos = it.first(c) + 64 * x + off;
-        if (valid <= 0) continue;
-        // whole: the half's 64 queries see all 128 keys
-        const bool whole = valid >= 64 && qpos >= it.key0 + kBM - 1 &&
-                           (qpos + 63 < it.key0 + p.window || it.key0 + kBM <= p.sinks);
-        const int c_lo = key - qpos;  // columns below do not see this key
-        const int c_hi = min(min(valid, 64), key < p.sinks ? 64 : key - qpos + p.window);
-        if (!mbar_wait_w(&s_full[x], s_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
-        ++s_waits;
+      for (int c = it.c0; c < it.c1; ++c, ++waits) {
+        const int valid = it.valid(c), qpos = it.first(c) + off;
+        // whole: all 128 queries see all 128 keys
+        const bool whole = valid == kBM && qpos >= it.key0 + kBM - 1 &&
+                           (qpos + kBM - 1 < it.key0 + p.window || it.key0 + kBM <= p.sinks);
+        const int c_lo = key - qpos - kCW * e;  // columns below do not see this key
+        const int c_hi = min(valid, key < p.sinks ? kBM : min(kBM, key - qpos + p.window)) - kCW * e;
+        if (!mbar_wait_w(s_full, waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
         tc_fence_after();
-        uint32_t pp[2][16], pd[2][16];
-        // 16 columns from q0 on, from their raw S^T and dP^T
-        auto form = [&](int q0, const uint32_t(&rs)[16], const uint32_t(&rd)[16]) {
-          const uint32_t bits = whole ? 0xffffu : bits_below(c_hi - q0) & ~bits_below(c_lo - q0);
+        float2 pr[kCW / 2];
+        uint32_t bits[kCW / 32];
+        uint32_t r[kCW / 32][32];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int w = q0 / 2 + k;
-            const float2 sv = make_float2(__uint_as_float(rs[2 * k]), __uint_as_float(rs[2 * k + 1]));
+        for (int g = 0; g < kCW / 32; ++g) tmem_ld32(s_tm + 32 * g, r[g]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int g = 0; g < kCW / 32; ++g) reg_fence32(r[g]);
+#pragma unroll
+        for (int g = 0; g < kCW / 32; ++g) {
+          bits[g] = whole ? 0xffffffffu : bits_below(c_hi - 32 * g) & ~bits_below(c_lo - 32 * g);
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 sv = make_float2(__uint_as_float(r[g][2 * k]), __uint_as_float(r[g][2 * k + 1]));
             const float2 t = kIsHalf<T> ? fma2(sv, sl2, shift) : mul2(sv, sl2);
-            float2 pr = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-            float2 dr = mul2(pr, make_float2(__uint_as_float(rd[2 * k]), __uint_as_float(rd[2 * k + 1])));
-            if (kIsHalf<T>) dr = mul2(dr, dsm);
+            float2 x = make_float2(ex2_approx(t.x), ex2_approx(t.y));
             if (!whole) {
-              if (!(bits & (1u << (2 * k)))) pr.x = 0.f, dr.x = 0.f;
-              if (!(bits & (2u << (2 * k)))) pr.y = 0.f, dr.y = 0.f;
+              if (!(bits[g] & (1u << (2 * k)))) x.x = 0.f;
+              if (!(bits[g] & (2u << (2 * k)))) x.y = 0.f;
             }
-            pp[w >> 4][w & 15] = Elem<T>::pack(pr.x, pr.y);
-            pd[w >> 4][w & 15] = Elem<T>::pack(dr.x, dr.y);
+            pr[16 * g + k] = x;
+            w[k] = Elem<T>::pack(x.x, x.y);
           }
-        };
-        {
-          // four quarters of 16 columns, the next quarter's load in flight
-          uint32_t s0[16], d0[16], s1[16], d1[16];
-          tmem_ld16(s_tm, s0);
-          tmem_ld16(d_tm, d0);
-          tmem_ld_wait_regs(s0, d0);
-          tmem_ld16(s_tm + 16, s1);
-          tmem_ld16(d_tm + 16, d1);
-          form(0, s0, d0);
-          tmem_ld_wait_regs(s1, d1);
-          tmem_ld16(s_tm + 32, s0);
-          tmem_ld16(d_tm + 32, d0);
-          form(16, s1, d1);
-          tmem_ld_wait_regs(s0, d0);
-          tmem_ld16(s_tm + 48, s1);
-          tmem_ld16(d_tm + 48, d1);
-          // the first 32 columns have been read by this lane, the only one that does
-          tmem_st16(s_tm, pp[0]);
-          tmem_st16(d_tm, pd[0]);
-          form(32, s0, d0);
-          tmem_ld_wait_regs(s1, d1);
-          form(48, s1, d1);
+          tmem_st16(s_tm + 16 * g, w);
         }
-        tmem_st16(s_tm + 16, pp[1]);
-        tmem_st16(d_tm + 16, pd[1]);
         tmem_st_wait();
         tc_fence_before();
-        warp_arrive(&p_ready[x], lane);
+        warp_arrive(p_ready, lane);
+        if (!mbar_wait_w(dp_full, waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int g = 0; g < kCW / 32; ++g) tmem_ld32(d_tm + 32 * g, r[g]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int g = 0; g < kCW / 32; ++g) reg_fence32(r[g]);
+#pragma unroll
+        for (int g = 0; g < kCW / 32; ++g) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float2 x = mul2(pr[16 * g + k], make_float2(__uint_as_float(r[g][2 * k]), __uint_as_float(r[g][2 * k + 1])));
+            if (kIsHalf<T>) x = mul2(x, dsm);
+            if (!whole) {
+              // what is not seen may be anything, times a P of zero
+              if (!(bits[g] & (1u << (2 * k)))) x.x = 0.f;
+              if (!(bits[g] & (2u << (2 * k)))) x.y = 0.f;
+            }
+            w[k] = Elem<T>::pack(x.x, x.y);
+          }
+          tmem_st16(d_tm + 16 * g, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(ds_ready, lane);
       }
       if (!ok) break;
-      // epilogue: warpgroup 0 writes dV, 1 dK
       if (it.rows <= 0) continue;
       const bool any = it.c0 < it.c1;
       if (any) {
         if (!mbar_wait_w(acc_done, items & 1, ctl, kErrBwdWait)) { ok = false; break; }
         tc_fence_after();
       }
-      const uint32_t col = x ? C::kTmDK : C::kTmDV;
-      const float mul = x ? p.scale / fac : exp2f(-kPShift<T>);
-      const Rows &out = x ? p.dk : p.dv;
-      char *dst = out.p + 2 * (it.s.slice * out.b + it.hk * out.h + (long long)(it.s.k0 + (key & ~3)) * out.r);
+      // epilogue: the first half of the warpgroups writes dV, the second half dK, kOut columns each
+      constexpr int kHalf = R::kGroups / 2, kOut = D / kHalf;
+      static_assert(kOut % 32 == 0, "whole 32-column TMEM loads");
+      const int which = e / kHalf, part = e % kHalf;
+      const uint32_t col = (which ? C::kTmDK : C::kTmDV) + part * kOut;
+      const float mul = which ? p.scale / fac : exp2f(-kPShift<T>);
+      const Rows &out = which ? p.dk : p.dv;
+      char *dst = out.p + 2 * (it.s.slice * out.b + it.hk * out.h + (long long)(it.s.k0 + (key & ~3)) * out.r + part * kOut);
       const int quad_rows = it.rows - (row & ~3);
       // the parts' sums, four columns of all rows behind one another
-      float4 *sums = reinterpret_cast<float4 *>(p.parts) + (it.slot * 2 + x) * (kBM * D / 4) + row;
+      float4 *sums = reinterpret_cast<float4 *>(p.parts) + ((it.slot * 2 + which) * (D / 4) + part * kOut / 4) * kBM + row;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < kOut / 32; ++c) {
         uint32_t r[32];
         if (any) {
           tmem_ld32(tmem + lane_off + col + c * 32, r);
