@@ -269,6 +269,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   ItemRing<KeyItem> ring(tmem_slot + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // window_dq may take the SMs that find no item any more
+  asm volatile("griddepcontrol.launch_dependents;");
 
   if (threadIdx.x == 0) {
     ring.init(R::kMathWarps + 2);
@@ -1022,6 +1024,8 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // this grid does not end before window_dkdv, which may still be running
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int D, class T>
@@ -1036,12 +1040,21 @@ cudaError_t launch(const WinParams &p, const CUtensorMap *m, int num_sms, cudaSt
   const int kv_items = (p.sink_blocks * p.sink_segs + (nkb - p.sink_blocks) * p.norm_segs) * slices;
   if (kv_items > 0) {
     window_dkdv_kernel<D, T><<<kv_items, K::R::kThreads, K::kSmem, stream>>>(m[0], m[1], m[2], m[3], p);
-    const int joined = p.norm_segs > 1 ? nkb : p.sink_segs > 1 ? p.sink_blocks : 0;
-    if (joined > 0) window_join_kernel<D, T><<<dim3(joined, slices), 256, 0, stream>>>(p);
   }
   const int q_items = nqb * p.batch * p.heads;
-  if (q_items > 0)
-    window_dq_kernel<D, T><<<q_items, Q::R::kThreads, Q::kSmem, stream>>>(m[0], m[1], m[2], m[3], p);
+  if (q_items > 0) {
+    // It needs nothing of window_dkdv, so it starts while that one's last items
+    // run (their SMs free up one by one over about an item's time).
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(q_items), cfg.blockDim = dim3(Q::R::kThreads), cfg.dynamicSmemBytes = Q::kSmem, cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr, cfg.numAttrs = kv_items > 0 ? 1 : 0;
+    if (const cudaError_t e = cudaLaunchKernelEx(&cfg, window_dq_kernel<D, T>, m[0], m[1], m[2], m[3], p)) return e;
+  }
+  const int joined = kv_items == 0 ? 0 : p.norm_segs > 1 ? nkb : p.sink_segs > 1 ? p.sink_blocks : 0;
+  if (joined > 0) window_join_kernel<D, T><<<dim3(joined, slices), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
