@@ -668,21 +668,31 @@ struct QueryItem {
 };
 
 // The warpgroups share each chunk of 128 keys (64 or 32 columns each); dS has
-// columns of its own, so the next chunk's S and dP are computed while dS is
-// formed.  (Halves of 64 keys, as in window_dkdv, were slower here: 867 against
+// columns of its own.  At head dim 128 S and dP take turns: P is formed while dP
+// is being computed, dS while the next chunk's S is.  At head dim 64 the products
+// are short and the waits are what counts, so both are handed over at once (2
+// sequences of 4096, 16 heads, window 512: 149 against 152 us, dK and dV
+// included; at 128, 8192 tokens, 24 heads without a window: 1425 in turns
+// against 1562 us).  (Halves of 64 keys, as in window_dkdv, were slower here: 867 against
 // 796 us at 8192 tokens, 24 heads, d 128, window 2048, dK and dV included: the
 // products of 64 columns run at 60% of the rate, and nothing waits for room.)
 template <int D>
 struct DqCfg {
   static constexpr uint32_t kTile = kBM * D * 2;
-  static constexpr int kSlots = D == 128 ? 4 : 8;
+  // Slots of a chunk's K and of its V: K is held until dQ has read it, and the
+  // one after the next must be there by then.
+  static constexpr int kSlotsK = D == 128 ? 3 : 4, kSlotsV = D == 128 ? 2 : 4, kSlots = kSlotsK + kSlotsV;
   using R = Roles<D == 64 ? 4 : 2>;
-  // full[S] empty[S] raw[S] q_full q_free s_full s_read ds_ready ds_free acc_done acc_free drain
-  static constexpr int kNumBars = 3 * kSlots + 9;
+  // full[S] empty[S] raw[S] q_full q_free s_full s_read dp_full dp_read ds_ready ds_free acc_done acc_free drain
+  static constexpr int kNumBars = 3 * kSlots + 11;
   static constexpr uint32_t kSmem = (2 + kSlots) * kTile + kNumBars * 8 + 64 + ItemRing<QueryItem>::kBytes + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
   static constexpr uint32_t kTmS = 0, kTmDP = 128, kTmDS = 256, kTmDQ = 320;
   static_assert(kTmDQ + D <= 512, "TMEM budget");
+  static constexpr bool kTurns = D == 128;
+  // Load l is K (even) or V (odd) of chunk l / 2 of the CTA's.
+  static __device__ __forceinline__ uint32_t slot(uint32_t l) { return l & 1 ? kSlotsK + l / 2 % kSlotsV : l / 2 % kSlotsK; }
+  static __device__ __forceinline__ uint32_t phase(uint32_t l) { return l / 2 / (l & 1 ? kSlotsV : kSlotsK) & 1; }
 };
 
 __device__ __forceinline__ QueryItem query_item(const WinParams &p, int item) {
@@ -718,11 +728,11 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(slots + C::kSlots * C::kTile);
   uint64_t *full = bars, *empty = bars + C::kSlots, *raw = bars + 2 * C::kSlots;
   uint64_t *q_full = bars + 3 * C::kSlots, *q_free = q_full + 1;
-  uint64_t *s_full = q_full + 2;    // S, dP of a chunk are in TMEM
-  uint64_t *s_read = q_full + 3;    // ... and have been read
-  uint64_t *ds_ready = q_full + 4;  // dS written
-  uint64_t *ds_free = q_full + 5;   // the dQ products have read it
-  uint64_t *acc_done = q_full + 6, *acc_free = q_full + 7, *drain = q_full + 8;
+  uint64_t *s_full = q_full + 2, *s_read = q_full + 3;    // S of a chunk is in TMEM, has been read
+  uint64_t *dp_full = q_full + 4, *dp_read = q_full + 5;  // dP
+  uint64_t *ds_ready = q_full + 6;                        // dS written
+  uint64_t *ds_free = q_full + 7;                         // the dQ products have read it
+  uint64_t *acc_done = q_full + 8, *acc_free = q_full + 9, *drain = q_full + 10;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   ItemRing<QueryItem> ring(tmem_slot + 16);
@@ -730,16 +740,11 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
 
   if (threadIdx.x == 0) {
     ring.init(R::kMathWarps + 2);
-    for (int i = 0; i < 3 * C::kSlots; ++i) mbar_init(&bars[i], 1);
-    mbar_init(q_full, 1);
-    mbar_init(q_free, 1);
-    mbar_init(s_full, 1);
-    mbar_init(s_read, R::kMathWarps);
-    mbar_init(ds_ready, R::kMathWarps);
-    mbar_init(ds_free, 1);
-    mbar_init(acc_done, 1);
-    mbar_init(acc_free, R::kMathWarps);
-    mbar_init(drain, 1);
+    for (int i = 0; i < C::kNumBars; ++i) {
+      uint64_t *bar = bars + i;
+      const bool by_math = bar == s_read || bar == dp_read || bar == ds_ready || bar == acc_free;
+      mbar_init(bar, by_math ? R::kMathWarps : 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -782,8 +787,8 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
         for (int s = 0; s < 2 * it.nc; ++s) {  // K0 V0 K1 V1 ...
           int first, valid;
           it.chunk(s >> 1, first, valid);
-          const uint32_t slot = ld % C::kSlots, phase = (ld / C::kSlots) & 1, bit = 1u << slot;
-          if (!mbar_wait(&empty[slot], phase ^ 1, ctl, kErrBwdWait)) { ok = false; break; }
+          const uint32_t slot = C::slot(ld), bit = 1u << slot;
+          if (!mbar_wait(&empty[slot], C::phase(ld) ^ 1, ctl, kErrBwdWait)) { ok = false; break; }
           const bool clear = !(s & 1) && valid % 16 != 0;
           uint64_t *bar = clear ? &raw[slot] : &full[slot];
           raw_last = clear ? raw_last | bit : raw_last & ~bit;
@@ -796,11 +801,12 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
         asked = false;
       }
       if (!ok) {
-        const uint32_t start = ld > (uint32_t)C::kSlots ? ld - C::kSlots : 0;
+        const uint32_t start = ld > 2u * C::kSlotsK ? ld - 2 * C::kSlotsK : 0;
         for (uint32_t i = start; i < ld; ++i) {
-          const uint32_t slot = i % C::kSlots;
+          const uint32_t slot = C::slot(i);
+          if (ld - i > 2u * (i % 2 ? C::kSlotsV : C::kSlotsK)) continue;  // its slot has been loaded again
           if (raw_last >> slot & 1) drain_wait(&raw[slot], (raw_par >> slot & 1) ^ 1);
-          else drain_wait(&full[slot], (i / C::kSlots) & 1);
+          else drain_wait(&full[slot], C::phase(i));
         }
         if (items > 0) drain_wait(q_full, (items - 1) & 1);
         if (item >= 0) ring.discard(n, asked);
@@ -818,7 +824,7 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
         int first, valid;
         it.chunk(j, first, valid);
         if (valid % 16 == 0) continue;
-        const uint32_t slot = (ld + 2 * j) % C::kSlots;
+        const uint32_t slot = C::slot(ld + 2 * j);
         ok = mbar_wait_w(&raw[slot], raw_par >> slot & 1, ctl, kErrBwdWait);
         raw_par ^= 1u << slot;
         if (!ok) break;
@@ -836,28 +842,25 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
     const uint64_t sm0 = smem_desc_sw128(smem_u32(slots), kTilePanel, 1024);  // MN-major K
     uint32_t ld = 0, items = 0, ds_waits = 0, r_waits = 0;
     bool ok = true, issued = false;
-    auto wait_pair = [&](uint32_t lk) -> bool {
-      if (!mbar_wait_w(&full[lk % C::kSlots], (lk / C::kSlots) & 1, ctl, kErrBwdWait) ||
-          !mbar_wait_w(&full[(lk + 1) % C::kSlots], ((lk + 1) / C::kSlots) & 1, ctl, kErrBwdWait))
-        return false;
+    auto wait_slot = [&](uint32_t l) -> bool {
+      if (!mbar_wait_w(&full[C::slot(l)], C::phase(l), ctl, kErrBwdWait)) return false;
       tc_fence_after();
       return true;
     };
-    // S = Q K^T and dP = dO V^T for the chunk whose K is load lk and whose V is lk + 1
-    auto issue_s = [&](uint32_t lk) {
-      const uint32_t ks = lk % C::kSlots, vs = (lk + 1) % C::kSlots;
+    // S = Q K^T of the K in load l, dP = dO V^T of the V in load l
+    auto issue = [&](uint32_t tm, uint64_t a, uint32_t l, uint64_t *done) {
+      const uint32_t so = (C::slot(l) * C::kTile) >> 4;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
-        mma_ss_w(tmem + C::kTmS, qd + off, sk0 + ((ks * C::kTile) >> 4) + off, idesc_ss, kk > 0 ? 1u : 0u);
+        mma_ss_w(tm, a + off, sk0 + so + off, idesc_ss, kk > 0 ? 1u : 0u);
       }
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
-        mma_ss_w(tmem + C::kTmDP, dod + off, sk0 + ((vs * C::kTile) >> 4) + off, idesc_ss, kk > 0 ? 1u : 0u);
-      }
-      mma_commit_w(s_full);
-      mma_commit_w(&empty[vs]);  // V is read by dP only
+      if (done) mma_commit_w(done);
+    };
+    auto issue_s = [&](uint32_t lk) { issue(tmem + C::kTmS, qd, lk, C::kTurns ? s_full : nullptr); };
+    auto issue_dp = [&](uint32_t lv) {
+      issue(tmem + C::kTmDP, dod, lv, dp_full);
+      mma_commit_w(&empty[C::slot(lv)]);  // V is read by dP only
     };
     for (uint32_t n = 0;; ++n) {
       const QueryItem *at = ring.get(n, ok, ctl, kErrBwdWait);
@@ -867,21 +870,27 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
       if (it.nc == 0) continue;
       if (!mbar_wait_w(q_full, items & 1, ctl, kErrBwdWait)) { ok = false; break; }
       tc_fence_after();
-      if (!wait_pair(ld)) { ok = false; break; }
+      if (!wait_slot(ld)) { ok = false; break; }
       issue_s(ld);
       issued = true;
+      if (!wait_slot(ld + 1)) { ok = false; break; }
+      issue_dp(ld + 1);
       if (it.nc == 1) mma_commit_w(q_free);
       for (int j = 0; j < it.nc && ok; ++j) {
-        const uint32_t lk = ld + 2 * j, ks = lk % C::kSlots;
+        const uint32_t lk = ld + 2 * j, ks = C::slot(lk);
         int first, valid;
         it.chunk(j, first, valid);
         const int steps = (valid + 15) / 16;
         if (j + 1 < it.nc) {
-          // the next chunk's S / dP as soon as this chunk's have been read
-          if (!wait_pair(lk + 2) || !mbar_wait_w(s_read, r_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
-          ++r_waits;
+          // the next chunk's S and dP as soon as this chunk's have been read
+          if (!wait_slot(lk + 2) || (!C::kTurns && !wait_slot(lk + 3))) { ok = false; break; }
+          if (!mbar_wait_w(C::kTurns ? s_read : dp_read, r_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
           tc_fence_after();
           issue_s(lk + 2);
+          if (C::kTurns && (!wait_slot(lk + 3) || !mbar_wait_w(dp_read, r_waits & 1, ctl, kErrBwdWait))) { ok = false; break; }
+          ++r_waits;
+          tc_fence_after();
+          issue_dp(lk + 3);
           if (j + 2 == it.nc) mma_commit_w(q_free);  // Q and dO are no longer read
         }
         if (!mbar_wait_w(ds_ready, ds_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
@@ -930,43 +939,61 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
         it.chunk(j, first, valid);
         const bool whole = valid == kBM && first + kBM - 1 <= it.pos0 &&
                            (first > it.pos0 + kBM - 1 - p.window || first + kBM <= p.sinks);
-        if (!mbar_wait_w(s_full, s_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
+        if (!mbar_wait_w(C::kTurns ? s_full : dp_full, s_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
         ++s_waits;
         tc_fence_after();
-        uint32_t rs[kCW / 32][32], rd[kCW / 32][32];
+        uint32_t r[kCW / 32][32], rd[kCW / 32][32];
         const uint32_t base = tmem + lane_off + kCW * e;
+        auto load = [&](uint32_t(&v)[kCW / 32][32], uint32_t tm) {
 #pragma unroll
-        for (int hf = 0; hf < kCW / 32; ++hf) tmem_ld32(base + C::kTmS + 32 * hf, rs[hf]);
+          for (int g = 0; g < kCW / 32; ++g) tmem_ld32(tm + 32 * g, v[g]);
+        };
+        // the loads are done: what they read may be written once every warp says so
+        auto loaded = [&](uint64_t *read) {
+          tmem_ld_wait();
 #pragma unroll
-        for (int hf = 0; hf < kCW / 32; ++hf) tmem_ld32(base + C::kTmDP + 32 * hf, rd[hf]);
-        tmem_ld_wait();
+          for (int g = 0; g < kCW / 32; ++g) {
+            if (!C::kTurns || read == s_read) reg_fence32(r[g]);
+            if (!C::kTurns || read == dp_read) reg_fence32(rd[g]);
+          }
+          if (j + 1 < it.nc) {
+            tc_fence_before();
+            warp_arrive(read, lane);
+          }
+        };
+        load(r, base + C::kTmS);
+        if (!C::kTurns) load(rd, base + C::kTmDP);
+        loaded(C::kTurns ? s_read : dp_read);
+        float2 pr[kCW / 2];
+        uint32_t bits[kCW / 32];
 #pragma unroll
-        for (int hf = 0; hf < kCW / 32; ++hf) {
-          reg_fence32(rs[hf]);
-          reg_fence32(rd[hf]);
+        for (int g = 0; g < kCW / 32; ++g) {
+          bits[g] = whole ? 0xffffffffu : visible_bits(it.pos0 + row, first, valid, p.window, p.sinks, (kCW / 32) * e + g);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 t = fma2(make_float2(__uint_as_float(r[g][2 * k]), __uint_as_float(r[g][2 * k + 1])), sl2, nlse2);
+            pr[16 * g + k] = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+          }
         }
-        if (j + 1 < it.nc) {
-          tc_fence_before();
-          warp_arrive(s_read, lane);
+        if constexpr (C::kTurns) {
+          if (!mbar_wait_w(dp_full, (s_waits - 1) & 1, ctl, kErrBwdWait)) { ok = false; break; }
+          tc_fence_after();
+          load(rd, base + C::kTmDP);
+          loaded(dp_read);
         }
         uint32_t pd[kCW / 32][16];
 #pragma unroll
-        for (int hf = 0; hf < kCW / 32; ++hf) {
-          const uint32_t bits =
-              whole ? 0xffffffffu : visible_bits(it.pos0 + row, first, valid, p.window, p.sinks, (kCW / 32) * e + hf);
+        for (int g = 0; g < kCW / 32; ++g)
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float2 t = fma2(make_float2(__uint_as_float(rs[hf][2 * k]), __uint_as_float(rs[hf][2 * k + 1])), sl2, nlse2);
-            const float2 pr = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-            float2 dr = mul2(pr, add2(make_float2(__uint_as_float(rd[hf][2 * k]), __uint_as_float(rd[hf][2 * k + 1])), ndd));
+            float2 dr = mul2(pr[16 * g + k], add2(make_float2(__uint_as_float(rd[g][2 * k]), __uint_as_float(rd[g][2 * k + 1])), ndd));
             if (kIsHalf<T>) dr = mul2(dr, fac2);
             if (!whole) {
-              if (!(bits & (1u << (2 * k)))) dr.x = 0.f;
-              if (!(bits & (2u << (2 * k)))) dr.y = 0.f;
+              if (!(bits[g] & (1u << (2 * k)))) dr.x = 0.f;
+              if (!(bits[g] & (2u << (2 * k)))) dr.y = 0.f;
             }
-            pd[hf][k] = Elem<T>::pack(dr.x, dr.y);
+            pd[g][k] = Elem<T>::pack(dr.x, dr.y);
           }
-        }
         if (s_waits > 1) {
           // the dQ products of the chunk before have read its dS
           if (!mbar_wait_w(ds_free, s_waits & 1, ctl, kErrBwdWait)) { ok = false; break; }
