@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
   }
 }
 
-// The parts of a key block added up in order.
+// The parts of a key block added up in order, four columns of a row per thread.
 template <int D, class T>
 __global__ void __launch_bounds__(256) window_join_kernel(const WinParams p) {
   const int kb = blockIdx.x, slice = blockIdx.y, slices = gridDim.y;
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(256) window_join_kernel(const WinParams p) {
   const bool sink = kb < p.sink_blocks;
   const int unit = sink ? kb * p.sink_segs : p.sink_blocks * p.sink_segs + (kb - p.sink_blocks) * p.norm_segs;
   constexpr int kPer = D / 4;
-  for (int i = threadIdx.x; i < 2 * kBM * kPer; i += 256) {
+  for (int i = blockIdx.z * 256 + threadIdx.x; i < 2 * kBM * kPer; i += gridDim.z * 256) {
     const int row = i % kBM, col = i / kBM % kPer, which = i / (kBM * kPer);
     if (row >= it.rows) continue;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1081,7 +1081,7 @@ cudaError_t launch(const WinParams &p, const CUtensorMap *m, int num_sms, cudaSt
     if (const cudaError_t e = cudaLaunchKernelEx(&cfg, window_dq_kernel<D, T>, m[0], m[1], m[2], m[3], p)) return e;
   }
   const int joined = kv_items == 0 ? 0 : p.norm_segs > 1 ? nkb : p.sink_segs > 1 ? p.sink_blocks : 0;
-  if (joined > 0) window_join_kernel<D, T><<<dim3(joined, slices), 256, 0, stream>>>(p);
+  if (joined > 0) window_join_kernel<D, T><<<dim3(joined, slices, 2 * kBM * D / 4 / 256), 256, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
