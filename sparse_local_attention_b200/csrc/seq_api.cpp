@@ -78,7 +78,7 @@ BackwardLayout backward_layout(const sta_window_problem *p) {
   BackwardLayout l{};
   auto up = [](long long n, long long m) { return (n + m - 1) / m; };
   const long long group = p->heads / p->kv_heads, slices = (long long)p->batch * p->kv_heads;
-  const long long nkb = up(p->kv_len, 128), nqb = up(p->q_len, 128);
+  const long long nkb = up(p->kv_len, 128);
   const bool windowed = p->window > 0 && p->window < p->kv_len;
   const long long all = up(p->q_len + 7ll, 128), seen = windowed ? up(p->window + 135ll, 128) : all;
   const long long norm = (seen < all ? seen : all) * group;
@@ -92,7 +92,7 @@ BackwardLayout backward_layout(const sta_window_problem *p) {
   const size_t packed_row = p->q_rows ? (size_t)up(p->q_rows, 8) * 8 + 8 * (size_t)p->batch + 8 : 0;
   const size_t aug_rows = rows > packed_row * p->heads ? rows : packed_row * p->heads;
   l.aug_rows = (int)packed_row;  // the dense form's is set by the caller
-  l.n_norms = (int)(nqb * p->heads * p->batch);
+  l.n_norms = (int)(up(p->q_len, sta::pre_rows(p->head_dim)) * p->heads * p->batch);
   size_t slots = 0;
   if (l.norm_segs > 1) slots = (size_t)slices * (l.sink_blocks * l.sink_segs + (nkb - l.sink_blocks) * l.norm_segs);
   else if (l.sink_segs > 1) slots = (size_t)slices * l.sink_blocks * l.sink_segs;
@@ -181,10 +181,9 @@ bool kv_map(CUtensorMap *m, const sta_rows *x, const sta_window_problem *p, bool
 // Make the current device's context current for this thread, too: a thread that
 // has not used the device before (such as an autograd worker) has none, and
 // encoding a tensor map needs it.
-bool open_device(int *multiprocessors) {
+bool open_device() {
   int dev = -1;
-  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess &&
-         cudaDeviceGetAttribute(multiprocessors, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
 }
 
 sta_status check_workspace(const void *ws, size_t have, size_t need) {
@@ -271,9 +270,8 @@ sta_status sta_window_forward(const sta_window_problem *p, const sta_rows *q, co
       if (sta::launch_window_split(w, p->type, stream) != cudaSuccess) return STA_ERR_CUDA;
       return finish(ws, stream, flags);
     }
-    int sms = 0;
     CUtensorMap maps[3];
-    if (!open_device(&sms) || !q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
+    if (!open_device() || !q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
         !kv_map(&maps[2], v, p, cu_q) || sta::launch_window_tiles(w, p->type, maps, stream) != cudaSuccess)
       return STA_ERR_CUDA;
   }
@@ -302,11 +300,10 @@ sta_status sta_window_backward(const sta_window_problem *p, const sta_rows *q, c
   w.parts = reinterpret_cast<float *>(base + l.parts);
   w.seg_chunks = l.seg_chunks, w.sink_blocks = l.sink_blocks, w.sink_segs = l.sink_segs, w.norm_segs = l.norm_segs;
   if ((flags & STA_CALL_CHECK) && cudaMemsetAsync(ws, 0, sizeof(int), stream) != cudaSuccess) return STA_ERR_CUDA;
-  int sms = 0;
   CUtensorMap maps[4];
-  if (!open_device(&sms) || !q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
+  if (!open_device() || !q_map(&maps[0], q, p, cu_q) || !kv_map(&maps[1], k, p, cu_q) ||
       !kv_map(&maps[2], v, p, cu_q) || !q_map(&maps[3], dout, p, cu_q) ||
-      sta::launch_window_backward(w, p->type, maps, sms, stream) != cudaSuccess)
+      sta::launch_window_backward(w, p->type, maps, stream) != cudaSuccess)
     return STA_ERR_CUDA;
   return finish(ws, stream, flags);
 }

@@ -35,7 +35,7 @@ struct WinParams {
   float *dd;       // D = rowsum(dO o O), laid out like lse
   uint8_t *aug;    // operand panels of -LSE and -D: 256 bytes per 8 query rows
   int aug_rows;    // panel rows per head
-  float *norms;    // largest row norm of dO per 128-row block (fp16)
+  float *norms;    // largest row norm of dO per pre_rows(d) rows (fp16)
   int n_norms;
   float *parts;    // fp32 sums of dK and dV of the parts of key blocks
   int seg_chunks;  // chunks of 128 queries per part
@@ -43,6 +43,9 @@ struct WinParams {
   int *status;
   unsigned long long wait_limit_ns;
 };
+
+// Query rows per block of the backward's first pass.
+__host__ __device__ constexpr int pre_rows(int d) { return d == 128 ? 64 : 128; }
 
 // The cache of sta_cache, with its pages addressed through a table.
 struct CacheParams {
@@ -83,7 +86,6 @@ cudaError_t launch_window_tiles(const WinParams &p, int type, const CUtensorMap 
 // Forward of a few query rows per key head, the keys split over the GPU.
 cudaError_t launch_window_split(const WinParams &p, int type, cudaStream_t stream);
 // Backward; maps: q, k, v, dO.
-cudaError_t launch_window_backward(const WinParams &p, int type, const CUtensorMap *maps, int num_sms,
-                                   cudaStream_t stream);
+cudaError_t launch_window_backward(const WinParams &p, int type, const CUtensorMap *maps, cudaStream_t stream);
 
 }  // namespace sta

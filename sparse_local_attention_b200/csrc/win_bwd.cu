@@ -100,7 +100,8 @@ __device__ __forceinline__ float ds_factor(const WinParams &p, float *smem_word)
 }
 
 // ----------------------------------------------------------------------- 1. preprocess
-// A group of D / 8 lanes per row, a CTA per 128 rows of a head.
+// A group of D / 8 lanes per row, a CTA per pre_rows(D) rows of a head: four
+// rows per lane group, all of them in flight at once.
 template <int D, class T>
 __global__ void __launch_bounds__(256) window_pre_kernel(const WinParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
@@ -108,25 +109,32 @@ __global__ void __launch_bounds__(256) window_pre_kernel(const WinParams p) {
   const Sequence s = sequence(p, b);
   float norm = 0.f;
   const long long aug0 = aug_row(p, s, b, h);
-#pragma unroll 2
-  for (int i = 0; i < kBM / (8 * kRows); ++i) {
-    const int row = blockIdx.x * kBM + (i * 8 + (threadIdx.x >> 5)) * kRows + sub;
-    const bool valid = row < s.nq;
-    float acc = 0.f, sq = 0.f, lse = 0.f;
-    long long at = 0;
-    if (valid) {
-      const long long r = s.q0 + row;
-      at = stat_row(p, s, h, row);
-      const uint4 a = reinterpret_cast<const uint4 *>(p.o.p + 2 * (s.slice * p.o.b + h * p.o.h + r * p.o.r))[part];
-      const uint4 g = reinterpret_cast<const uint4 *>(p.dout.p + 2 * (s.slice * p.dout.b + h * p.dout.h + r * p.dout.r))[part];
-      if (part == 0) lse = p.lse[at];
-      const uint32_t av[4] = {a.x, a.y, a.z, a.w}, gv[4] = {g.x, g.y, g.z, g.w};
+  constexpr int kPass = 8 * kRows, kPasses = pre_rows(D) / kPass;
+  const int row0 = blockIdx.x * pre_rows(D) + (threadIdx.x >> 5) * kRows + sub;
+  const char *o_at = p.o.p + 2 * (s.slice * p.o.b + h * p.o.h + (long long)(s.q0 + row0) * p.o.r) + 16 * part;
+  const char *g_at = p.dout.p + 2 * (s.slice * p.dout.b + h * p.dout.h + (long long)(s.q0 + row0) * p.dout.r) + 16 * part;
+  const float *lse_at = p.lse + stat_row(p, s, h, row0);
+  uint4 a[kPasses], g[kPasses];
+  float lse[kPasses];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 af = Elem<T>::unpack(av[e]), gf = Elem<T>::unpack(gv[e]);
-        acc = fmaf(af.x, gf.x, fmaf(af.y, gf.y, acc));
-        sq = fmaf(gf.x, gf.x, fmaf(gf.y, gf.y, sq));
-      }
+  for (int i = 0; i < kPasses; ++i) {
+    a[i] = g[i] = make_uint4(0u, 0u, 0u, 0u), lse[i] = 0.f;
+    if (row0 + i * kPass < s.nq) {
+      a[i] = __ldg(reinterpret_cast<const uint4 *>(o_at + 2ll * i * kPass * p.o.r));
+      g[i] = __ldg(reinterpret_cast<const uint4 *>(g_at + 2ll * i * kPass * p.dout.r));
+      if (part == 0) lse[i] = __ldg(lse_at + i * kPass);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int row = row0 + i * kPass;
+    float acc = 0.f, sq = 0.f;
+    const uint32_t av[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, gv[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 af = Elem<T>::unpack(av[e]), gf = Elem<T>::unpack(gv[e]);
+      acc = fmaf(af.x, gf.x, fmaf(af.y, gf.y, acc));
+      sq = fmaf(gf.x, gf.x, fmaf(gf.y, gf.y, sq));
     }
 #pragma unroll
     for (int off = kLanes / 2; off > 0; off >>= 1) {
@@ -134,12 +142,13 @@ __global__ void __launch_bounds__(256) window_pre_kernel(const WinParams p) {
       if (kIsHalf<T>) sq += __shfl_xor_sync(0xffffffffu, sq, off);
     }
     norm = fmaxf(norm, sqrtf(sq));
-    if (valid && part == 0) p.dd[at] = acc;
+    const bool valid = row < s.nq;
+    if (valid && part == 0) p.dd[stat_row(p, s, h, row)] = acc;
     if (valid && part < 2) {
       uint32_t w[4] = {0u, 0u, 0u, 0u};
       if (part == 0) {
         // a row that sees nothing has LSE = -inf; all its pairs are masked
-        w[0] = hi_lo<T>(lse == -INFINITY ? 0.f : -lse / p.scale * (1.f / kLseSel<T>));
+        w[0] = hi_lo<T>(lse[i] == -INFINITY ? 0.f : -lse[i] / p.scale * (1.f / kLseSel<T>));
         if constexpr (kIsHalf<T>) {
           const float big = fabsf(acc);
           if (big > 1024.f) w[2] = hi_lo<T>(-acc * (1.f / kDSel));
@@ -269,8 +278,6 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   ItemRing<KeyItem> ring(tmem_slot + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // window_dq may take the SMs that find no item any more
-  asm volatile("griddepcontrol.launch_dependents;");
 
   if (threadIdx.x == 0) {
     ring.init(R::kMathWarps + 2);
@@ -299,6 +306,8 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
     reinterpret_cast<uint4 *>(sel_s)[c] = w;
   }
   fence_proxy_async_cta();
+  // window_dq may take the SMs that find no item any more
+  asm volatile("griddepcontrol.launch_dependents;");
   const float fac = ds_factor<T>(p, reinterpret_cast<float *>(tmem_slot + 2));
   tc_fence_before();
   __syncthreads();
@@ -1056,28 +1065,27 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
 }
 
 template <int D, class T>
-cudaError_t launch(const WinParams &p, const CUtensorMap *m, int num_sms, cudaStream_t stream) {
+cudaError_t launch(const WinParams &p, const CUtensorMap *m, cudaStream_t stream) {
   using K = DkvCfg<D>;
   using Q = DqCfg<D>;
   static std::atomic<uint64_t> done_kv{0}, done_q{0};
   if (const cudaError_t e = allow_shared(window_dkdv_kernel<D, T>, (int)K::kSmem, done_kv)) return e;
   if (const cudaError_t e = allow_shared(window_dq_kernel<D, T>, (int)Q::kSmem, done_q)) return e;
   const int nqb = (p.q_len + kBM - 1) / kBM, nkb = (p.kv_len + kBM - 1) / kBM, slices = p.batch * p.kv_heads;
-  if (nqb > 0) window_pre_kernel<D, T><<<dim3(nqb, p.heads, p.batch), 256, 0, stream>>>(p);
+  if (nqb > 0)
+    window_pre_kernel<D, T><<<dim3((p.q_len + pre_rows(D) - 1) / pre_rows(D), p.heads, p.batch), 256, 0, stream>>>(p);
   const int kv_items = (p.sink_blocks * p.sink_segs + (nkb - p.sink_blocks) * p.norm_segs) * slices;
-  if (kv_items > 0) {
-    window_dkdv_kernel<D, T><<<kv_items, K::R::kThreads, K::kSmem, stream>>>(m[0], m[1], m[2], m[3], p);
-  }
   const int q_items = nqb * p.batch * p.heads;
+  if (kv_items > 0) window_dkdv_kernel<D, T><<<kv_items, K::R::kThreads, K::kSmem, stream>>>(m[0], m[1], m[2], m[3], p);
   if (q_items > 0) {
     // It needs nothing of window_dkdv, so it starts while that one's last items
     // run (their SMs free up one by one over about an item's time).
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(q_items), cfg.blockDim = dim3(Q::R::kThreads), cfg.dynamicSmemBytes = Q::kSmem, cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr, cfg.numAttrs = kv_items > 0 ? 1 : 0;
+    cfg.attrs = &early, cfg.numAttrs = kv_items > 0 ? 1 : 0;
     if (const cudaError_t e = cudaLaunchKernelEx(&cfg, window_dq_kernel<D, T>, m[0], m[1], m[2], m[3], p)) return e;
   }
   const int joined = kv_items == 0 ? 0 : p.norm_segs > 1 ? nkb : p.sink_segs > 1 ? p.sink_blocks : 0;
@@ -1087,13 +1095,12 @@ cudaError_t launch(const WinParams &p, const CUtensorMap *m, int num_sms, cudaSt
 
 }  // namespace
 
-cudaError_t launch_window_backward(const WinParams &p, int type, const CUtensorMap *maps, int num_sms,
-                                   cudaStream_t stream) {
+cudaError_t launch_window_backward(const WinParams &p, int type, const CUtensorMap *maps, cudaStream_t stream) {
   if (p.d == 128)
-    return type == STA_TYPE_BF16 ? launch<128, __nv_bfloat16>(p, maps, num_sms, stream)
-                                 : launch<128, __half>(p, maps, num_sms, stream);
-  return type == STA_TYPE_BF16 ? launch<64, __nv_bfloat16>(p, maps, num_sms, stream)
-                               : launch<64, __half>(p, maps, num_sms, stream);
+    return type == STA_TYPE_BF16 ? launch<128, __nv_bfloat16>(p, maps, stream)
+                                 : launch<128, __half>(p, maps, stream);
+  return type == STA_TYPE_BF16 ? launch<64, __nv_bfloat16>(p, maps, stream)
+                               : launch<64, __half>(p, maps, stream);
 }
 
 }  // namespace sta
