@@ -9,8 +9,10 @@ semantics; the work runs in the CUDA kernels of libsta.so.
 from __future__ import annotations
 
 import contextlib
+import copy
 import ctypes
 import functools
+import weakref
 from typing import Optional
 
 import torch
@@ -257,41 +259,43 @@ def window_backward(q, k, v, o, lse, dout, window: int = 0, sinks: int = 0, scal
                          workspace, check)
 
 
-def _accumulators(tensors):
-    """The leaves' gradient accumulators, marked with the stream of this use.
+def _note_use(ctx, leaf: torch.Tensor, stream: int):
+    """Remember that the graph of `ctx` was built on `stream` over a leaf.
 
     A gradient that is accumulated into a leaf runs on the stream on which the
     leaf was first used for as long as a graph of that use lives.  A backward
     pass captured on another stream would have to join that stream, which ends
-    the capture and the process, so such a capture is refused.  The caller
-    holds the result until its own graph does (the mark goes with it)."""
-    capturing = torch.cuda.is_current_stream_capturing()
-    here = torch.cuda.current_stream().cuda_stream
-    nodes = [torch.autograd.graph.get_gradient_edge(t).node for t in tensors if t.requires_grad and t.is_leaf]
-    for n in nodes:
-        if capturing and n.metadata.get("sta_stream", here) != here:
-            raise RuntimeError("sliding_window_attention: an eager graph of the same leaf tensors is still alive; "
-                               "release it (and its outputs) before capturing, or capture on detached leaves")
-        n.metadata.setdefault("sta_stream", here)
-    return nodes
+    the capture and the process, so such a capture is refused."""
+    uses = [u for u in getattr(leaf, "_sta_uses", ()) if u[1]() is not None]
+    if torch.cuda.is_current_stream_capturing() and any(u[0] != stream for u in uses):
+        raise RuntimeError("sliding_window_attention: an eager graph of the same leaf tensors is still alive; release "
+                           "it (and its outputs) before capturing, or capture on detached leaves")
+    uses.append((stream, weakref.ref(ctx)))
+    leaf._sta_uses = uses
 
 
 class _SlidingWindowAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, args):
         with _on(q.device, None):
+            stream = _current_stream(q.device)
+            for t, needed in zip((q, k, v), ctx.needs_input_grad):
+                if needed and t.is_leaf:
+                    _note_use(ctx, t, stream)
             c = _Call(q, k, v, *args)
             o, lse = _forward(c)
-        ctx.save_for_backward(q, k, v, o, lse)
-        ctx.args = args
+        ctx.save_for_backward(c.q, c.k, c.v, o, lse)
+        c.q = c.k = c.v = None  # autograd's to keep, and to let go after the backward
+        ctx.call = c
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        q, k, v, o, lse = ctx.saved_tensors
-        with _on(q.device, None):
-            dq, dk, dv = _backward(_Call(q, k, v, *ctx.args), o, lse, dout)
+        c = copy.copy(ctx.call)
+        c.q, c.k, c.v, o, lse = ctx.saved_tensors
+        with _on(o.device, None):
+            dq, dk, dv = _backward(c, o, lse, dout)
         return dq, dk, dv, None
 
 
@@ -304,8 +308,5 @@ def sliding_window_attention(q, k, v, window: int = 0, sinks: int = 0, scale: fl
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, v)):
         device = _device_of(q)
         with _on(device, None):
-            held = _accumulators((q, k, v))
-            o = _SlidingWindowAttention.apply(q, k, v, args)
-            del held
-            return o
+            return _SlidingWindowAttention.apply(q, k, v, args)
     return window_forward(q, k, v, *args, want_lse=False)[0]
