@@ -44,6 +44,9 @@ struct Item {
   int pos0[2], lo[2], hi[2];  // position of row 0; first window key; last key (below 0: none)
   int base, last, nsink;      // window keys [base, last], sink keys [0, nsink)
   int ns, nc;                 // sink chunks, chunks
+  int n0;                     // split: chunks [0, n0) are warpgroup 0's, [n0, nc) warpgroup 1's
+  __device__ __forceinline__ int begin(int x) const { return x ? n0 : 0; }
+  __device__ __forceinline__ int end(int x) const { return x ? nc : n0; }
   __device__ __forceinline__ void chunk(int j, int &first, int &valid) const {
     first = j < ns ? j * kBM : base + (j - ns) * kBM;
     valid = min(kBM, (j < ns ? nsink : last + 1) - first);
@@ -54,6 +57,25 @@ struct Item {
 // below 2^15 and the smallest number stands for 2^-31 of the row's largest.
 template <class T> constexpr float kHead = std::is_same<T, __half>::value ? 7.f : 0.f;
 
+// The chunks of an item in the order of their loads, K and V, until f(x, chunk,
+// is_v) is false.  Shared: K0 V0 K1 V1 ...; split: the first K of each
+// warpgroup, then V(j) and K(j + 1) of the one and of the other.
+template <bool kSplit, class F>
+__device__ __forceinline__ bool for_loads(const Item &it, F &&f) {
+  if constexpr (!kSplit) {
+    for (int c = 0; c < it.nc; ++c)
+      if (!f(0, c, false) || !f(0, c, true)) return false;
+  } else {
+    for (int j = -1; j < it.n0; ++j)
+      for (int x = 0; x < 2; ++x) {
+        const int c = it.begin(x) + j, end = it.end(x);
+        if (j >= 0 && c < end && !f(x, c, true)) return false;
+        if (c + 1 < end && !f(x, c + 1, false)) return false;
+      }
+  }
+  return true;
+}
+
 template <int D>
 struct Cfg {
   static constexpr uint32_t kTile = kBM * D * 2;
@@ -63,7 +85,7 @@ struct Cfg {
   static constexpr int kLead = D == 128 ? 96 : 64;  // keys of the first part of P V
   // full[S] empty[S] raw[S] q_full q_free s_full[2] p_ready[2] pv_done[2] o_free[2] drain p_lead[2]
   static constexpr int kNumBars = 3 * kSlots + 13;
-  static constexpr uint32_t kSmem = (2 + kSlots) * kTile + kNumBars * 8 + 64 + ItemRing<Item>::kBytes + 1024;
+  static constexpr uint32_t kSmem = (2 + kSlots) * kTile + kNumBars * 8 + 64 + 4 * kBM * 4 + ItemRing<Item>::kBytes + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -72,19 +94,20 @@ __device__ __forceinline__ bool sees(const Item &it, int x, int first, int valid
   return first <= it.hi[x] && (first + valid > it.lo[x] || first < sinks);
 }
 
+template <bool kSplit>
 __device__ __forceinline__ Item decode(const WinParams &p, int item) {
   Item it;
   it.stop = item < 0;
   if (it.stop) return it;
   const int slices = p.batch * p.kv_heads, nqb = (p.q_len + kBM - 1) / kBM;
-  const int pairs = (nqb * p.group + 1) / 2;
-  const int pair = pairs - 1 - item / slices, slice = item % slices;  // the last blocks have the most keys
+  const int per = kSplit ? 1 : 2, rounds = (nqb * p.group + per - 1) / per;  // units of an item, items of a key head
+  const int round = rounds - 1 - item / slices, slice = item % slices;  // the last blocks have the most keys
   const int b = slice / p.kv_heads;
   it.hk = slice % p.kv_heads;
   it.s = sequence(p, b);
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const int unit = 2 * pair + x;
+    const int unit = kSplit ? round : 2 * round + x;
     it.qb[x] = unit / p.group;
     it.h[x] = it.hk * p.group + unit % p.group;
     const int rows = min(kBM, it.s.nq - it.qb[x] * kBM);
@@ -98,10 +121,11 @@ __device__ __forceinline__ Item decode(const WinParams &p, int item) {
   it.nsink = min(p.sinks, it.base);
   it.ns = (it.nsink + kBM - 1) / kBM;
   it.nc = it.has[0] && it.last >= 0 ? it.ns + (it.last - it.base + kBM) / kBM : 0;
+  it.n0 = (it.nc + 1) / 2;
   return it;
 }
 
-template <int D, class T>
+template <int D, class T, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const WinParams p) {
@@ -117,7 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *drain = o_free + 2, *p_lead = drain + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  ItemRing<Item> ring(tmem_slot + 16);
+  float *ml_s = reinterpret_cast<float *>(tmem_slot + 16);  // split: m of both warpgroups' rows, then l
+  ItemRing<Item> ring(ml_s + 4 * kBM);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -156,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int item = blockIdx.x;
       bool ok = true, asked = false;
       while (true) {
-        const Item it = decode(p, item);
+        const Item it = decode<kSplit>(p, item);
         if (!ring.put(n, it, ctl, kErrWaitProducer)) { ok = false; break; }
         if (it.stop) break;
         ring.ask();
@@ -167,24 +192,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         if (!mbar_wait(q_free, (items & 1) ^ 1, ctl, kErrWaitProducer)) { ok = false; break; }
-        mbar_arrive_expect_tx(q_full, (it.has[1] ? 2 : 1) * C::kTile);
+        const int n_q = !kSplit && it.has[1] ? 2 : 1;
+        mbar_arrive_expect_tx(q_full, n_q * C::kTile);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
-          if (it.has[x]) load_tile<D>(q_smem + x * C::kTile, &tmap_q, it.s.q0 + it.qb[x] * kBM, it.h[x], it.s.slice, q_full);
+          if (x < n_q) load_tile<D>(q_smem + x * C::kTile, &tmap_q, it.s.q0 + it.qb[x] * kBM, it.h[x], it.s.slice, q_full);
         ++items;
-        for (int s = 0; s < 2 * it.nc; ++s) {  // K0 V0 K1 V1 ...
+        ok = for_loads<kSplit>(it, [&](int, int c, bool is_v) {
           int first, valid;
-          it.chunk(s >> 1, first, valid);
+          it.chunk(c, first, valid);
           const uint32_t slot = ld % C::kSlots, phase = (ld / C::kSlots) & 1, bit = 1u << slot;
-          if (!mbar_wait(&empty[slot], phase ^ 1, ctl, kErrWaitProducer)) { ok = false; break; }
-          const bool clear = (s & 1) && valid % 16 != 0;
+          if (!mbar_wait(&empty[slot], phase ^ 1, ctl, kErrWaitProducer)) return false;
+          const bool clear = is_v && valid % 16 != 0;
           uint64_t *bar = clear ? &raw[slot] : &full[slot];
           raw_last = clear ? raw_last | bit : raw_last & ~bit;
           if (clear) raw_par ^= bit;
           mbar_arrive_expect_tx(bar, C::kTile);
-          load_tile<D>(slots + slot * C::kTile, (s & 1) ? &tmap_v : &tmap_k, it.s.k0 + first, it.hk, it.s.slice, bar);
+          load_tile<D>(slots + slot * C::kTile, is_v ? &tmap_v : &tmap_k, it.s.k0 + first, it.hk, it.s.slice, bar);
           ++ld;
-        }
+          return true;
+        });
         if (!ok || !ring.take(n++, item, ctl, kErrWaitProducer)) { ok = false; break; }
         asked = false;
       }
@@ -207,17 +234,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item *at = ring.get(n, ok, ctl, kErrWaitProducer);
       if (!at) break;
       const Item &it = *at;
-      for (int j = 0; j < it.nc && ok; ++j) {
+      uint32_t l = ld;
+      ok = for_loads<kSplit>(it, [&](int, int c, bool is_v) {
+        const uint32_t slot = l++ % C::kSlots;
         int first, valid;
-        it.chunk(j, first, valid);
-        if (valid % 16 == 0) continue;
-        const uint32_t slot = (ld + 2 * j + 1) % C::kSlots;
-        ok = mbar_wait_w(&raw[slot], raw_par >> slot & 1, ctl, kErrWaitProducer);
+        it.chunk(c, first, valid);
+        if (!is_v || valid % 16 == 0) return true;
+        if (!mbar_wait_w(&raw[slot], raw_par >> slot & 1, ctl, kErrWaitProducer)) return false;
         raw_par ^= 1u << slot;
-        if (!ok) break;
         clear_rows<D>(slots + slot * C::kTile, valid, (valid + 15) & ~15, lane);
         if (lane == 0) mbar_arrive(&full[slot]);
-      }
+        return true;
+      });
       if (!ok) break;
       ld += 2 * it.nc;
       ring.release(n, lane);
@@ -233,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t p_waits[2] = {0, 0}, o_waits[2] = {0, 0}, used[2] = {0, 0};
     bool ok = true, issued = false;
     auto mma_s = [&](int x, uint32_t slot) {
-      const uint64_t qd = qdesc0 + ((x * C::kTile) >> 4), kd = kdesc0 + ((slot * C::kTile) >> 4);
+      const uint64_t qd = qdesc0 + (((kSplit ? 0 : x) * C::kTile) >> 4), kd = kdesc0 + ((slot * C::kTile) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
@@ -274,47 +302,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       ++items;
       const uint32_t k0 = ld;
-      if (!wait_slot(k0)) { ok = false; break; }
-      int first, valid;
-      it.chunk(0, first, valid);
-      bool act[2] = {sees(it, 0, first, valid, p.sinks), sees(it, 1, first, valid, p.sinks)};
       bool begun[2] = {false, false};
-      issued = true;
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (act[x]) mma_s(x, k0 % C::kSlots);
-      mma_commit_w(&empty[k0 % C::kSlots]);
-      if (it.nc == 1) mma_commit_w(q_free);
-      for (int j = 0; j < it.nc && ok; ++j) {
-        const uint32_t vj = k0 + 2 * j + 1, kn = vj + 1;
-        const bool more = j + 1 < it.nc;
-        const int steps = (valid + 15) / 16;
-        it.chunk(j + 1, first, valid);
-        const bool next[2] = {more && sees(it, 0, first, valid, p.sinks), more && sees(it, 1, first, valid, p.sinks)};
-        if (!wait_slot(vj) || (more && !wait_slot(kn))) { ok = false; break; }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (act[x]) {
-            const uint32_t ph = p_waits[x] & 1;
-            ++p_waits[x];
-            if (!mbar_wait_w(&p_lead[x], ph, ctl, kErrWaitMma)) { ok = false; break; }
-            tc_fence_after();
-            if (!begun[x] && used[x] > 0) {
-              // the epilogue of this half's previous item has read O_X
-              if (!mbar_wait_w(&o_free[x], o_waits[x] & 1, ctl, kErrWaitMma)) { ok = false; break; }
-              ++o_waits[x];
-              tc_fence_after();
-            }
-            if (!mma_pv(x, vj % C::kSlots, !begun[x], ph, steps)) { ok = false; break; }
-            begun[x] = true;
-          }
-          act[x] = next[x];
-          if (act[x]) mma_s(x, kn % C::kSlots);
+      // P V of unit x's chunk whose V is in `slot`
+      auto attend = [&](int x, uint32_t slot, int steps) -> bool {
+        const uint32_t ph = p_waits[x] & 1;
+        ++p_waits[x];
+        if (!mbar_wait_w(&p_lead[x], ph, ctl, kErrWaitMma)) return false;
+        tc_fence_after();
+        if (!begun[x] && used[x] > 0) {
+          // the epilogue of the previous item here has read O_X
+          if (!mbar_wait_w(&o_free[x], o_waits[x] & 1, ctl, kErrWaitMma)) return false;
+          ++o_waits[x];
+          tc_fence_after();
         }
-        if (!ok) break;
-        mma_commit_w(&empty[vj % C::kSlots]);
-        if (more) mma_commit_w(&empty[kn % C::kSlots]);
-        if (j + 2 == it.nc) mma_commit_w(q_free);
+        const bool first = !begun[x];
+        begun[x] = true;
+        return mma_pv(x, slot, first, ph, steps);
+      };
+      if constexpr (!kSplit) {
+        if (!wait_slot(k0)) { ok = false; break; }
+        int first, valid;
+        it.chunk(0, first, valid);
+        bool act[2] = {sees(it, 0, first, valid, p.sinks), sees(it, 1, first, valid, p.sinks)};
+        issued = true;
+  #pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (act[x]) mma_s(x, k0 % C::kSlots);
+        mma_commit_w(&empty[k0 % C::kSlots]);
+        if (it.nc == 1) mma_commit_w(q_free);
+        for (int j = 0; j < it.nc && ok; ++j) {
+          const uint32_t vj = k0 + 2 * j + 1, kn = vj + 1;
+          const bool more = j + 1 < it.nc;
+          const int steps = (valid + 15) / 16;
+          it.chunk(j + 1, first, valid);
+          const bool next[2] = {more && sees(it, 0, first, valid, p.sinks), more && sees(it, 1, first, valid, p.sinks)};
+          if (!wait_slot(vj) || (more && !wait_slot(kn))) { ok = false; break; }
+  #pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (act[x]) {
+              if (!attend(x, vj % C::kSlots, steps)) { ok = false; break; }
+            }
+            act[x] = next[x];
+            if (act[x]) mma_s(x, kn % C::kSlots);
+          }
+          if (!ok) break;
+          mma_commit_w(&empty[vj % C::kSlots]);
+          if (more) mma_commit_w(&empty[kn % C::kSlots]);
+          if (j + 2 == it.nc) mma_commit_w(q_free);
+        }
+      } else {
+        uint32_t l = k0;
+        int s_left = it.nc;
+        // S of warpgroup x's next chunk from its K, which is load l
+        auto score = [&](int x) -> bool {
+          if (!wait_slot(l)) return false;
+          mma_s(x, l % C::kSlots);
+          issued = true;
+          mma_commit_w(&empty[l++ % C::kSlots]);
+          if (--s_left == 0) mma_commit_w(q_free);
+          return true;
+        };
+        ok = score(0) && (it.n0 == it.nc || score(1));
+        for (int j = 0; j < it.n0 && ok; ++j)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int c = it.begin(x) + j;
+            if (c >= it.end(x)) continue;
+            int first, valid;
+            it.chunk(c, first, valid);
+            const uint32_t vl = l++;
+            // the next K, too, while the softmax works
+            if (!wait_slot(vl) || (c + 1 < it.end(x) && !wait_slot(l)) || !attend(x, vl % C::kSlots, (valid + 15) / 16)) {
+              ok = false;
+              break;
+            }
+            mma_commit_w(&empty[vl % C::kSlots]);
+            if (c + 1 < it.end(x) && !score(x)) { ok = false; break; }
+          }
       }
       if (!ok) break;
       ld = k0 + 2 * it.nc;
@@ -338,18 +402,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item *at = ring.get(n, ok, ctl, kErrWaitSoftmax);
       if (!at) break;
       const Item &it = *at;  // stays in shared memory: beside a row of scores registers are short
-      if (!it.has[x]) {
+      const int u = kSplit ? 0 : x;  // its unit
+      if (!it.has[u]) {
         ring.release(n, lane);
         continue;
       }
       float m = -INFINITY, l = 0.f;
       bool seen = false;
-      for (int j = 0; j < it.nc; ++j) {
+      for (int j = kSplit ? it.begin(x) : 0; j < (kSplit ? it.end(x) : it.nc); ++j) {
         int first, valid;
         it.chunk(j, first, valid);
-        if (!sees(it, x, first, valid, p.sinks)) continue;
+        if (!kSplit && !sees(it, x, first, valid, p.sinks)) continue;
         // whole: every row of the unit sees all 128 keys
-        const int pos0 = it.pos0[x];
+        const int pos0 = it.pos0[u];
         const bool whole = valid == kBM && first + kBM - 1 <= pos0 &&
                            (first > pos0 + kBM - 1 - p.window || first + kBM <= p.sinks);
         if (!mbar_wait_w(&s_full[x], s_waits & 1, ctl, kErrWaitSoftmax)) { ok = false; break; }
@@ -459,44 +524,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(&p_ready[x], lane);
         seen = true;
       }
-      if (!ok) break;
-      if (seen) {
+      if (!kSplit && !ok) break;
+      if (seen && ok) {
         // one P V per chunk so far: the last one's phase
-        if (!mbar_wait_w(&pv_done[x], (s_waits - 1) & 1, ctl, kErrWaitEpilogue)) { ok = false; break; }
+        ok = mbar_wait_w(&pv_done[x], (s_waits - 1) & 1, ctl, kErrWaitEpilogue);
         tc_fence_after();
       }
-      const int qrow = it.qb[x] * kBM + row;
+      if (!kSplit && !ok) break;
+      const int qrow = it.qb[u] * kBM + row;
       const bool row_valid = qrow < it.s.nq;
+      float f[2] = {1.f, 0.f};  // split: the weights of the two partial O
+      if constexpr (kSplit) {
+        // join the two halves of the keys: each warpgroup writes half of the columns
+        ml_s[x * kBM + row] = m, ml_s[(2 + x) * kBM + row] = l;
+        ok = named_bar_and(1, 256, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const float m0 = ml_s[row], m1 = ml_s[kBM + row], top = fmaxf(m0, m1);
+        f[0] = m0 == -INFINITY ? 0.f : ex2_approx(m0 - top), f[1] = m1 == -INFINITY ? 0.f : ex2_approx(m1 - top);
+        m = top, l = ml_s[2 * kBM + row] * f[0] + ml_s[3 * kBM + row] * f[1];
+      }
       const bool none = l == 0.f;
       const float inv_l = none ? 0.f : 1.f / l;
+      f[0] *= inv_l, f[1] *= inv_l;
       // the quad's first row, and how many of its rows there are
-      char *dst = p.o.p + 2 * ((long long)it.s.slice * p.o.b + (long long)it.h[x] * p.o.h +
+      char *dst = p.o.p + 2 * ((long long)it.s.slice * p.o.b + (long long)it.h[u] * p.o.h +
                                (long long)(it.s.q0 + (qrow & ~3)) * p.o.r);
       const int quad_rows = it.s.nq - (qrow & ~3);
+      constexpr int kOut = kSplit ? D / 2 : D;  // columns of this warpgroup
+      const uint32_t from = tmem + lane_off + C::kTmO + (kSplit ? x * kOut : x * D);
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t r[32];
-        if (seen) {
-          tmem_ld32(o_tm + c * 32, r);
-          tmem_ld_wait();
-          reg_fence32(r);
+      for (int c = 0; c < kOut / 32; ++c) {
+        uint32_t r[32], r1[32];
+        if (kSplit ? it.nc > 0 : seen) tmem_ld32(from + c * 32, r);
+        if (kSplit && it.nc > it.n0) tmem_ld32(from + D + c * 32, r1);
+        tmem_ld_wait();
+        reg_fence32(r);
+        if constexpr (kSplit) {
+          reg_fence32(r1);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float y = __uint_as_float(r[i]) * f[0];
+            if (it.nc > it.n0) y = fmaf(__uint_as_float(r1[i]), f[1], y);
+            r[i] = __float_as_uint(y);
+          }
         }
         uint4 w[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           auto pair = [&](int e) {
-            return none ? 0u : Elem<T>::pack(__uint_as_float(r[8 * v + 2 * e]) * inv_l, __uint_as_float(r[8 * v + 2 * e + 1]) * inv_l);
+            const float k = kSplit ? 1.f : f[0];
+            return none ? 0u : Elem<T>::pack(__uint_as_float(r[8 * v + 2 * e]) * k, __uint_as_float(r[8 * v + 2 * e + 1]) * k);
           };
           w[v] = make_uint4(pair(0), pair(1), pair(2), pair(3));
         }
-        store_quad(w, dst + 64 * c, 2 * p.o.r, quad_rows, lane);
+        store_quad(w, dst + 64 * c + (kSplit ? 2 * x * kOut : 0), 2 * p.o.r, quad_rows, lane);
+      }
+      if (kSplit) {
+        tc_fence_before();
+        named_bar_sync(2, 256);  // both warpgroups have read both O, m and l
       }
       if (seen) {
         tc_fence_before();
         warp_arrive(&o_free[x], lane);
       }
-      if (row_valid && p.lse)
-        p.lse[stat_row(p, it.s, it.h[x], qrow)] = none ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+      if (row_valid && p.lse && (!kSplit || x == 0))
+        p.lse[stat_row(p, it.s, it.h[u], qrow)] = none ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
       ring.release(n, lane);
     }
   }
@@ -510,15 +603,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+template <int D, class T, bool kSplit>
+cudaError_t launch_mode(const WinParams &p, const CUtensorMap *maps, long long items, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  if (const cudaError_t e = allow_shared(window_fwd_kernel<D, T, kSplit>, (int)Cfg<D>::kSmem, done)) return e;
+  window_fwd_kernel<D, T, kSplit><<<(unsigned)items, kThreads, Cfg<D>::kSmem, stream>>>(maps[0], maps[1], maps[2], p);
+  return cudaGetLastError();
+}
+
+// Pairs of units share their keys; where one round of the GPU has room for
+// every unit on its own, the two warpgroups take half of its keys each.
 template <int D, class T>
 cudaError_t launch(const WinParams &p, const CUtensorMap *maps, cudaStream_t stream) {
-  using C = Cfg<D>;
-  static std::atomic<uint64_t> done{0};
-  if (const cudaError_t e = allow_shared(window_fwd_kernel<D, T>, (int)C::kSmem, done)) return e;
-  const long long nqb = (p.q_len + kBM - 1) / kBM;
-  const long long items = (nqb * p.group + 1) / 2 * p.batch * p.kv_heads;
-  window_fwd_kernel<D, T><<<(unsigned)items, kThreads, C::kSmem, stream>>>(maps[0], maps[1], maps[2], p);
-  return cudaGetLastError();
+  const long long units = (long long)((p.q_len + kBM - 1) / kBM) * p.group, slices = (long long)p.batch * p.kv_heads;
+  if (units * slices <= 148) return launch_mode<D, T, true>(p, maps, units * slices, stream);
+  return launch_mode<D, T, false>(p, maps, (units + 1) / 2 * slices, stream);
 }
 
 }  // namespace
