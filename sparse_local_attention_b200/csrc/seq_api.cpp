@@ -59,8 +59,27 @@ size_t stat_rows(const sta_window_problem *p) {
   return dense > packed ? dense : packed;
 }
 
-// Query rows of a key head up to which the keys are split over the GPU.
-constexpr long long kFewRows = 32;
+// Whether a forward call splits the keys over the GPU (16 query rows of a key
+// head at a time) or runs on 128-row tiles: what takes less by the rates of
+// either on a B200.  The split form does 1400 steps of 16 keys a microsecond at
+// head dim 64 and 550 at 128; a tile item takes 2.1 or 2.4 us for each 128 keys
+// of its pair of blocks, in rounds of 148, or 1.1 or 1.3 us with the keys of one
+// block split in its CTA, where all blocks fit in one round.  Measured, split
+// against tiles, in us: 8 sequences, 24 heads over 8, d 128, window 1024: 3 rows
+// 11 / 26, 24 rows 17 / 28, 96 rows 46 / 28; 1 sequence, 16 heads over 4, 8192
+// keys, d 128: 4 rows 11 / 86, 256 rows 52 / 87, 512 rows 102 / 87.
+bool splits_keys(const sta_window_problem *p) {
+  auto up = [](long long n, long long m) { return (n + m - 1) / m; };
+  const long long group = p->heads / p->kv_heads, slices = (long long)p->batch * p->kv_heads;
+  const long long rows = p->q_len * group, blocks = up(p->q_len, 128) * group;
+  if (rows > 256) return false;
+  const long long span = (long long)p->window + p->q_len - 1 + p->sinks;
+  const long long keys = p->window > 0 && span < p->kv_len ? span : p->kv_len;
+  const bool small = p->head_dim == 64;
+  const double split = (double)up(rows, 16) * slices * up(keys, 16) / (small ? 1400 : 550);
+  const double per = blocks * slices <= 148 ? (small ? 1.1 : 1.3) : (small ? 2.1 : 2.4) * up(up(blocks, 2) * slices, 148);
+  return rows <= 16 || split < per * (up(keys, 128) + 1);
+}
 
 size_t window_fwd_bytes(const sta_window_problem *) { return kStatusBytes; }
 
@@ -266,7 +285,7 @@ sta_status sta_window_forward(const sta_window_problem *p, const sta_rows *q, co
   w.q = rows_of(q), w.k = rows_of(k), w.v = rows_of(v), w.o = rows_of(o), w.lse = lse;
   if ((flags & STA_CALL_CHECK) && cudaMemsetAsync(ws, 0, sizeof(int), stream) != cudaSuccess) return STA_ERR_CUDA;
   if (p->q_len > 0) {
-    if ((long long)p->q_len * w.group <= kFewRows) {
+    if (splits_keys(p)) {
       if (sta::launch_window_split(w, p->type, stream) != cudaSuccess) return STA_ERR_CUDA;
       return finish(ws, stream, flags);
     }

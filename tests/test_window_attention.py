@@ -54,6 +54,10 @@ CASES = [
     (2, 2, 640, 640, 64, 10000, 5),    # a window longer than the sequence
     (2, 2, 70, 0, 64, 10, 2),          # no keys
     (4, 4, 1500, 1500, 64, 96, 700),   # sinks over many tiles
+    # more blocks than SMs: two blocks of a key head share their keys
+    (48, 16, 200, 333, 64, 77, 5),
+    (40, 8, 260, 260, 128, 1000, 0),
+    (32, 32, 300, 300, 128, 100, 130),
 ]
 
 
