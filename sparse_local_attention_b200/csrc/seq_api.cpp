@@ -361,7 +361,7 @@ sta_status sta_cache_attention(const sta_cache *c, int32_t batch, int32_t heads,
   a.sinks = sinks < sta::kNoWindow ? sinks : sta::kNoWindow;
   a.scale_log2 = (scale > 0.f ? scale : 1.f / std::sqrt((float)c->head_dim)) * 1.4426950408889634f;
   a.q = rows_of(q), a.o = rows_of(o), a.lse = lse, a.lengths = lengths;
-  a.page_inv = 16.f / c->page_size, a.blocks = c->page_size / c->block;
+  a.blocks = c->page_size / c->block;
   while ((1 << a.block_shift) < c->block) ++a.block_shift;
   if (q_len > 0 && sta::launch_cache_attention(a, c->type, type, stream) != cudaSuccess) return STA_ERR_CUDA;
   return finish(nullptr, stream, flags);

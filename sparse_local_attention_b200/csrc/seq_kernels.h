@@ -76,7 +76,6 @@ struct CacheAttn {
   Rows q, o;
   float *lse;
   const int32_t *lengths;
-  float page_inv;            // 16 / page_size
   int blocks, block_shift;   // scales per page and head, log2(block)
 };
 cudaError_t launch_cache_attention(const CacheAttn &a, int cache_type, int io_type, cudaStream_t stream);

@@ -102,7 +102,6 @@ struct Seen {
 // that the lanes of one access touch all banks (8-byte rows of V: half of them).
 struct Source {
   const char *k, *v;  // first key
-  long long k_pitch, v_pitch;
   const float *k_scale, *v_scale;
 };
 
@@ -126,23 +125,39 @@ struct CacheKeys {
   __device__ __forceinline__ float *lse_at(int h, int i) const {
     return a.lse ? a.lse + ((long long)b * a.heads + h) * a.q_len + i : nullptr;
   }
-  // Where a step's keys lie, looked up a step before their loads.
+  // Where a step's keys lie: the page (-1: absent), looked up a step before the
+  // loads that need it, its place in the table, and the steps before it in the page.
   struct Place {
-    int page, at;  // page (-1: absent), first key within it
+    int page, index, in_page;
   };
-  __device__ __forceinline__ Place place(int step) const {
-    const int per = a.c.page_size / kStep;  // uniform
-    int i = (int)(__int2float_rz(step) * a.page_inv), r = step - i * per;
-    while (r < 0) --i, r += per;
-    while (r >= per) ++i, r -= per;
-    const int page = __ldg(a.c.table + (long long)b * a.c.table_pages + i);
-    return Place{(unsigned)page < (unsigned)a.c.pages ? page : -1, r * kStep};
+  __device__ __forceinline__ void look_up(Place &p) const {
+    const int page = __ldg(a.c.table + (long long)b * a.c.table_pages + p.index);
+    p.page = (unsigned)page < (unsigned)a.c.pages ? page : -1;
   }
+  __device__ __forceinline__ Place place(int step) const {
+    const int per = a.c.page_size / kStep;
+    Place p{-1, step / per, step % per};
+    look_up(p);
+    return p;
+  }
+  __device__ __forceinline__ void advance(Place &p, int steps) const {
+    const int per = a.c.page_size / kStep;
+    p.in_page += steps;
+    if (p.in_page < per) return;  // still the same page
+    do {
+      p.in_page -= per;
+      ++p.index;
+    } while (p.in_page >= per);
+    look_up(p);
+  }
+  static __device__ __forceinline__ constexpr int k_pitch() { return D; }
+  static __device__ __forceinline__ constexpr int v_pitch() { return D; }
   __device__ __forceinline__ bool there(const Place &p) const { return p.page >= 0; }
   __device__ __forceinline__ Source source(const Place &p, int) const {
-    const long long ph = (long long)p.page * a.c.kv_heads + hk, row = (ph * a.c.page_size + p.at) * D;
-    const long long sc = ph * a.blocks + (p.at >> a.block_shift);
-    return Source{reinterpret_cast<const char *>(a.c.k + row), reinterpret_cast<const char *>(a.c.v + row), D, D,
+    const long long ph = (long long)p.page * a.c.kv_heads + hk;
+    const int at = p.in_page * kStep;
+    const long long row = (ph * a.c.page_size + at) * D, sc = ph * a.blocks + (at >> a.block_shift);
+    return Source{reinterpret_cast<const char *>(a.c.k + row), reinterpret_cast<const char *>(a.c.v + row),
                   a.c.k_scale + sc, a.c.v_scale + sc};
   }
   // A operand of the s-th 16 columns of d, from 64 bytes' pieces of rows g and g + 8
@@ -185,12 +200,15 @@ struct RowKeys {
   __device__ __forceinline__ float *lse_at(int h, int i) const { return p.lse ? p.lse + stat_row(p, s, h, i) : nullptr; }
   struct Place {};
   __device__ __forceinline__ Place place(int) const { return Place{}; }
+  __device__ __forceinline__ void advance(Place &, int) const {}
   __device__ __forceinline__ bool there(const Place &) const { return true; }
   __device__ __forceinline__ Source source(const Place &, int step) const {
     const long long row = s.k0 + step * kStep;
     return Source{p.k.p + 2 * (s.slice * p.k.b + hk * p.k.h + row * p.k.r), p.v.p + 2 * (s.slice * p.v.b + hk * p.v.h + row * p.v.r),
-                  2 * p.k.r, 2 * p.v.r, nullptr, nullptr};
+                  nullptr, nullptr};
   }
+  __device__ __forceinline__ long long k_pitch() const { return 2 * p.k.r; }
+  __device__ __forceinline__ long long v_pitch() const { return 2 * p.v.r; }
   static constexpr int kPerPiece = 2;
   static __device__ __forceinline__ void k_frag(const uint32_t (&w)[2][4], int i, uint32_t (&f)[4]) {
     f[0] = w[0][2 * i], f[2] = w[0][2 * i + 1], f[1] = w[1][2 * i], f[3] = w[1][2 * i + 1];
@@ -267,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas) split_
   }
   const int begin = (int)((long long)n_steps * rank / shape.splits);
   const int end = (int)((long long)n_steps * (rank + 1) / shape.splits);
-  auto step_of = [&](int i) { return i < sink_steps ? i : base_step + i - sink_steps; };
+  const int skipped = base_step - sink_steps;  // steps between the sinks and the window
+  auto step_of = [&](int i) { return i < sink_steps ? i : i + skipped; };
 
   float o[NT][D / 16][4], m[NT][2], l[NT][2];
   float v_top = kLeastScale, v_inv = 1.f / kLeastScale;
@@ -282,6 +301,10 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas) split_
   const uint32_t ring_at = smem_u32(ring);
   uint32_t here_bits = 0;  // stages whose keys are there
   typename Keys::Place next{};
+  // a lane's 16-byte pieces of a step: kPieces to a row, kPass rows apart
+  constexpr int kPieces = kRow / 16, kPass = 32 / kPieces;
+  const int lane_row = lane / kPieces, lane_col = lane % kPieces;
+  const long long k_off = lane_row * keys.k_pitch() + 16 * lane_col, v_off = lane_row * keys.v_pitch() + 16 * lane_col;
   // the copies of the step at i into a stage (a group of them, empty past the end)
   auto fetch = [&](int i, int stage) {
     if (i < end) {
@@ -289,23 +312,22 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas) split_
       if (keys.there(next)) {
         const Source src = keys.source(next, step_of(i));
         const uint32_t at = ring_at + stage * C::kStage;
-        // a lane's pieces: kRow / 16 to a row, kPass rows apart
-        constexpr int kPieces = kRow / 16, kPass = 32 / kPieces;
-        const int row0 = lane / kPieces, col = lane % kPieces;
-        const char *k = src.k + row0 * src.k_pitch + 16 * col, *v = src.v + row0 * src.v_pitch + 16 * col;
+        const char *k = src.k + k_off, *v = src.v + v_off;
         if (seen.whole(k0)) {
 #pragma unroll
           for (int j = 0; j < kStep / kPass; ++j) {
-            copy16(at + k_place<kRow>(row0 + kPass * j, col), k + kPass * j * src.k_pitch, true);
-            copy16(at + C::kHalf + v_place<kRow>(row0 + kPass * j, col), v + kPass * j * src.v_pitch, true);
+            const int row = lane_row + kPass * j;
+            copy16(at + k_place<kRow>(row, lane_col), k + kPass * j * keys.k_pitch(), true);
+            copy16(at + C::kHalf + v_place<kRow>(row, lane_col), v + kPass * j * keys.v_pitch(), true);
           }
         } else {
 #pragma unroll 1
           for (int j = 0; j < kStep / kPass; ++j) {
-            const bool there = seen(k0 + row0 + kPass * j);
+            const int row = lane_row + kPass * j;
+            const bool there = seen(k0 + row);
             // a row that is not there is not addressed either
-            copy16(at + k_place<kRow>(row0 + kPass * j, col), there ? k + kPass * j * src.k_pitch : src.k, there);
-            copy16(at + C::kHalf + v_place<kRow>(row0 + kPass * j, col), there ? v + kPass * j * src.v_pitch : src.v, there);
+            copy16(at + k_place<kRow>(row, lane_col), there ? k + kPass * j * keys.k_pitch() : src.k, there);
+            copy16(at + C::kHalf + v_place<kRow>(row, lane_col), there ? v + kPass * j * keys.v_pitch() : src.v, there);
           }
         }
         if (Keys::kScaled && lane < 2) copy4(at + 2 * C::kHalf + 4 * lane, lane ? src.v_scale : src.k_scale);
@@ -313,7 +335,10 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas) split_
       } else {
         here_bits &= ~(1u << stage);
       }
-      if (i + kWarps < end) next = keys.place(step_of(i + kWarps));
+      if (i + kWarps < end) {
+        if (i < sink_steps && i + kWarps >= sink_steps) next = keys.place(i + kWarps + skipped);
+        else keys.advance(next, kWarps);
+      }
     }
     copies_commit();
   };
