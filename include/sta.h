@@ -366,7 +366,8 @@ typedef struct {
  * block's codes always share one scale.  A code is x * (1 / scale) in fp32,
  * rounded to nearest even and cut to the largest code; NaN is no magnitude
  * and becomes code 0; infinities count as the input type's largest
- * value.  No two sequences of a call may write the same page. */
+ * value.  A call may not write a page for two sequences, nor for two places of
+ * a sequence's table (the bytes of such a page are undefined). */
 sta_status sta_cache_write(const sta_cache *cache, int32_t batch, int32_t rows, const sta_rows *k, const sta_rows *v,
                            int32_t in_type, const int32_t *page_table, int32_t table_pages, const int32_t *start,
                            const int32_t *count, void *stream, uint32_t flags);

@@ -11,8 +11,8 @@ from typing import Optional
 import torch
 
 from .sta import STA_CALL_CHECK, _check, lib
-from .window import (IO_TYPES, STA_TYPE_E4M3, STA_TYPE_INT8, _at, _current_stream, _flat, _in_place, _input, _on,
-                     _output, _rows)
+from .window import (IO_TYPES, STA_TYPE_E4M3, STA_TYPE_INT8, _at, _current_stream, _flat, _in_place, _input, _int32,
+                     _on, _output, _rows)
 
 STA_READ_ZERO = 0x2
 CACHE_TYPES = {torch.float8_e4m3fn: STA_TYPE_E4M3, torch.int8: STA_TYPE_INT8}
@@ -32,7 +32,7 @@ class KVCache:
     Sequences own pages through a page table (int32 [batch, table_pages], the
     page of each page_size tokens; entries outside [0, pages) are absent pages),
     which the caller keeps, as well as the number of tokens of each sequence.
-    One call may not write a page for two sequences."""
+    One call may not write a page for two sequences, nor twice for one."""
 
     def __init__(self, pages: int, kv_heads: int, page_size: int, head_dim: int, block: int = 64,
                  dtype: torch.dtype = torch.float8_e4m3fn, device="cuda"):
@@ -63,11 +63,16 @@ class KVCache:
         _flat(v, "v", k.shape, k.dtype, k.device)
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             _flat(t, name, (pages, kv_heads, blocks), torch.float32, k.device)
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._tensors = k, v, k_scale, v_scale  # whose addresses _c holds
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, kv_heads, page_size, head_dim
         self.block, self.dtype, self.device = page_size // blocks, k.dtype, k.device
         self._c = _Cache(pages, kv_heads, page_size, self.block, head_dim, CACHE_TYPES[k.dtype],
                          *(t.data_ptr() for t in (k, v, k_scale, v_scale)))
+
+    k = property(lambda self: self._tensors[0], doc="codes of the keys")
+    v = property(lambda self: self._tensors[1], doc="codes of the values")
+    k_scale = property(lambda self: self._tensors[2], doc="scales of the keys")
+    v_scale = property(lambda self: self._tensors[3], doc="scales of the values")
 
     def _table(self, page_table, batch):
         if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
@@ -150,7 +155,8 @@ class KVCache:
                 lse = torch.empty(shape[:3], dtype=torch.float32, device=self.device)
             _flat(lse, "lse", shape[:3], torch.float32, self.device)
             if batch and nq:
-                st = lib().sta_cache_attention(ctypes.byref(self._c), batch, heads, nq, int(window), int(sinks),
+                st = lib().sta_cache_attention(ctypes.byref(self._c), batch, heads, nq,
+                                               _int32(window, "window"), _int32(sinks, "sinks"),
                                                float(scale), IO_TYPES[q.dtype], _rows(q), _rows(o), _at(lse),
                                                _at(page_table), page_table.shape[1], _at(lengths),
                                                _current_stream(self.device),

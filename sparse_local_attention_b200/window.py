@@ -103,6 +103,14 @@ def _current_stream(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _int32(n, name: str) -> int:
+    """n as the C call takes it: an int32 argument would lose the bits above."""
+    n = int(n)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name}: expected a 32-bit integer, got {n}")
+    return n
+
+
 def _at(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -153,9 +161,12 @@ class _Call:
         kv_heads, nk = self.kv_shape[1:3]
         self.packed = cu_q is not None
         self.cu_q, self.cu_kv = cu_q, cu_kv
+        window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
         if self.packed:
             if batch != 1:
                 raise ValueError("packed sequences: expected a batch of 1")
+            if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or not cu_q.numel():
+                raise ValueError("cu_q: expected int32 [sequences + 1]")
             batch = cu_q.numel() - 1
             _flat(cu_q, "cu_q", (batch + 1,), torch.int32, q.device)
             _flat(cu_kv, "cu_kv", (batch + 1,), torch.int32, q.device)
@@ -164,9 +175,15 @@ class _Call:
         else:
             rows = (0, 0)
         self.empty = 0 in self.q_shape or (self.packed and batch == 0)
+        # no key rows: queries see nothing.  The packed form still has to tell
+        # the rows of its sequences from the rest, over a key row that none owns.
+        self.no_keys = 0 in self.kv_shape
+        if self.packed and self.no_keys and kv_heads and not self.empty:
+            self.k = self.v = q.new_zeros((1, kv_heads, 1, d))
+            self.no_keys = False
         if not self.empty:
             self.problem, self.fwd_bytes, self.bwd_bytes = _sized(
-                batch, heads, kv_heads, d, nq, nk, *rows, int(window), int(sinks), IO_TYPES[q.dtype], float(scale))
+                batch, heads, kv_heads, d, nq, nk, *rows, window, sinks, IO_TYPES[q.dtype], float(scale))
 
 
 def _forward(c: _Call, o=None, lse=None, workspace=None, check=False, want_lse=True):
@@ -182,7 +199,7 @@ def _forward(c: _Call, o=None, lse=None, workspace=None, check=False, want_lse=T
             lse.fill_(float("-inf"))
     _flat(lse, "lse", c.q_shape[:3], torch.float32, c.device)
     if not c.empty:
-        if 0 in c.kv_shape:  # no keys at all: every row is empty
+        if c.no_keys:
             o.zero_()
             if lse is not None:
                 lse.fill_(float("-inf"))
@@ -201,18 +218,21 @@ def _backward(c: _Call, o, lse, dout, dq=None, dk=None, dv=None, workspace=None,
     _flat(lse, "lse", c.q_shape[:3], torch.float32, c.device)
     outs, new = [], []
     for t, like, shape, name in ((dq, c.q, c.q_shape, "dq"), (dk, c.k, c.kv_shape, "dk"), (dv, c.v, c.kv_shape, "dv")):
-        outs.append(_new(like) if t is None else _output(t, name, shape, c.dtype, c.device))
+        outs.append(_output(t, name, shape, c.dtype, c.device) if t is not None else
+                    _new(like) if like.shape == shape else like.new_empty(shape))
         if t is None:
             new.append(outs[-1])
     dq, dk, dv = outs
-    if c.empty or 0 in c.kv_shape:
-        torch._foreach_zero_(outs)
-        return dq, dk, dv
     if c.packed and new:  # rows outside every sequence are not written
         torch._foreach_zero_(new)
+    if c.empty or c.no_keys:
+        if not c.packed:
+            torch._foreach_zero_(outs)
+        return dq, dk, dv
+    dk_rows, dv_rows = (_rows(t if 0 not in c.kv_shape else torch.empty_like(c.k)) for t in (dk, dv))
     ws = _scratch(workspace, c.bwd_bytes, c.device)
     st = lib().sta_window_backward(ctypes.byref(c.problem), _rows(c.q), _rows(c.k), _rows(c.v), _rows(o), _at(lse),
-                                   _rows(dout), _rows(dq), _rows(dk), _rows(dv), _at(c.cu_q), _at(c.cu_kv),
+                                   _rows(dout), _rows(dq), dk_rows, dv_rows, _at(c.cu_q), _at(c.cu_kv),
                                    ws.data_ptr(), ws.nbytes, _current_stream(c.device),
                                    STA_CALL_CHECK if check else 0)
     _check(st, "sta_window_backward")
@@ -284,8 +304,10 @@ class _SlidingWindowAttention(torch.autograd.Function):
                     _note_use(ctx, t, stream)
             c = _Call(q, k, v, *args)
             o, lse = _forward(c)
-        ctx.save_for_backward(c.q, c.k, c.v, o, lse)
-        c.q = c.k = c.v = None  # autograd's to keep, and to let go after the backward
+        # autograd's to keep, to let go after the backward, and to refuse where
+        # they have been written to in between
+        ctx.save_for_backward(c.q, c.k, c.v, o, lse, c.cu_q, c.cu_kv)
+        c.q = c.k = c.v = c.cu_q = c.cu_kv = None
         ctx.call = c
         return o
 
@@ -293,7 +315,7 @@ class _SlidingWindowAttention(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         c = copy.copy(ctx.call)
-        c.q, c.k, c.v, o, lse = ctx.saved_tensors
+        c.q, c.k, c.v, o, lse, c.cu_q, c.cu_kv = ctx.saved_tensors
         with _on(o.device, None):
             dq, dk, dv = _backward(c, o, lse, dout)
         return dq, dk, dv, None

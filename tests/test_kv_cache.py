@@ -362,3 +362,20 @@ def test_binding_refusals_on_device():
     for args in ((k, k.view(E4M3), s, s), (k, k, s[..., :1], s), (k, k, s.half(), s), (k[0], k[0], s, s), (k, k, s[:1], s[:1])):
         with pytest.raises(ValueError):
             KVCache.from_tensors(*args)
+
+
+@pytest.mark.gpu
+def test_a_cache_keeps_its_tensors():
+    """The calls use the tensors' addresses, so that no other tensor can take their place."""
+    c = KVCache(2, 1, 16, 64, block=16)
+    for name in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, torch.zeros_like(getattr(c, name)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", [dict(window=2 ** 32 + 3), dict(sinks=2 ** 32)])
+def test_numbers_past_32_bits_are_refused(kw):
+    c = KVCache(2, 1, 16, 64, block=16)
+    with pytest.raises(ValueError, match="32-bit"):
+        c.attention(torch.zeros(1, 2, 1, 64, dtype=BF16, device="cuda"), ints(0).view(1, 1).cuda(), ints(3).cuda(), **kw)

@@ -173,6 +173,46 @@ def test_packed_bounds_cut_and_bad_starts_are_dropped():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cu", [[3, 5, 5], [7]], ids=["two", "none"])
+def test_packed_sequences_without_keys_leave_the_other_rows(cu):
+    """Key tensors without a row, and no sequence at all: rows of sequences are
+    empty ones, rows outside stay as they were in tensors that are passed in."""
+    q, k, v, do = (t.cuda() for t in make(4, 2, 9, 0, 64, BF16))
+    cu_q = torch.tensor(cu, dtype=torch.int32).cuda()
+    seqs = dict(cu_q=cu_q, cu_kv=torch.zeros_like(cu_q))
+    o, lse, dq = torch.full_like(q, 7.0), torch.full((1, 4, 9), 7.0, device="cuda"), torch.full_like(q, 7.0)
+    window_forward(q, k, v, 5, 1, o=o, lse=lse, check=True, **seqs)
+    _, dk, dv = window_backward(q, k, v, o, lse, do, 5, 1, dq=dq, check=True, **seqs)
+    assert dk.shape == k.shape and dv.shape == v.shape
+    inside = torch.zeros(9, dtype=torch.bool)
+    inside[cu[0]:cu[-1]] = True
+    for t, empty in ((o, 0.0), (lse, float("-inf")), (dq, 0.0)):
+        assert (t[:, :, inside] == empty).all() and (t[:, :, ~inside] == 7.0).all()
+    q.requires_grad_()
+    out = sliding_window_attention(q, k, v, 5, 1, **seqs)
+    out.backward(do)
+    assert not out.any() and not q.grad.any()
+
+
+@pytest.mark.gpu
+def test_bounds_written_to_before_the_backward_are_noticed():
+    q, k, v, do = (t.cuda() for t in make(2, 1, 9, 9, 64, BF16))
+    cu = torch.tensor([0, 4, 9], dtype=torch.int32).cuda()
+    o = sliding_window_attention(q.requires_grad_(), k, v, 5, cu_q=cu, cu_kv=cu)
+    cu[1] = 5
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.backward(do)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", [dict(window=2 ** 32 + 3), dict(sinks=2 ** 32), dict(window=-2 ** 31 - 1)])
+def test_numbers_past_32_bits_are_refused(kw):
+    q, k, v, _ = (t.cuda() for t in make(2, 1, 9, 9, 64, BF16))
+    with pytest.raises(ValueError, match="32-bit"):
+        window_forward(q, k, v, **kw)
+
+
+@pytest.mark.gpu
 def test_hidden_keys_reach_nothing():
     """Keys that no query of the call sees hold NaN and infinities (and values
     of the type's lowest and highest)."""
