@@ -322,9 +322,10 @@ sta_status sta_window_workspace_size(const sta_window_problem *problem, size_t *
  * batch + 1 int32; sequence b is rows [cu[b], cu[b + 1]) of every head, at
  * most q_len / kv_len of them, inside [0, q_rows) / [0, kv_rows) (what lies
  * outside is dropped).  Rows of o and lse outside every sequence are not
- * written.  Calls of few query rows (a rule on the problem's sizes alone) split
+ * written, or become zeros and -inf with STA_PACKED_ZERO in flags.  Calls of few query rows (a rule on the problem's sizes alone) split
  * the keys over the GPU and join the parts; the others run on the tensor
  * cores' 128-row tiles. */
+#define STA_PACKED_ZERO 0x4u
 sta_status sta_window_forward(const sta_window_problem *problem, const sta_rows *q, const sta_rows *k,
                               const sta_rows *v, const sta_rows *o, float *lse, const int32_t *cu_q,
                               const int32_t *cu_kv, void *workspace, size_t workspace_bytes, void *stream,
@@ -333,7 +334,8 @@ sta_status sta_window_forward(const sta_window_problem *problem, const sta_rows 
 /* Gradients of sta_window_forward (the formulas of sta_backward over the
  * visible pairs).  o and lse as the forward wrote them; dk and dv sum over the
  * query heads that share a key head, in fp32 and in a fixed order, and rows
- * outside every sequence of a packed call are not written.  fp16: products
+ * outside every sequence of a packed call are not written, or become zeros with
+ * STA_PACKED_ZERO in flags (where q_len is above 0).  fp16: products
  * |dO_i| |V_j| are scaled to the largest |dO_i|, and V rows up to a norm of 8192
  * do not overflow. */
 sta_status sta_window_backward(const sta_window_problem *problem, const sta_rows *q, const sta_rows *k,

@@ -39,7 +39,7 @@ bool io_type_ok(int32_t t) { return t == STA_TYPE_BF16 || t == STA_TYPE_FP16; }
 sta_status check_problem(const sta_window_problem *p) {
   if (!p) return STA_ERR_INVALID_ARG;
   if (p->batch < 1 || p->heads < 1 || p->kv_heads < 1 || p->q_len < 0 || p->kv_len < 0 || p->q_rows < 0 ||
-      p->kv_rows < 0 || p->heads % p->kv_heads || p->batch > 65535 || p->heads > 65535)
+      p->kv_rows < 0 || p->heads % p->kv_heads || p->batch > 65534 || p->heads > 65535)
     return STA_ERR_SHAPE;
   if (p->head_dim != 64 && p->head_dim != 128) return STA_ERR_UNSUPPORTED;
   if (!io_type_ok(p->type)) return STA_ERR_UNSUPPORTED;
@@ -147,6 +147,10 @@ sta_status finish(void *ws, cudaStream_t stream, uint32_t flags) {
     if (st != 0) return STA_ERR_TIMEOUT;
   }
   return STA_OK;
+}
+
+bool bad_window_call(uint32_t flags, const int32_t *cu_q, const int32_t *cu_kv) {
+  return (flags & ~(STA_CALL_CHECK | (cu_q ? STA_PACKED_ZERO : 0u))) || (cu_q == nullptr) != (cu_kv == nullptr);
 }
 
 sta_status check_tensors(const sta_window_problem *p, bool packed, const sta_rows *const *q_side, int nq,
@@ -276,7 +280,7 @@ sta_status sta_window_forward(const sta_window_problem *p, const sta_rows *q, co
                               const sta_rows *o, float *lse, const int32_t *cu_q, const int32_t *cu_kv, void *ws,
                               size_t ws_bytes, void *stream_, uint32_t flags) {
   if (const sta_status st = check_problem(p)) return st;
-  if ((flags & ~STA_CALL_CHECK) || (cu_q == nullptr) != (cu_kv == nullptr)) return STA_ERR_INVALID_ARG;
+  if (bad_window_call(flags, cu_q, cu_kv)) return STA_ERR_INVALID_ARG;
   const sta_rows *qs[] = {q, o}, *ks[] = {k, v};
   if (const sta_status st = check_tensors(p, cu_q, qs, 2, ks, 2)) return st;
   if (const sta_status st = check_workspace(ws, ws_bytes, window_fwd_bytes(p))) return st;
@@ -284,6 +288,8 @@ sta_status sta_window_forward(const sta_window_problem *p, const sta_rows *q, co
   sta::WinParams w = window_params(p, cu_q, cu_kv, ws);
   w.q = rows_of(q), w.k = rows_of(k), w.v = rows_of(v), w.o = rows_of(o), w.lse = lse;
   if ((flags & STA_CALL_CHECK) && cudaMemsetAsync(ws, 0, sizeof(int), stream) != cudaSuccess) return STA_ERR_CUDA;
+  w.zero = (flags & STA_PACKED_ZERO) != 0;
+  if (w.zero && p->q_rows > 0 && sta::launch_window_clear(w, stream) != cudaSuccess) return STA_ERR_CUDA;
   if (p->q_len > 0) {
     if (splits_keys(p)) {
       if (sta::launch_window_split(w, p->type, stream) != cudaSuccess) return STA_ERR_CUDA;
@@ -302,7 +308,7 @@ sta_status sta_window_backward(const sta_window_problem *p, const sta_rows *q, c
                                const sta_rows *dk, const sta_rows *dv, const int32_t *cu_q, const int32_t *cu_kv,
                                void *ws, size_t ws_bytes, void *stream_, uint32_t flags) {
   if (const sta_status st = check_problem(p)) return st;
-  if ((flags & ~STA_CALL_CHECK) || (cu_q == nullptr) != (cu_kv == nullptr) || !lse) return STA_ERR_INVALID_ARG;
+  if (bad_window_call(flags, cu_q, cu_kv) || !lse) return STA_ERR_INVALID_ARG;
   const sta_rows *qs[] = {q, o, dout, dq}, *ks[] = {k, v, dk, dv};
   if (const sta_status st = check_tensors(p, cu_q, qs, 4, ks, 4)) return st;
   if (const sta_status st = check_workspace(ws, ws_bytes, window_bwd_bytes(p))) return st;
@@ -311,6 +317,7 @@ sta_status sta_window_backward(const sta_window_problem *p, const sta_rows *q, c
   w.q = rows_of(q), w.k = rows_of(k), w.v = rows_of(v), w.o = rows_of(o), w.dout = rows_of(dout);
   w.dq = rows_of(dq), w.dk = rows_of(dk), w.dv = rows_of(dv);
   w.lse = const_cast<float *>(lse);
+  w.zero = (flags & STA_PACKED_ZERO) != 0;
   const BackwardLayout l = backward_layout(p);
   char *base = static_cast<char *>(ws);
   w.dd = reinterpret_cast<float *>(base + l.dd);

@@ -82,6 +82,40 @@ __device__ __forceinline__ bool visible(int pos, int key, int window, int sinks)
   return key <= pos && (key > pos - window || key < sinks);
 }
 
+// Whether a row of a packed tensor is in a sequence.  Exact where the starts
+// ascend; of starts that do not, some rows of sequences are called outside.
+__device__ __forceinline__ bool in_sequence(const int32_t *cu, int batch, int rows, int longest, int row) {
+  int lo = 0, hi = batch - 1;  // the last sequence that starts at or before the row
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (__ldg(cu + mid) <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  int first, n;
+  packed_range(cu, lo, rows, longest, first, n);
+  return row >= first && row < first + n;
+}
+
+// Rows [32 i, 32 i + 32) of up to two packed tensors (and lse) that no sequence
+// holds become zeros (-inf), by one warp.  What writes the sequences' rows runs
+// afterwards.
+__device__ __forceinline__ void clear_outside(const int32_t *cu, int batch, int rows, int longest, int i, int heads, int d,
+                                              const Rows &x, const Rows &y, float *lse) {
+  const int lane = threadIdx.x & 31, row0 = 32 * i, mine = row0 + lane;
+  uint32_t out = __ballot_sync(0xffffffffu, mine < rows && !in_sequence(cu, batch, rows, longest, mine));
+  const int per = d / 8, pieces = heads * per;  // 16 bytes each
+  for (; out; out &= out - 1) {
+    const long long row = row0 + __ffs(out) - 1;
+    for (int j = lane; j < pieces; j += 32) {
+      const int h = j / per, at = 16 * (j % per);
+      *reinterpret_cast<uint4 *>(x.p + 2 * (h * x.h + row * x.r) + at) = make_uint4(0u, 0u, 0u, 0u);
+      if (y.p) *reinterpret_cast<uint4 *>(y.p + 2 * (h * y.h + row * y.r) + at) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (lse)
+      for (int h = lane; h < heads; h += 32) lse[(long long)h * rows + row] = -INFINITY;
+  }
+}
+
 // Page that holds token `pos` of sequence b, or -1 (absent, or past the table).
 __device__ __forceinline__ int page_of(const CacheParams &c, int b, int pos) {
   const int i = pos / c.page_size;

@@ -40,6 +40,7 @@ struct WinParams {
   float *parts;    // fp32 sums of dK and dV of the parts of key blocks
   int seg_chunks;  // chunks of 128 queries per part
   int sink_blocks, sink_segs, norm_segs;  // key blocks that hold sinks; parts per block there and elsewhere, at most
+  bool zero;       // packed: rows outside every sequence become zeros (-inf in lse)
   int *status;
   unsigned long long wait_limit_ns;
 };
@@ -80,7 +81,9 @@ struct CacheAttn {
 };
 cudaError_t launch_cache_attention(const CacheAttn &a, int cache_type, int io_type, cudaStream_t stream);
 
-// Forward on 128-row tiles; maps: q, k, v.
+// o and lse of rows outside every sequence (p.zero).
+cudaError_t launch_window_clear(const WinParams &p, cudaStream_t stream);
+// Forward on 128-row tiles; maps: q, k, v.  With p.zero, after launch_window_clear.
 cudaError_t launch_window_tiles(const WinParams &p, int type, const CUtensorMap *maps, cudaStream_t stream);
 // Forward of a few query rows per key head, the keys split over the GPU.
 cudaError_t launch_window_split(const WinParams &p, int type, cudaStream_t stream);

@@ -111,7 +111,17 @@ __device__ __forceinline__ float ds_factor(const WinParams &p, float *smem_word)
 template <int D, class T>
 __global__ void __launch_bounds__(256) window_pre_kernel(const WinParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-  const int lane = threadIdx.x & 31, sub = lane / kLanes, part = lane % kLanes, h = blockIdx.y, b = blockIdx.z;
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, part = lane % kLanes, h = blockIdx.y;
+  int b = blockIdx.z;
+  if (p.zero && b-- == 0) {
+    // the first blocks: gradients of rows outside every sequence
+    const int q_parts = (p.q_rows + 31ll) / 32, kv_parts = (p.kv_rows + 31ll) / 32, warps = gridDim.x * gridDim.y * 8;
+    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * 8 + (threadIdx.x >> 5); i < q_parts + kv_parts; i += warps) {
+      if (i < q_parts) clear_outside(p.cu_q, p.batch, p.q_rows, p.q_len, i, p.heads, D, p.dq, Rows{}, nullptr);
+      else clear_outside(p.cu_kv, p.batch, p.kv_rows, p.kv_len, i - q_parts, p.kv_heads, D, p.dk, p.dv, nullptr);
+    }
+    return;
+  }
   const Sequence s = sequence(p, b);
   float norm = 0.f;
   const long long aug0 = aug_row(p, s, b, h);
@@ -1085,7 +1095,8 @@ cudaError_t launch(const WinParams &p, const CUtensorMap *m, cudaStream_t stream
   if (const cudaError_t e = allow_shared(window_dq_kernel<D, T>, (int)Q::kSmem, done_q)) return e;
   const int nqb = (p.q_len + kBM - 1) / kBM, nkb = (p.kv_len + kBM - 1) / kBM, slices = p.batch * p.kv_heads;
   if (nqb > 0)
-    window_pre_kernel<D, T><<<dim3((p.q_len + pre_rows(D) - 1) / pre_rows(D), p.heads, p.batch), 256, 0, stream>>>(p);
+    window_pre_kernel<D, T>
+        <<<dim3((p.q_len + pre_rows(D) - 1) / pre_rows(D), p.heads, p.batch + p.zero), 256, 0, stream>>>(p);
   const int kv_items = (p.sink_blocks * p.sink_segs + (nkb - p.sink_blocks) * p.norm_segs) * slices;
   const int q_items = nqb * p.batch * p.heads;
   if (kv_items > 0) window_dkdv_kernel<D, T><<<kv_items, K::R::kThreads, K::kSmem, stream>>>(m[0], m[1], m[2], m[3], p);

@@ -554,6 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool none = l == 0.f;
       const float inv_l = none ? 0.f : 1.f / l;
       f[0] *= inv_l, f[1] *= inv_l;
+      // rows outside the sequences have been cleared
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       // the quad's first row, and how many of its rows there are
       char *dst = p.o.p + 2 * ((long long)it.s.slice * p.o.b + (long long)it.h[u] * p.o.h +
                                (long long)(it.s.q0 + (qrow & ~3)) * p.o.r);
@@ -608,14 +610,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmCols);
   }
+  // this grid does not end before window_clear
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// A warp per 32 rows.
+__global__ void __launch_bounds__(256) window_clear_kernel(const WinParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i * 32ll < p.q_rows) clear_outside(p.cu_q, p.batch, p.q_rows, p.q_len, i, p.heads, p.d, p.o, Rows{}, p.lse);
 }
 
 template <int D, class T, bool kSplit>
 cudaError_t launch_mode(const WinParams &p, const CUtensorMap *maps, long long items, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   if (const cudaError_t e = allow_shared(window_fwd_kernel<D, T, kSplit>, (int)Cfg<D>::kSmem, done)) return e;
-  window_fwd_kernel<D, T, kSplit><<<(unsigned)items, kThreads, Cfg<D>::kSmem, stream>>>(maps[0], maps[1], maps[2], p);
-  return cudaGetLastError();
+  // beside window_clear: only its stores wait for that
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)items), cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<D>::kSmem, cfg.stream = stream;
+  cfg.attrs = &early, cfg.numAttrs = p.zero ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, window_fwd_kernel<D, T, kSplit>, maps[0], maps[1], maps[2], p);
 }
 
 // Pairs of units share their keys; where one round of the GPU has room for
@@ -631,6 +649,11 @@ cudaError_t launch(const WinParams &p, const CUtensorMap *maps, cudaStream_t str
 }
 
 }  // namespace
+
+cudaError_t launch_window_clear(const WinParams &p, cudaStream_t stream) {
+  window_clear_kernel<<<(unsigned)((p.q_rows + 255ll) / 256), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_window_tiles(const WinParams &p, int type, const CUtensorMap *maps, cudaStream_t stream) {
   if (p.d == 128)

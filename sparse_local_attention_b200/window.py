@@ -20,6 +20,7 @@ from torch.autograd.function import once_differentiable
 
 from .sta import STA_CALL_CHECK, _check, _Rows, lib
 
+STA_PACKED_ZERO = 0x4
 STA_TYPE_BF16, STA_TYPE_FP16, STA_TYPE_E4M3, STA_TYPE_INT8 = 0, 1, 2, 3
 IO_TYPES = {torch.bfloat16: STA_TYPE_BF16, torch.float16: STA_TYPE_FP16}
 
@@ -187,17 +188,23 @@ class _Call:
 
 
 def _forward(c: _Call, o=None, lse=None, workspace=None, check=False, want_lse=True):
+    new = []
     if o is None:
         o = _new(c.q)
-        if c.packed:  # rows outside every sequence are not written
-            o.zero_()
+        new.append((o, 0.0))
     else:
         _output(o, "o", c.q_shape, c.dtype, c.device)
     if lse is None and want_lse:
         lse = torch.empty(c.q_shape[:3], dtype=torch.float32, device=c.device)
-        if c.packed:
-            lse.fill_(float("-inf"))
+        new.append((lse, float("-inf")))
     _flat(lse, "lse", c.q_shape[:3], torch.float32, c.device)
+    flags = STA_CALL_CHECK if check else 0
+    if c.packed:  # rows outside every sequence are not written
+        if len(new) == 1 + (lse is not None) and not c.empty:
+            flags |= STA_PACKED_ZERO
+        else:
+            for t, value in new:
+                t.fill_(value)
     if not c.empty:
         if c.no_keys:
             o.zero_()
@@ -207,7 +214,7 @@ def _forward(c: _Call, o=None, lse=None, workspace=None, check=False, want_lse=T
         ws = _scratch(workspace, c.fwd_bytes, c.device)
         st = lib().sta_window_forward(ctypes.byref(c.problem), _rows(c.q), _rows(c.k), _rows(c.v), _rows(o), _at(lse),
                                       _at(c.cu_q), _at(c.cu_kv), ws.data_ptr(), ws.nbytes,
-                                      _current_stream(c.device), STA_CALL_CHECK if check else 0)
+                                      _current_stream(c.device), flags)
         _check(st, "sta_window_forward")
     return o, lse
 
@@ -223,8 +230,12 @@ def _backward(c: _Call, o, lse, dout, dq=None, dk=None, dv=None, workspace=None,
         if t is None:
             new.append(outs[-1])
     dq, dk, dv = outs
+    flags = STA_CALL_CHECK if check else 0
     if c.packed and new:  # rows outside every sequence are not written
-        torch._foreach_zero_(new)
+        if len(new) == 3 and not c.empty:
+            flags |= STA_PACKED_ZERO
+        else:
+            torch._foreach_zero_(new)
     if c.empty or c.no_keys:
         if not c.packed:
             torch._foreach_zero_(outs)
@@ -233,8 +244,7 @@ def _backward(c: _Call, o, lse, dout, dq=None, dk=None, dv=None, workspace=None,
     ws = _scratch(workspace, c.bwd_bytes, c.device)
     st = lib().sta_window_backward(ctypes.byref(c.problem), _rows(c.q), _rows(c.k), _rows(c.v), _rows(o), _at(lse),
                                    _rows(dout), _rows(dq), dk_rows, dv_rows, _at(c.cu_q), _at(c.cu_kv),
-                                   ws.data_ptr(), ws.nbytes, _current_stream(c.device),
-                                   STA_CALL_CHECK if check else 0)
+                                   ws.data_ptr(), ws.nbytes, _current_stream(c.device), flags)
     _check(st, "sta_window_backward")
     return dq, dk, dv
 

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import seq_ref
-from sparse_local_attention_b200 import sliding_window_attention, sta, window_backward, window_forward
+from sparse_local_attention_b200 import sliding_window_attention, sta, window, window_backward, window_forward
 from sparse_local_attention_b200.window import _WindowProblem
 
 BF16, FP16 = torch.bfloat16, torch.float16
@@ -192,6 +192,28 @@ def test_packed_sequences_without_keys_leave_the_other_rows(cu):
     out = sliding_window_attention(q, k, v, 5, 1, **seqs)
     out.backward(do)
     assert not out.any() and not q.grad.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv_heads,d,dtype,max_n", [(2, 1, 64, BF16, 0), (6, 3, 128, FP16, 0), (2, 2, 128, BF16, 70)])
+@pytest.mark.parametrize("cu", [[40, 41, 41, 300, 433], [0, 16], [470, 500], [9, 9], [-7, 200, 10 ** 6]],
+                         ids=["gaps", "tail", "head", "empty", "wild"])
+def test_new_packed_outputs_are_empty_outside_the_sequences(monkeypatch, heads, kv_heads, d, dtype, max_n, cu):
+    """Rows before, behind and between sequences (cut ones) hold zeros, -inf in lse,
+    whatever the memory held; the others are those of outputs that are passed in."""
+    n = 500
+    q, k, v, do = (t.cuda() for t in make(heads, kv_heads, n, n, d, dtype, seed=n))
+    kw = dict(cu_q=torch.tensor(cu, dtype=torch.int32).cuda(), cu_kv=torch.tensor(cu, dtype=torch.int32).cuda(),
+              max_q=max_n, max_kv=max_n, check=True)
+    o, lse = torch.zeros_like(q), torch.full(q.shape[:3], float("-inf"), device="cuda")
+    window_forward(q, k, v, 60, 4, o=o, lse=lse, **kw)
+    grads = [torch.zeros_like(t) for t in (q, k, v)]
+    window_backward(q, k, v, o, lse, do, 60, 4, dq=grads[0], dk=grads[1], dv=grads[2], **kw)
+    monkeypatch.setattr(window, "_new", lambda like: torch.full_like(like, 7.0))
+    o2, lse2 = window_forward(q, k, v, 60, 4, **kw)
+    new = window_backward(q, k, v, o, lse, do, 60, 4, **kw)
+    for a, b in zip((o, lse, *grads), (o2, lse2, *new)):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.gpu
