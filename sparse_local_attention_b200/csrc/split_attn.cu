@@ -18,7 +18,7 @@
 // which the matrix instructions take.
 //
 // With one row per sequence the bound is reading the keys: 64 sequences up to
-// 8192 tokens, 8 key heads, d 128, e4m3: 148 us for 0.70 GB, 4.8 TB/s (73% of a
+// 8192 tokens, 8 key heads, d 128, e4m3: 129 us for 0.70 GB, 5.5 TB/s (83% of a
 // copy's rate).  With 16 rows and d 64 it is the instructions of a step, 480 per
 // warp, most of them the widening of the codes and the softmax (32 sequences x 4
 // tokens, 16 heads over 4, window 4096, int8: 32 us for 68 MB).  Small calls are
@@ -123,10 +123,15 @@ struct CacheKeys {
   CacheAttn a;
   int b, hk, nk, nq;
   static constexpr int kRowBytes = D;
+  __device__ __forceinline__ int length(int i) const {
+    return min(max(__ldg(a.lengths + i), 0), a.c.table_pages * a.c.page_size);
+  }
   __device__ __forceinline__ void open(int slice) {
     b = slice / a.c.kv_heads, hk = slice % a.c.kv_heads, nq = a.q_len;
-    nk = min(max(__ldg(a.lengths + b), 0), a.c.table_pages * a.c.page_size);
+    nk = length(b);
   }
+  __device__ __forceinline__ int batch() const { return a.batch; }
+  __device__ __forceinline__ int kv_heads() const { return a.c.kv_heads; }
   __device__ __forceinline__ const char *q_row(int h, int i) const {
     return a.q.p + 2 * (b * a.q.b + h * a.q.h + i * a.q.r);
   }
@@ -195,6 +200,9 @@ struct RowKeys {
   Sequence s;
   int hk, nk, nq;
   static constexpr int kRowBytes = 2 * D;
+  __device__ __forceinline__ int length(int i) const { return sequence(p, i).nk; }
+  __device__ __forceinline__ int batch() const { return p.batch; }
+  __device__ __forceinline__ int kv_heads() const { return p.kv_heads; }
   __device__ __forceinline__ void open(int slice) {
     hk = slice % p.kv_heads;
     s = sequence(p, slice / p.kv_heads);
@@ -257,8 +265,36 @@ __device__ __forceinline__ int v_place(int row, int col) {
 
 struct SplitShape {
   int splits, group, window, sinks;
+  int span;      // keys that the rows of a sequence may see, at most
+  bool by_keys;  // slices in the order of their keys, most first
   float scale_log2;
 };
+
+// The slice'th slice (sequence and key head) by the keys it reads, most first, so
+// that the longest do not start last.  By the whole CTA, for at most kThreads
+// sequences; `words` holds kThreads + 1 of them.
+template <class Keys>
+__device__ __forceinline__ int by_keys(const Keys &keys, int slice, int span, uint32_t *words) {
+  const int t = threadIdx.x, n = keys.batch(), want = slice / keys.kv_heads();
+  // steps up to 2^23 and the sequence's number: no two are equal
+  const uint32_t mine =
+      t < n ? (uint32_t)min(min(keys.length(t), span) / kStep + 1, (1 << 23) - 1) << 8 | (uint32_t)(kThreads - 1 - t) : 0u;
+  words[t] = mine;
+  __syncthreads();
+  if (mine) {
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; j += 4) {
+      const uint4 w = *reinterpret_cast<const uint4 *>(words + j);  // zeros past the last one
+      rank += (w.x > mine) + (w.y > mine) + (w.z > mine) + (w.w > mine);
+    }
+    if (rank == want) words[kThreads] = t;
+  }
+  __syncthreads();
+  const int b = words[kThreads];
+  __syncthreads();  // before anything else is written there
+  return b * keys.kv_heads() + slice % keys.kv_heads();
+}
 
 // NT groups of 8 query rows.  Grid: (splits x slices, row blocks), a cluster
 // per slice.
@@ -277,7 +313,9 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
   float *all_m = cta_l + kRows, *all_l = all_m + kMaxSplits * kRows;  // [splits][kRows]
   Keys keys = keys_in;
   const int rank = blockIdx.x % shape.splits;
-  keys.open(blockIdx.x / shape.splits);
+  int slice = blockIdx.x / shape.splits;
+  if (shape.by_keys) slice = by_keys(keys, slice, shape.span, reinterpret_cast<uint32_t *>(smem));
+  keys.open(slice);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int group = shape.group, row0 = blockIdx.y * kRows, rows = min(kRows, keys.nq * group - row0);
   // row r is query r / group of head r % group of the key head's
@@ -623,20 +661,21 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
 }
 
 // Blocks per slice (units: slices and row blocks).  As many as fill the GPU
-// once, with a step for each warp; beyond that, while sequences of uneven
-// length would leave SMs idle at the end, up to three times the GPU, with 16
-// steps for each warp.  Measured with 1 / 2 / 4 / 8 / 16 blocks, in us (* chosen):
-//   1 x 1031 tokens, d 128, cache:             14.0  11.4   9.4   8.5   8.6*
-//   1 x 8192, 16 heads over 4, d 128, bf16:    63.4  36.7  22.3  15.6  12.2*
-//   8 x 1024, 24 heads over 8, d 128, bf16:    14.5  12.3* 18.5  36.2  63.4
-//   32 x 4096, 4 key heads, d 64, cache:       41.0  32.0* 40.0  57.6   111
-//   64 x 1500, 16 heads over 4, d 64, bf16:    17.2* 22.5  32.1  55.2   107
-//   64 x up to 8192, 8 key heads, d 128, cache: 157   146*  164   223   378
+// once, with a step for each warp; and twice that where the slices are no more
+// than the GPU holds and each warp is left 16 steps.  Measured with 1 / 2 / 4 / 8
+// / 16 blocks, in us (* chosen):
+//   1 x 1031 tokens, d 128, cache:              14.0  11.4   9.4   8.5   8.6*
+//   1 x 8192, 16 heads over 4, d 128, bf16:     63.4  36.7  22.3  15.6  12.2*
+//   8 x 1024, 24 heads over 8, d 128, bf16:     14.5  12.3* 18.5  36.2  63.4
+//   32 x 4096, 4 key heads, d 64, cache:        41.0  32.0* 40.0  57.6   111
+//   64 x 1500, 16 heads over 4, d 64, bf16:     17.2* 22.5  32.1  55.2   107
+//   32 x up to 8192, 8 key heads, d 128, cache: 87.5  76.3* 88.0
+//   64 x up to 8192, 8 key heads, d 128, cache:  124* 136   166   223   378
 int splits_for(long long units, long long most_keys, int ctas) {
   const long long steps = (most_keys + kStep - 1) / kStep, room = 148ll * ctas;
   int s = 1;
   while (s < kMaxSplits && ((units * 2 * s <= room && steps >= 2ll * s * kWarps) ||
-                            (units * s < 3 * room && steps >= 2ll * s * kWarps * 16)))
+                            (units * s <= room && steps >= 2ll * s * kWarps * 16)))
     s *= 2;
   return s;
 }
@@ -655,11 +694,20 @@ cudaError_t allow_wide_clusters(Kernel *kernel, std::atomic<uint64_t> &done) {
 }
 
 template <int D, int NT, class Keys>
-cudaError_t launch(const Keys &keys, SplitShape shape, long long slices, int rows, long long most_keys,
+cudaError_t launch(const Keys &keys, SplitShape shape, long long slices, int rows, long long longest,
                    cudaStream_t stream) {
   auto *kernel = split_attn_kernel<D, NT, Keys>;
+  const long long most_keys = longest < shape.span ? longest : shape.span;
   const int blocks = (rows + 8 * NT - 1) / (8 * NT);
   shape.splits = splits_for(slices * blocks, most_keys, SplitCfg<D, NT, Keys>::kCtas);
+  // Sequences in the order of their keys where that shortens the end: more blocks
+  // than the GPU holds, but not many rounds of them (the order costs each 1.5 us);
+  // keys enough for a difference; and no window that makes most of them equal.
+  // Measured as they come / most first, in us, 8 key heads, d 128, cache: 64 x up
+  // to 8192 159 / 124, 100 x 3000 89 / 80, 64 x 1000 32 / 30; left as they come:
+  // 200 x 1500 89 / 98, 256 x 300 53 / 69, 64 x 8192 with a window of 2000 57 / 60.
+  const long long room = 148 * SplitCfg<D, NT, Keys>::kCtas, all = slices * blocks * shape.splits;
+  shape.by_keys = shape.by_keys && all > room && all <= 4 * room && most_keys >= 512 && 2ll * shape.span >= longest;
   constexpr size_t smem = SplitCfg<D, NT, Keys>::kSmem;
   static std::atomic<uint64_t> done{0}, wide{0};
   if (const cudaError_t e = allow_shared(kernel, (int)smem, done)) return e;
@@ -675,42 +723,41 @@ cudaError_t launch(const Keys &keys, SplitShape shape, long long slices, int row
   return cudaLaunchKernelEx(&cfg, kernel, keys, shape);
 }
 
-// Up to 8 rows take one group (the case of 64 above: 148 us, with two groups 227;
-// 64 x 1500: 16.9 and 20.7).
+// Up to 8 rows take one group (64 x up to 8192 above, as they come in two blocks:
+// 149 us, with two groups 227; 64 x 1500: 16.9 and 20.7).
 template <int D, class Keys>
-cudaError_t launch_rows(const Keys &keys, const SplitShape &shape, long long slices, int rows, long long most_keys,
+cudaError_t launch_rows(const Keys &keys, const SplitShape &shape, long long slices, int rows, long long longest,
                         cudaStream_t stream) {
-  return rows <= 8 ? launch<D, 1>(keys, shape, slices, rows, most_keys, stream)
-                   : launch<D, 2>(keys, shape, slices, rows, most_keys, stream);
+  return rows <= 8 ? launch<D, 1>(keys, shape, slices, rows, longest, stream)
+                   : launch<D, 2>(keys, shape, slices, rows, longest, stream);
 }
 
-// keys that one query row may see
-long long visible_keys(long long nk, long long q_len, long long window, long long sinks) {
-  const long long w = window + q_len - 1 + sinks;
-  return w < nk ? w : nk;
+// `uneven`: sequences of lengths that only the device knows.
+SplitShape shape_of(int group, long long q_len, int window, int sinks, bool uneven, int batch, float scale_log2) {
+  const long long span = window + q_len - 1 + sinks;
+  return SplitShape{1, group, window, sinks, (int)(span < 0x7fffffff ? span : 0x7fffffff),
+                    uneven && batch > 1 && batch <= kThreads, scale_log2};
 }
 
 template <int D, int kType, class T>
 cudaError_t cache_launch(const CacheAttn &a, const SplitShape &shape, cudaStream_t stream) {
   CacheKeys<D, kType, T> keys{};
   keys.a = a;
-  const long long nk = (long long)a.c.table_pages * a.c.page_size;
   return launch_rows<D>(keys, shape, (long long)a.batch * a.c.kv_heads, a.q_len * a.group,
-                        visible_keys(nk, a.q_len, a.window, a.sinks), stream);
+                        (long long)a.c.table_pages * a.c.page_size, stream);
 }
 
 template <int D, class T>
 cudaError_t window_launch(const WinParams &p, const SplitShape &shape, cudaStream_t stream) {
   RowKeys<D, T> keys{};
   keys.p = p;
-  return launch_rows<D>(keys, shape, (long long)p.batch * p.kv_heads, p.q_len * p.group,
-                        visible_keys(p.kv_len, p.q_len, p.window, p.sinks), stream);
+  return launch_rows<D>(keys, shape, (long long)p.batch * p.kv_heads, p.q_len * p.group, p.kv_len, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_attention(const CacheAttn &a, int cache_type, int io_type, cudaStream_t stream) {
-  const SplitShape shape{1, a.group, a.window, a.sinks, a.scale_log2};
+  const SplitShape shape = shape_of(a.group, a.q_len, a.window, a.sinks, true, a.batch, a.scale_log2);
   auto io = [&](auto d, auto code) {
     constexpr int D = decltype(d)::value, kType = decltype(code)::value;
     return io_type == STA_TYPE_BF16 ? cache_launch<D, kType, __nv_bfloat16>(a, shape, stream)
@@ -724,7 +771,7 @@ cudaError_t launch_cache_attention(const CacheAttn &a, int cache_type, int io_ty
 }
 
 cudaError_t launch_window_split(const WinParams &p, int type, cudaStream_t stream) {
-  const SplitShape shape{1, p.group, p.window, p.sinks, p.scale_log2};
+  const SplitShape shape = shape_of(p.group, p.q_len, p.window, p.sinks, p.cu_q, p.batch, p.scale_log2);
   if (p.d == 128)
     return type == STA_TYPE_BF16 ? window_launch<128, __nv_bfloat16>(p, shape, stream)
                                  : window_launch<128, __half>(p, shape, stream);

@@ -379,3 +379,15 @@ def test_numbers_past_32_bits_are_refused(kw):
     c = KVCache(2, 1, 16, 64, block=16)
     with pytest.raises(ValueError, match="32-bit"):
         c.attention(torch.zeros(1, 2, 1, 64, dtype=BF16, device="cuda"), ints(0).view(1, 1).cuda(), ints(3).cuda(), **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch", [80, 256, 300])
+def test_many_sequences_of_uneven_lengths(batch):
+    """More sequences than the GPU holds at once, of lengths from none to all of
+    the table, equal ones among them: each as if alone."""
+    g = torch.Generator().manual_seed(batch)
+    lens = torch.randint(0, 641, (batch,), generator=g)
+    lens[1::3], lens[7] = 500, 640
+    p, table = filled(batch, lens.tolist(), 4, 64, 64, 64, INT8, seed=batch)
+    attend_and_check(p, table, lens.tolist(), randn(batch, 8, 1, 64, seed=1, dtype=FP16), 0, 0)
