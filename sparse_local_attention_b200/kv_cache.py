@@ -11,8 +11,8 @@ from typing import Optional
 import torch
 
 from .sta import STA_CALL_CHECK, _check, lib
-from .window import (IO_TYPES, STA_TYPE_E4M3, STA_TYPE_INT8, _at, _current_stream, _flat, _in_place, _input, _int32,
-                     _on, _output, _rows)
+from .window import (IO_TYPES, STA_TYPE_E4M3, STA_TYPE_INT8, _at, _current_stream, _flat, _input, _int32, _new, _on,
+                     _output, _rows, _statistics)
 
 STA_READ_ZERO = 0x2
 CACHE_TYPES = {torch.float8_e4m3fn: STA_TYPE_E4M3, torch.int8: STA_TYPE_INT8}
@@ -146,14 +146,13 @@ class KVCache:
             if lengths is None:
                 raise ValueError("lengths: expected int32 [batch]")
             if o is None:
-                o = torch.empty_like(q)
-                if not _in_place(o):
-                    o = torch.empty_like(q, memory_format=torch.contiguous_format)
+                o = _new(q)
             else:
                 _output(o, "o", shape, q.dtype, self.device)
             if lse is None and want_lse:
-                lse = torch.empty(shape[:3], dtype=torch.float32, device=self.device)
-            _flat(lse, "lse", shape[:3], torch.float32, self.device)
+                lse = _statistics(shape[:3], self.device)
+            else:
+                _flat(lse, "lse", shape[:3], torch.float32, self.device)
             if batch and nq:
                 st = lib().sta_cache_attention(ctypes.byref(self._c), batch, heads, nq,
                                                _int32(window, "window"), _int32(sinks, "sinks"),

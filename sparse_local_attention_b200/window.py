@@ -130,6 +130,19 @@ def _new(like: torch.Tensor) -> torch.Tensor:
     return t if _in_place(t) else torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
+def _statistics(shape, device) -> torch.Tensor:
+    """An fp32 tensor of [batch, heads, rows]."""
+    _, h, n = shape
+    return torch.empty_strided(shape, (h * n, n, 1), dtype=torch.float32, device=device)
+
+
+@functools.lru_cache(maxsize=64)
+def _status(device) -> torch.Tensor:
+    """The workspace of forward calls whose status nobody reads: its only word is
+    written where a wait of the kernels runs out, which `check` reports."""
+    return torch.empty(256, dtype=torch.uint8, device=device)
+
+
 @functools.lru_cache(maxsize=256)
 def _sized(batch, heads, kv_heads, head_dim, q_len, kv_len, q_rows, kv_rows, window, sinks, dtype, scale):
     """(problem, forward bytes, backward bytes) of one problem."""
@@ -153,13 +166,13 @@ class _Call:
             raise ValueError(f"q: expected bfloat16 or float16, got {q.dtype}")
         if (cu_q is None) != (cu_kv is None):
             raise ValueError("cu_q and cu_kv go together")
-        self.dtype, self.device = q.dtype, q.device
-        self.q_shape, self.kv_shape = tuple(q.shape), (q.shape[0], k.shape[1], k.shape[2], q.shape[3])
-        self.q = _input(q, "q", self.q_shape, q.dtype, q.device)
-        self.k = _input(k, "k", self.kv_shape, q.dtype, q.device)
-        self.v = _input(v, "v", self.kv_shape, q.dtype, q.device)
-        batch, heads, nq, d = self.q_shape
-        kv_heads, nk = self.kv_shape[1:3]
+        self.dtype, self.device = dtype, device = q.dtype, q.device
+        self.q_shape = batch, heads, nq, d = tuple(q.shape)
+        _, kv_heads, nk, _ = k.shape
+        self.kv_shape = batch, kv_heads, nk, d
+        self.q = _input(q, "q", self.q_shape, dtype, device)
+        self.k = _input(k, "k", self.kv_shape, dtype, device)
+        self.v = _input(v, "v", self.kv_shape, dtype, device)
         self.packed = cu_q is not None
         self.cu_q, self.cu_kv = cu_q, cu_kv
         window, sinks = _int32(window, "window"), _int32(sinks, "sinks")
@@ -184,7 +197,7 @@ class _Call:
             self.no_keys = False
         if not self.empty:
             self.problem, self.fwd_bytes, self.bwd_bytes = _sized(
-                batch, heads, kv_heads, d, nq, nk, *rows, window, sinks, IO_TYPES[q.dtype], float(scale))
+                batch, heads, kv_heads, d, nq, nk, *rows, window, sinks, IO_TYPES[dtype], float(scale))
 
 
 def _forward(c: _Call, o=None, lse=None, workspace=None, check=False, want_lse=True):
@@ -195,9 +208,10 @@ def _forward(c: _Call, o=None, lse=None, workspace=None, check=False, want_lse=T
     else:
         _output(o, "o", c.q_shape, c.dtype, c.device)
     if lse is None and want_lse:
-        lse = torch.empty(c.q_shape[:3], dtype=torch.float32, device=c.device)
+        lse = _statistics(c.q_shape[:3], c.device)
         new.append((lse, float("-inf")))
-    _flat(lse, "lse", c.q_shape[:3], torch.float32, c.device)
+    else:
+        _flat(lse, "lse", c.q_shape[:3], torch.float32, c.device)
     flags = STA_CALL_CHECK if check else 0
     if c.packed:  # rows outside every sequence are not written
         if len(new) == 1 + (lse is not None) and not c.empty:
@@ -211,7 +225,8 @@ def _forward(c: _Call, o=None, lse=None, workspace=None, check=False, want_lse=T
             if lse is not None:
                 lse.fill_(float("-inf"))
             return o, lse
-        ws = _scratch(workspace, c.fwd_bytes, c.device)
+        ws = (_status(c.device) if workspace is None and not check and c.fwd_bytes <= 256 else
+              _scratch(workspace, c.fwd_bytes, c.device))
         st = lib().sta_window_forward(ctypes.byref(c.problem), _rows(c.q), _rows(c.k), _rows(c.v), _rows(o), _at(lse),
                                       _at(c.cu_q), _at(c.cu_kv), ws.data_ptr(), ws.nbytes,
                                       _current_stream(c.device), flags)
