@@ -169,35 +169,41 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheMove m) {
   const bool is_v = blockIdx.z & 1;
   const int b = blockIdx.z >> 1, h = blockIdx.y, part = threadIdx.x % kPer;
   const int start = __ldg(m.start + b), count = clamp_count(m, b);
-  const long long span = (long long)c.table_pages * c.page_size;
   const uint8_t *codes = is_v ? c.v : c.k;
   const float *scales = is_v ? c.v_scale : c.k_scale;
-  const int blocks = c.page_size / c.block;
+  const int blocks = c.page_size / c.block, shift = 31 - __clz(c.block);  // a power of two
+  // place of the first row's token in the table; the next row's is kPass further
+  const int row0 = blockIdx.x * kReadRows * kPass + threadIdx.x / kPer;
+  const long long first = start + (long long)row0;
+  int in_page = 0;
+  long long index = -1;
+  if (start >= 0 && first < (long long)c.table_pages * c.page_size) {
+    index = (int)first / c.page_size;
+    in_page = (int)first - (int)index * c.page_size;
+  }
   uint4 w[kReadRows];
   float s[kReadRows];
   bool there[kReadRows];
 #pragma unroll
   for (int i = 0; i < kReadRows; ++i) {
-    const int row = (blockIdx.x * kReadRows + i) * kPass + threadIdx.x / kPer;
-    int page = -1, pos = 0;
-    if (start >= 0 && row < count && start + (long long)row < span) {
-      pos = start + row;
-      page = page_of(c, b, pos);
-    }
-    there[i] = page >= 0;
+    int page = -1;
+    if (index >= 0 && index < c.table_pages && row0 + i * kPass < count)
+      page = __ldg(c.table + (long long)b * c.table_pages + index);
+    there[i] = (unsigned)page < (unsigned)c.pages;
     w[i] = make_uint4(0u, 0u, 0u, 0u), s[i] = 0.f;
     if (there[i]) {
-      const int in_page = pos % c.page_size;
       const long long ph = (long long)page * c.kv_heads + h;
       w[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (ph * c.page_size + in_page) * D + 16 * part));
-      s[i] = __ldg(scales + ph * blocks + in_page / c.block);
+      s[i] = __ldg(scales + ph * blocks + (in_page >> shift));
     }
+    in_page += kPass;
+    while (index >= 0 && in_page >= c.page_size) in_page -= c.page_size, ++index;
   }
   const Rows &x = is_v ? m.v : m.k;
   char *out = x.p + 2 * ((long long)b * x.b + (long long)h * x.h + 16 * part);
 #pragma unroll
   for (int i = 0; i < kReadRows; ++i) {
-    const int row = (blockIdx.x * kReadRows + i) * kPass + threadIdx.x / kPer;
+    const int row = row0 + i * kPass;
     if (row >= m.rows || !(there[i] || m.zero)) continue;
     const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
     uint32_t v[8];

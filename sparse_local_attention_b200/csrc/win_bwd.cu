@@ -106,6 +106,20 @@ __device__ __forceinline__ float ds_factor(const WinParams &p, float *smem_word)
 }
 
 // ----------------------------------------------------------------------- 1. preprocess
+// Sums of four rows' values over a group of kLanes lanes; lane `part` gets row
+// 2 (part & 1) + (part >> 1 & 1)'s.  The group's lanes share the rows after two
+// exchanges, so that what follows runs once for four rows.
+template <int kLanes>
+__device__ __forceinline__ float sum_rows(const float (&v)[4], int part) {
+  const bool up = part & 1, upper = part & 2;
+  const float a = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 1);
+  const float b = (up ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 1);
+  float x = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 2);
+#pragma unroll
+  for (int off = 4; off < kLanes; off *= 2) x += __shfl_xor_sync(0xffffffffu, x, off);
+  return x;
+}
+
 // A group of D / 8 lanes per row, a CTA per pre_rows(D) rows of a head: four
 // rows per lane group, all of them in flight at once.
 template <int D, class T>
@@ -123,66 +137,63 @@ __global__ void __launch_bounds__(256) window_pre_kernel(const WinParams p) {
     return;
   }
   const Sequence s = sequence(p, b);
-  float norm = 0.f;
   const long long aug0 = aug_row(p, s, b, h);
-  constexpr int kPass = 8 * kRows, kPasses = pre_rows(D) / kPass;
+  constexpr int kPass = 8 * kRows;
+  static_assert(pre_rows(D) == 4 * kPass, "four rows per lane group");
   const int row0 = blockIdx.x * pre_rows(D) + (threadIdx.x >> 5) * kRows + sub;
   const char *o_at = p.o.p + 2 * (s.slice * p.o.b + h * p.o.h + (long long)(s.q0 + row0) * p.o.r) + 16 * part;
-  const char *g_at = p.dout.p + 2 * (s.slice * p.dout.b + h * p.dout.h + (long long)(s.q0 + row0) * p.dout.r) + 16 * part;
-  const float *lse_at = p.lse + stat_row(p, s, h, row0);
-  uint4 a[kPasses], g[kPasses];
-  float lse[kPasses];
+  const char *g_at =
+      p.dout.p + 2 * (s.slice * p.dout.b + h * p.dout.h + (long long)(s.q0 + row0) * p.dout.r) + 16 * part;
+  // the row that this lane (and those that differ from it in the upper bits) finishes
+  const int row = row0 + (2 * (part & 1) + (part >> 1 & 1)) * kPass;
+  const bool valid = row < s.nq;
+  uint4 a[4], g[4];
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    a[i] = g[i] = make_uint4(0u, 0u, 0u, 0u), lse[i] = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    a[i] = g[i] = make_uint4(0u, 0u, 0u, 0u);
     if (row0 + i * kPass < s.nq) {
       a[i] = __ldg(reinterpret_cast<const uint4 *>(o_at + 2ll * i * kPass * p.o.r));
       g[i] = __ldg(reinterpret_cast<const uint4 *>(g_at + 2ll * i * kPass * p.dout.r));
-      if (part == 0) lse[i] = __ldg(lse_at + i * kPass);
     }
   }
+  const float lse = valid ? __ldg(p.lse + stat_row(p, s, h, row)) : 0.f;
+  float accs[4], sqs[4];
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int row = row0 + i * kPass;
-    float acc = 0.f, sq = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    accs[i] = 0.f, sqs[i] = 0.f;
     const uint32_t av[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, gv[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 af = Elem<T>::unpack(av[e]), gf = Elem<T>::unpack(gv[e]);
-      acc = fmaf(af.x, gf.x, fmaf(af.y, gf.y, acc));
-      sq = fmaf(gf.x, gf.x, fmaf(gf.y, gf.y, sq));
+      accs[i] = fmaf(af.x, gf.x, fmaf(af.y, gf.y, accs[i]));
+      sqs[i] = fmaf(gf.x, gf.x, fmaf(gf.y, gf.y, sqs[i]));
     }
-#pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) {
-      acc += __shfl_xor_sync(0xffffffffu, acc, off);
-      if (kIsHalf<T>) sq += __shfl_xor_sync(0xffffffffu, sq, off);
-    }
-    norm = fmaxf(norm, sqrtf(sq));
-    const bool valid = row < s.nq;
-    if (valid && part == 0) p.dd[stat_row(p, s, h, row)] = acc;
-    if (valid && part < 2) {
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-      if (part == 0) {
-        // a row that sees nothing has LSE = -inf; all its pairs are masked
-        w[0] = hi_lo<T>(lse[i] == -INFINITY ? 0.f : -lse[i] / p.scale * (1.f / kLseSel<T>));
-        if constexpr (kIsHalf<T>) {
-          const float big = fabsf(acc);
-          if (big > 1024.f) w[2] = hi_lo<T>(-acc * (1.f / kDSel));
-          else if (big < 1.f / 16) w[3] = hi_lo<T>(-acc * kDSel);
-          else w[1] = hi_lo<T>(-acc);
-        } else {
-          w[1] = hi_lo<T>(-acc);
-        }
+  }
+  const float acc = sum_rows<kLanes>(accs, part);
+  if (valid && part < 8) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (part < 4) {
+      p.dd[stat_row(p, s, h, row)] = acc;
+      // a row that sees nothing has LSE = -inf; all its pairs are masked
+      w[0] = hi_lo<T>(lse == -INFINITY ? 0.f : -lse / p.scale * (1.f / kLseSel<T>));
+      if constexpr (kIsHalf<T>) {
+        const float big = fabsf(acc);
+        if (big > 1024.f) w[2] = hi_lo<T>(-acc * (1.f / kDSel));
+        else if (big < 1.f / 16) w[3] = hi_lo<T>(-acc * kDSel);
+        else w[1] = hi_lo<T>(-acc);
+      } else {
+        w[1] = hi_lo<T>(-acc);
       }
-      const long long ar = aug0 + row;
-      *reinterpret_cast<uint4 *>(p.aug + ar / 8 * 256 + part * 128 + ar % 8 * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    const long long ar = aug0 + row;  // two halves of 16 bytes, the second one zero
+    *reinterpret_cast<uint4 *>(p.aug + ar / 8 * 256 + part / 4 * 128 + ar % 8 * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   if constexpr (kIsHalf<T>) {
     __shared__ int top;
     if (threadIdx.x == 0) top = 0;
     __syncthreads();
-    if (part == 0) atomicMax(&top, __float_as_int(norm));
+    const int most = __reduce_max_sync(0xffffffffu, __float_as_int(sqrtf(sum_rows<kLanes>(sqs, part))));
+    if (lane == 0) atomicMax(&top, most);  // nonnegative floats order like integers
     __syncthreads();
     if (threadIdx.x == 0) p.norms[((long long)b * p.heads + h) * gridDim.x + blockIdx.x] = __int_as_float(top);
   }
