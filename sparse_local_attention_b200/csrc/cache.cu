@@ -7,9 +7,10 @@
 //   become round(c * s_old * (1 / s)).
 // Bound by memory: 2 bytes read and 1 written per element, 1 read and 2 written
 // on the way back (prompts of 8 sequences up to 4096 tokens, 8 key heads, d 128:
-// written in 26.5 us and read in 28.8, 4.8 and 4.4 TB/s); a few rows are two
-// latencies of memory, 3.3 us.
+// written in 26.5 us and read in 25.8, 4.8 and 4.9 TB/s); a few rows are two
+// latencies of memory, 3.2 us.
 #include "seq_common.cuh"
+#include "sm100_ptx.cuh"
 
 namespace sta {
 namespace {
@@ -35,6 +36,9 @@ template <> struct Code<STA_TYPE_E4M3> {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(d), "f"(c));
     return uint32_t(x) | (uint32_t(y) << 16);
   }
+  static __device__ __forceinline__ void unpack4(uint32_t w, float2 &a, float2 &b) {
+    a = unpack(w & 0xffffu), b = unpack(w >> 16);
+  }
   static __device__ __forceinline__ float2 unpack(uint32_t w) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
@@ -54,11 +58,12 @@ template <> struct Code<STA_TYPE_INT8> {
     auto bits = [](float x) { return __float_as_uint(__fadd_rn(x, 12582912.f)); };  // not fused with the product before
     return __byte_perm(__byte_perm(bits(a), bits(b), 0x0040), __byte_perm(bits(c), bits(d), 0x0040), 0x5410);
   }
-  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+  static __device__ __forceinline__ void unpack4(uint32_t w, float2 &a, float2 &b) {
     // c ^ 0x80 in the low byte of 2^23 is 2^23 + 128 + c
-    w ^= 0x8080u;
-    return make_float2(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)) - 8388736.f,
-                       __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441)) - 8388736.f);
+    w ^= 0x80808080u;
+    const float2 off = make_float2(-8388736.f, -8388736.f);
+    auto at = [&](int s) { return __uint_as_float(__byte_perm(w, 0x4b000000u, s)); };
+    a = add2(make_float2(at(0x7440), at(0x7441)), off), b = add2(make_float2(at(0x7442), at(0x7443)), off);
   }
 };
 
@@ -152,70 +157,65 @@ __global__ void __launch_bounds__(128) cache_write_kernel(const CacheMove m) {
     // the block's earlier tokens at the new scale
     for (int i = threadIdx.x; i < lo * D / 4; i += 128) {
       uint32_t *w = reinterpret_cast<uint32_t *>(codes) + i;
-      const float2 a = Code<kType>::unpack(*w & 0xffffu), z = Code<kType>::unpack(*w >> 16);
+      float2 a, z;
+      Code<kType>::unpack4(*w, a, z);
       *w = Code<kType>::pack(a.x * old * inv, a.y * old * inv) | (Code<kType>::pack(z.x * old * inv, z.y * old * inv) << 16);
     }
   }
 }
 
-// A thread per 16 codes of two rows, whose loads are in flight together (prompts
-// of 8 sequences up to 4096: one row 34 us, two 29, four 28; a call of few rows
-// takes 3.3 us with one or two and 4.4 with four).
-constexpr int kReadRows = 2;
+// A warp per 16 tokens that begin at a multiple of 16: one page and one scale,
+// a run of 16 D codes, of which a lane takes 8 at a time so that a warp's stores
+// are whole lines (a lookup per row and lane, and stores of half sectors: 26.7 us
+// where this takes 25.8, prompts of 8 sequences up to 4096; 512 tokens of 16
+// sequences, d 64: 4.7 and 3.9).
+constexpr int kReadTokens = 16, kReadWarps = 4;
 template <int D, int kType, class T>
-__global__ void __launch_bounds__(256) cache_read_kernel(const CacheMove m) {
+__global__ void __launch_bounds__(32 * kReadWarps) cache_read_kernel(const CacheMove m) {
   const CacheParams &c = m.c;
-  constexpr int kPer = D / 16, kPass = 256 / kPer;
+  constexpr int kPer = D / 8, kRows = 32 / kPer, kLoads = kReadTokens / kRows;  // lanes per row, rows per load
   const bool is_v = blockIdx.z & 1;
-  const int b = blockIdx.z >> 1, h = blockIdx.y, part = threadIdx.x % kPer;
-  const int start = __ldg(m.start + b), count = clamp_count(m, b);
-  const uint8_t *codes = is_v ? c.v : c.k;
-  const float *scales = is_v ? c.v_scale : c.k_scale;
-  const int blocks = c.page_size / c.block, shift = 31 - __clz(c.block);  // a power of two
-  // place of the first row's token in the table; the next row's is kPass further
-  const int row0 = blockIdx.x * kReadRows * kPass + threadIdx.x / kPer;
-  const long long first = start + (long long)row0;
-  int in_page = 0;
-  long long index = -1;
+  const int b = blockIdx.z >> 1, h = blockIdx.y, lane = threadIdx.x & 31;
+  const int start = __ldg(m.start + b), count = clamp_count(m, b), base = max(start, 0);
+  const long long first = (base / kReadTokens + (long long)blockIdx.x * kReadWarps + (threadIdx.x >> 5)) * kReadTokens;
+  if (first - base >= m.rows) return;
+  const int row0 = (int)(first - base) + lane / kPer, col = lane % kPer * 8;  // row0: from -15 on
+  int page = -1, in_page = 0;
   if (start >= 0 && first < (long long)c.table_pages * c.page_size) {
-    index = (int)first / c.page_size;
-    in_page = (int)first - (int)index * c.page_size;
+    page = page_of(c, b, (int)first);
+    in_page = (int)first % c.page_size;
   }
-  uint4 w[kReadRows];
-  float s[kReadRows];
-  bool there[kReadRows];
+  const long long ph = (long long)page * c.kv_heads + h;
+  const uint8_t *codes = (is_v ? c.v : c.k) + (ph * c.page_size + in_page) * D + 8 * lane;
+  uint2 w[kLoads];
 #pragma unroll
-  for (int i = 0; i < kReadRows; ++i) {
-    int page = -1;
-    if (index >= 0 && index < c.table_pages && row0 + i * kPass < count)
-      page = __ldg(c.table + (long long)b * c.table_pages + index);
-    there[i] = (unsigned)page < (unsigned)c.pages;
-    w[i] = make_uint4(0u, 0u, 0u, 0u), s[i] = 0.f;
-    if (there[i]) {
-      const long long ph = (long long)page * c.kv_heads + h;
-      w[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (ph * c.page_size + in_page) * D + 16 * part));
-      s[i] = __ldg(scales + ph * blocks + (in_page >> shift));
-    }
-    in_page += kPass;
-    while (index >= 0 && in_page >= c.page_size) in_page -= c.page_size, ++index;
+  for (int i = 0; i < kLoads; ++i) {
+    const int row = row0 + kRows * i;
+    w[i] = make_uint2(0u, 0u);
+    if (page >= 0 && row >= 0 && row < count) w[i] = __ldg(reinterpret_cast<const uint2 *>(codes + 256 * i));
   }
+  float s = 0.f;
+  if (page >= 0) s = __ldg((is_v ? c.v_scale : c.k_scale) + ph * (c.page_size / c.block) + in_page / c.block);
   const Rows &x = is_v ? m.v : m.k;
-  char *out = x.p + 2 * ((long long)b * x.b + (long long)h * x.h + 16 * part);
+  char *out = x.p + 2 * ((long long)b * x.b + (long long)h * x.h + (long long)row0 * x.r + col);
+  const float2 s2 = make_float2(s, s);
 #pragma unroll
-  for (int i = 0; i < kReadRows; ++i) {
-    const int row = row0 + i * kPass;
-    if (row >= m.rows || !(there[i] || m.zero)) continue;
-    const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-    uint32_t v[8];
+  for (int i = 0; i < kLoads; ++i) {
+    const int row = row0 + kRows * i;
+    const bool there = page >= 0 && row < count;
+    if (row < 0 || row >= m.rows || !(there || m.zero)) continue;
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    if (there) {
+      const uint32_t in[2] = {w[i].x, w[i].y};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = Code<kType>::unpack(in[e] & 0xffffu), g = Code<kType>::unpack(in[e] >> 16);
-      v[2 * e] = Elem<T>::pack(f.x * s[i], f.y * s[i]);
-      v[2 * e + 1] = Elem<T>::pack(g.x * s[i], g.y * s[i]);
+      for (int e = 0; e < 2; ++e) {
+        float2 f, g;
+        Code<kType>::unpack4(in[e], f, g);
+        f = mul2(f, s2), g = mul2(g, s2);
+        v[2 * e] = Elem<T>::pack(f.x, f.y), v[2 * e + 1] = Elem<T>::pack(g.x, g.y);
+      }
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(out + 2ll * row * x.r);
-    dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    *reinterpret_cast<uint4 *>(out + 2ll * kRows * i * x.r) = make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 
@@ -233,9 +233,10 @@ cudaError_t write_launch(const CacheMove &m, cudaStream_t stream) {
 }
 template <int D, int kType, class T>
 cudaError_t read_launch(const CacheMove &m, cudaStream_t stream) {
-  constexpr int kRows = kReadRows * 256 / (D / 16);
-  const dim3 grid((m.rows + kRows - 1) / kRows, m.c.kv_heads, 2 * m.batch);
-  cache_read_kernel<D, kType, T><<<grid, 256, 0, stream>>>(m);
+  // a run of `rows` tokens that starts anywhere touches at most this many groups
+  const int groups = (m.rows + kReadTokens - 2) / kReadTokens + 1;
+  const dim3 grid((groups + kReadWarps - 1) / kReadWarps, m.c.kv_heads, 2 * m.batch);
+  cache_read_kernel<D, kType, T><<<grid, 32 * kReadWarps, 0, stream>>>(m);
   return cudaGetLastError();
 }
 
