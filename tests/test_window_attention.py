@@ -156,6 +156,24 @@ def test_packed_sequences(dtype, d, lens_q, lens_k, window, sinks, bounds):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,dtype,n", [(64, FP16, 150), (128, BF16, 100)])
+def test_packed_tokens_of_many_uneven_sequences(d, dtype, n):
+    """A token each of more sequences than the GPU holds at once, of uneven lengths."""
+    g = torch.Generator().manual_seed(n)
+    lens_k = torch.randint(0, 600, (n,), generator=g)
+    lens_k[3], lens_k[::4] = 600, 333
+    q, k, v, _, cu_q, cu_k = packed([1] * n, lens_k.tolist(), 8, 4, d, dtype, seed=n)
+    o, lse = window_forward(*(t.cuda() for t in (q, k, v)), 450, 5, cu_q=cu_q.cuda(), cu_kv=cu_k.cuda(), max_q=1, max_kv=600,
+                            check=True)
+    for b in range(n):
+        rk = slice(int(cu_k[b]), int(cu_k[b + 1]))
+        want = seq_ref.attention(q[0, :, b:b + 1], k[0, :, rk], v[0, :, rk], seq_ref.mask_of(1, int(lens_k[b]), 450, 5),
+                                 d ** -0.5, dtype=dtype)
+        seq_ref.check(o[0, :, b:b + 1], want["o"], f"o of sequence {b}")
+        seq_ref.check(lse[0, :, b:b + 1], want["lse"], f"lse of sequence {b}")
+
+
+@pytest.mark.gpu
 def test_packed_bounds_cut_and_bad_starts_are_dropped():
     """max_q below a length computes the sequence's first max_q rows against its
     first max_kv keys; starts outside the tensor are cut to it."""
