@@ -121,10 +121,15 @@ class KVCache:
             raise ValueError("page_table: expected int32 [batch, table_pages]")
         shape = (page_table.shape[0], self.kv_heads, int(rows), self.head_dim)
         with _on(self.device, stream):
-            flags = (STA_CALL_CHECK if check else 0) | (STA_READ_ZERO if k is None and v is None else 0)
-            new = torch.empty if flags & STA_READ_ZERO else torch.zeros
-            k, v = (new(shape, dtype=dtype, device=self.device) if t is None
-                    else _output(t, name, shape, dtype, self.device) for t, name in ((k, "k"), (v, "v")))
+            flags = STA_CALL_CHECK if check else 0
+            if k is None and v is None:
+                flags |= STA_READ_ZERO
+                _, h, n, d = shape
+                k, v = (torch.empty_strided(shape, (h * n * d, n * d, d, 1), dtype=dtype, device=self.device)
+                        for _ in range(2))
+            else:
+                k, v = (torch.zeros(shape, dtype=dtype, device=self.device) if t is None
+                        else _output(t, name, shape, dtype, self.device) for t, name in ((k, "k"), (v, "v")))
             self._move("sta_cache_read", k, v, page_table, start, count, flags)
         return k, v
 

@@ -391,3 +391,12 @@ def test_many_sequences_of_uneven_lengths(batch):
     lens[1::3], lens[7] = 500, 640
     p, table = filled(batch, lens.tolist(), 4, 64, 64, 64, INT8, seed=batch)
     attend_and_check(p, table, lens.tolist(), randn(batch, 8, 1, 64, seed=1, dtype=FP16), 0, 0)
+
+
+@pytest.mark.gpu
+def test_many_long_sequences_over_shared_pages():
+    """Long sequences of uneven lengths, each split over two blocks, that share their pages."""
+    p, one = filled(1, [4224], 2, 64, 64, 64, E4M3, seed=21)
+    lens = torch.randint(0, 4225, (80,), generator=torch.Generator().manual_seed(22))
+    lens[5], lens[6] = 4224, 0
+    attend_and_check(p, one.expand(80, -1).contiguous(), lens.tolist(), randn(80, 4, 1, 64, seed=23, dtype=BF16), 0, 3)
