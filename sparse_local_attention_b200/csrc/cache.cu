@@ -7,7 +7,7 @@
 //   become round(c * s_old * (1 / s)).
 // Bound by memory: 2 bytes read and 1 written per element, 1 read and 2 written
 // on the way back (prompts of 8 sequences up to 4096 tokens, 8 key heads, d 128:
-// written in 22.4 us and read in 25.7, 5.6 and 4.9 TB/s); a few rows are two
+// written in 22.4 us and read in 25.2, 5.6 and 5.0 TB/s); a few rows are two
 // latencies of memory, 3.2 us.
 #include "seq_common.cuh"
 #include "sm100_ptx.cuh"
@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(128) cache_write_kernel(const CacheMove m) {
 // A warp per 16 tokens that begin at a multiple of 16: one page and one scale,
 // a run of 16 D codes, of which a lane takes 8 at a time so that a warp's stores
 // are whole lines (a lookup per row and lane, and stores of half sectors: 26.7 us
-// where this takes 25.8, prompts of 8 sequences up to 4096; 512 tokens of 16
-// sequences, d 64: 4.7 and 3.9).
+// where this takes 25.2, prompts of 8 sequences up to 4096; 512 tokens of 16
+// sequences, d 64: 4.7 and 3.7).
 constexpr int kReadTokens = 16, kReadWarps = 4;
 template <int D, int kType, class T>
 __global__ void __launch_bounds__(32 * kReadWarps) cache_read_kernel(const CacheMove m) {
@@ -204,24 +204,25 @@ __global__ void __launch_bounds__(32 * kReadWarps) cache_read_kernel(const Cache
   if (page >= 0) s = __ldg((is_v ? c.v_scale : c.k_scale) + ph * (c.page_size / c.block) + in_page / c.block);
   const Rows &x = is_v ? m.v : m.k;
   char *out = x.p + 2 * ((long long)b * x.b + (long long)h * x.h + (long long)row0 * x.r + col);
+  const long long out_step = 2 * kRows * x.r;
   const float2 s2 = make_float2(s, s);
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int row = row0 + kRows * i;
     const bool there = page >= 0 && row < count;
-    if (row < 0 || row >= m.rows || !(there || m.zero)) continue;
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
-    if (there) {
-      const uint32_t in[2] = {w[i].x, w[i].y};
+    const float2 by = there ? s2 : make_float2(0.f, 0.f);  // whatever the scale of a block without tokens
+    uint32_t v[4];
+    const uint32_t in[2] = {w[i].x, w[i].y};
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float2 f, g;
-        Code<kType>::unpack4(in[e], f, g);
-        f = mul2(f, s2), g = mul2(g, s2);
-        v[2 * e] = Elem<T>::pack(f.x, f.y), v[2 * e + 1] = Elem<T>::pack(g.x, g.y);
-      }
+    for (int e = 0; e < 2; ++e) {
+      float2 f, g;
+      Code<kType>::unpack4(in[e], f, g);
+      f = mul2(f, by), g = mul2(g, by);
+      v[2 * e] = Elem<T>::pack(f.x, f.y), v[2 * e + 1] = Elem<T>::pack(g.x, g.y);
     }
-    *reinterpret_cast<uint4 *>(out + 2ll * kRows * i * x.r) = make_uint4(v[0], v[1], v[2], v[3]);
+    if (row >= 0 && row < m.rows && (there || m.zero))
+      *reinterpret_cast<uint4 *>(out) = make_uint4(v[0], v[1], v[2], v[3]);
+    out += out_step;
   }
 }
 

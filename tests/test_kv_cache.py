@@ -400,3 +400,19 @@ def test_many_long_sequences_over_shared_pages():
     lens = torch.randint(0, 4225, (80,), generator=torch.Generator().manual_seed(22))
     lens[5], lens[6] = 4224, 0
     attend_and_check(p, one.expand(80, -1).contiguous(), lens.tolist(), randn(80, 4, 1, 64, seed=23, dtype=BF16), 0, 3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [E4M3, INT8], ids=["e4m3", "int8"])
+def test_rows_behind_the_count_are_zeros_whatever_the_page_holds(fmt):
+    p, table = filled(2, [40, 64], 2, 64, 64, 16, fmt, seed=31)
+    want = p.cache.read(table.cuda(), ints(0, 3).cuda(), ints(33, 20).cuda(), 60)
+    for t in (p.cache.k, p.cache.v):
+        t.view(torch.uint8)[int(table[0, 0]), :, 33:] = 0x7F
+        t.view(torch.uint8)[int(table[1, 0]), :, 23:] = 0x7F
+    for t in (p.cache.k_scale, p.cache.v_scale):
+        t[int(table[0, 0]), :, 3] = float("nan")
+        t[int(table[1, 0]), :, 2:] = float("inf")
+    got = p.cache.read(table.cuda(), ints(0, 3).cuda(), ints(33, 20).cuda(), 60, check=True)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b) and not b[0, :, 33:].any() and not b[1, :, 20:].any() and b[0, :, :33].any()
