@@ -487,15 +487,19 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
       bool grows = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float f[2] = {fac[nt][0] * ks, fac[nt][1] * ks};
+        const float2 f = mul2(make_float2(fac[nt][0], fac[nt][1]), make_float2(ks, ks));
+        const float2 most = add2(make_float2(m[nt][0], m[nt][1]), make_float2(kHead + 8.f, kHead + 8.f));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[nt][e] *= f[e & 1];
+        for (int e = 0; e < 4; e += 2) {
+          const float2 y = mul2(make_float2(x[nt][e], x[nt][e + 1]), f);
+          x[nt][e] = y.x, x[nt][e + 1] = y.y;
           if (!whole) {
-            const int key = k0 + g + 8 * (e >> 1);
-            if (key >= keys.nk || !visible(pos[nt][e & 1], key, shape.window, shape.sinks)) x[nt][e] = -INFINITY;
+            const int key = k0 + g + 4 * e;
+#pragma unroll
+            for (int c2 = 0; c2 < 2; ++c2)
+              if (key >= keys.nk || !visible(pos[nt][c2], key, shape.window, shape.sinks)) x[nt][e + c2] = -INFINITY;
           }
-          grows = grows || x[nt][e] > m[nt][e & 1] + (kHead + 8.f);
+          grows = grows || x[nt][e] > most.x || x[nt][e + 1] > most.y;
         }
       }
       if (__any_sync(0xffffffffu, grows)) {
@@ -536,10 +540,13 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[nt][e] = ex2_approx(x[nt][e] - m[nt][e & 1]);
-          l[nt][e & 1] += x[nt][e];
-          if constexpr (Keys::kScaled) x[nt][e] *= pv;
+        for (int e = 0; e < 4; e += 2) {
+          float2 y = add2(make_float2(x[nt][e], x[nt][e + 1]), make_float2(-m[nt][0], -m[nt][1]));
+          y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+          const float2 sum = add2(make_float2(l[nt][0], l[nt][1]), y);
+          l[nt][0] = sum.x, l[nt][1] = sum.y;
+          if constexpr (Keys::kScaled) y = mul2(y, make_float2(pv, pv));
+          x[nt][e] = y.x, x[nt][e + 1] = y.y;
         }
         pb[nt][0] = transpose8(Elem<Op>::pack(x[nt][0], x[nt][1]));
         pb[nt][1] = transpose8(Elem<Op>::pack(x[nt][2], x[nt][3]));
