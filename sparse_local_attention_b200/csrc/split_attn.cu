@@ -139,38 +139,37 @@ struct CacheKeys {
   __device__ __forceinline__ float *lse_at(int h, int i) const {
     return a.lse ? a.lse + ((long long)b * a.heads + h) * a.q_len + i : nullptr;
   }
-  // Where a step's keys lie: the page (-1: absent), looked up a step before the
-  // loads that need it, its place in the table, and the steps before it in the page.
+  // Where a step's keys lie, looked up a step before the loads that need it: from
+  // the first key of the page on (-1: absent) and of its scales, its place in the
+  // table, and the steps before it in the page.
   struct Place {
-    int page, index, in_page;
+    long long row, scale;
+    int index, in_page;
   };
   __device__ __forceinline__ void look_up(Place &p) const {
     const int page = __ldg(a.c.table + (long long)b * a.c.table_pages + p.index);
-    p.page = (unsigned)page < (unsigned)a.c.pages ? page : -1;
+    const long long ph = (long long)page * a.c.kv_heads + hk;
+    p.row = (unsigned)page < (unsigned)a.c.pages ? ph * a.c.page_size * D : -1;
+    p.scale = ph * a.blocks;
   }
   __device__ __forceinline__ Place place(int step) const {
     const int per = a.c.page_size / kStep;
-    Place p{-1, step / per, step % per};
+    Place p{-1, 0, step / per, step % per};
     look_up(p);
     return p;
   }
-  __device__ __forceinline__ void advance(Place &p, int steps) const {
-    const int per = a.c.page_size / kStep;
-    p.in_page += steps;
-    if (p.in_page < per) return;  // still the same page
-    do {
-      p.in_page -= per;
-      ++p.index;
-    } while (p.in_page >= per);
+  __device__ __forceinline__ void advance(Place &p) const {
+    if (++p.in_page < a.c.page_size / kStep) return;
+    p.in_page = 0;
+    ++p.index;
     look_up(p);
   }
   static __device__ __forceinline__ constexpr int k_pitch() { return D; }
   static __device__ __forceinline__ constexpr int v_pitch() { return D; }
-  __device__ __forceinline__ bool there(const Place &p) const { return p.page >= 0; }
+  __device__ __forceinline__ bool there(const Place &p) const { return p.row >= 0; }
   __device__ __forceinline__ Source source(const Place &p, int) const {
-    const long long ph = (long long)p.page * a.c.kv_heads + hk;
     const int at = p.in_page * kStep;
-    const long long row = (ph * a.c.page_size + at) * D, sc = ph * a.blocks + (at >> a.block_shift);
+    const long long row = p.row + at * D, sc = p.scale + (at >> a.block_shift);
     return Source{reinterpret_cast<const char *>(a.c.k + row), reinterpret_cast<const char *>(a.c.v + row),
                   a.c.k_scale + sc, a.c.v_scale + sc};
   }
@@ -217,7 +216,7 @@ struct RowKeys {
   __device__ __forceinline__ float *lse_at(int h, int i) const { return p.lse ? p.lse + stat_row(p, s, h, i) : nullptr; }
   struct Place {};
   __device__ __forceinline__ Place place(int) const { return Place{}; }
-  __device__ __forceinline__ void advance(Place &, int) const {}
+  __device__ __forceinline__ void advance(Place &) const {}
   __device__ __forceinline__ bool there(const Place &) const { return true; }
   __device__ __forceinline__ Source source(const Place &, int step) const {
     const long long row = s.k0 + step * kStep;
@@ -331,8 +330,9 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
     sink_steps = min((min(shape.sinks, lo) + kStep - 1) / kStep, base_step);
     n_steps = sink_steps + (seen.end - 1) / kStep - base_step + 1;
   }
-  const int begin = (int)((long long)n_steps * rank / shape.splits);
-  const int end = (int)((long long)n_steps * (rank + 1) / shape.splits);
+  // a warp's steps, one behind another
+  const int parts = shape.splits * kWarps, part = rank * kWarps + warp;
+  const int begin = (int)((long long)n_steps * part / parts), end = (int)((long long)n_steps * (part + 1) / parts);
   const int skipped = base_step - sink_steps;  // steps between the sinks and the window
   auto step_of = [&](int i) { return i < sink_steps ? i : i + skipped; };
 
@@ -383,19 +383,19 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
       } else {
         here_bits &= ~(1u << stage);
       }
-      if (i + kWarps < end) {
-        if (i < sink_steps && i + kWarps >= sink_steps) next = keys.place(i + kWarps + skipped);
-        else keys.advance(next, kWarps);
+      if (i + 1 < end) {
+        if (i + 1 == sink_steps) next = keys.place(sink_steps + skipped);
+        else keys.advance(next);
       }
     }
     copies_commit();
   };
-  int i = begin + warp, ahead = i, stage = 0, into = 0;
+  int i = begin, ahead = i, stage = 0, into = 0;
   if (i < end) next = keys.place(step_of(i));
 #pragma unroll
   for (int a = 0; a < kAhead; ++a) {
     fetch(ahead, into++);
-    ahead += kWarps;
+    ++ahead;
   }
   // Q as the B operand: lane (g, c) holds row g, columns k_col(s, c) .. + 3
   uint32_t qf[NT][D / 16][2];
@@ -444,10 +444,10 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
     }
   }
 
-  for (; i < end; i += kWarps) {
+  for (; i < end; ++i) {
     const int step = step_of(i);
     fetch(ahead, into);  // into the stage read last
-    ahead += kWarps;
+    ++ahead;
     into = into + 1 == C::kStages ? 0 : into + 1;
     copies_wait<kAhead>();
     __syncwarp();
