@@ -18,10 +18,10 @@
 // which the matrix instructions take.
 //
 // With one row per sequence the bound is reading the keys: 64 sequences up to
-// 8192 tokens, 8 key heads, d 128, e4m3: 129 us for 0.70 GB, 5.5 TB/s (83% of a
-// copy's rate).  With 16 rows and d 64 it is the instructions of a step, 480 per
-// warp, most of them the widening of the codes and the softmax (32 sequences x 4
-// tokens, 16 heads over 4, window 4096, int8: 32 us for 68 MB).  Small calls are
+// 8192 tokens, 8 key heads, d 128, e4m3: 117 us for 0.70 GB, 6.0 TB/s (91% of a
+// copy's rate).  With 16 rows and d 64 it is the instructions of a step, some 300
+// per warp, most of them the widening of the codes and the softmax (32 sequences x
+// 4 tokens, 16 heads over 4, window 4096, int8: 30 us for 68 MB).  Small calls are
 // latency: 8 us for one token of one sequence over 1031.
 #include <cooperative_groups.h>
 

@@ -31,7 +31,7 @@
 // hide each other's: about 3900 cycles at head dim 128 (the products alone take
 // 2100), and 1.5 pairs more for an item's start and end.  8192 tokens, 24 heads,
 // d 128: without a window 410 us (1.0 PFLOP/s, 60% of a library product's rate),
-// window 2048 221 us (0.81); window 512, d 64, 2 x 4096 tokens, 16 heads: 61 us.
+// window 2048 222 us (0.81); window 512, d 64, 2 x 4096 tokens, 16 heads: 60 us.
 #include "seq_tile.cuh"
 
 namespace sta {
