@@ -416,3 +416,28 @@ def test_rows_behind_the_count_are_zeros_whatever_the_page_holds(fmt):
     got = p.cache.read(table.cuda(), ints(0, 3).cuda(), ints(33, 20).cuda(), 60, check=True)
     for a, b in zip(want, got):
         assert torch.equal(a, b) and not b[0, :, 33:].any() and not b[1, :, 20:].any() and b[0, :, :33].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [E4M3, INT8], ids=["e4m3", "int8"])
+def test_offsets_past_32_bits(fmt):
+    """The last pages of a cache of more than 4 GB hold and give what those of a small one do."""
+    pages, kv_heads, page, d = 33000, 8, 128, 128
+    codes = torch.empty(pages, kv_heads, page, d, dtype=torch.uint8, device="cuda").view(fmt)
+    scales = [torch.zeros(pages, kv_heads, page // 16, device="cuda") for _ in range(2)]
+    assert codes.numel() > 2 ** 32
+    large = KVCache.from_tensors(codes, torch.empty_like(codes), *scales)
+    small = KVCache(3, kv_heads, page, d, block=16, dtype=fmt)
+    k, v, q = (randn(1, h, n, d, seed=41 + i, dtype=BF16).cuda() for i, (h, n) in enumerate(((8, 300), (8, 300), (16, 2))))
+    results = []
+    for cache, first in ((small, 0), (large, pages - 3)):
+        table = (torch.arange(3, dtype=torch.int32)[None] + first).cuda()
+        cache.write(k, v, table, ints(0).cuda(), check=True)
+        cache.write(k[:, :, :1] * 3, v[:, :, :1] * 3, table, ints(300).cuda(), check=True)
+        results.append([*cache.read(table, ints(0).cuda(), None, 301, BF16, check=True),
+                        *cache.attention(q, table, ints(301).cuda(), 200, 4, check=True),
+                        cache.k[first:first + 3].view(torch.uint8), cache.k_scale[first:first + 3]])
+    (*same, small_k, _), (*other, large_k, _) = results
+    for a, b in zip(same, other):
+        assert torch.equal(a, b)
+    assert torch.equal(small_k[:2], large_k[:2]) and torch.equal(results[0][-1], results[1][-1])

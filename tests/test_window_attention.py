@@ -321,6 +321,29 @@ def test_strides_orders_and_broadcasts(nq, nk):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("nq", [1, 300])
+def test_offsets_past_32_bits(nq):
+    """Sequences 2^31 elements apart give what contiguous ones give."""
+    big = torch.empty(2 ** 31 + 2 ** 22, dtype=BF16, device="cuda")
+
+    def far(t, slot):
+        v = big.as_strided(t.shape, (2 ** 31, *t.stride()[1:]), slot * 2 ** 18)
+        return v.copy_(t)
+
+    near = [t.cuda() for t in make(4, 2, nq, 300, 64, BF16, batch=2, seed=nq)]
+    o, lse = window_forward(*near[:3], 70, 5, check=True)
+    grads = window_backward(*near[:3], o, lse, near[3], 70, 5, check=True)
+    q, k, v, do = (far(t, i) for i, t in enumerate(near))
+    o2 = far(torch.zeros_like(o), 4)
+    _, lse2 = window_forward(q, k, v, 70, 5, o=o2, check=True)
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    dq, dk, dv = (far(torch.zeros_like(t), 5 + i) for i, t in enumerate(grads))
+    window_backward(q, k, v, o2, lse2, do, 70, 5, dq=dq, dk=dk, dv=dv, check=True)
+    for a, b in zip(grads, (dq, dk, dv)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
 def test_autograd_matches_the_calls_and_is_deterministic():
     q, k, v, do = (t.cuda() for t in make(6, 2, 500, 500, 128, BF16, batch=2, seed=4))
     o, lse = window_forward(q, k, v, 128, 4)
