@@ -7,7 +7,7 @@
 //   become round(c * s_old * (1 / s)).
 // Bound by memory: 2 bytes read and 1 written per element, 1 read and 2 written
 // on the way back (prompts of 8 sequences up to 4096 tokens, 8 key heads, d 128:
-// written in 22.4 us and read in 25.2, 5.6 and 5.0 TB/s); a few rows are two
+// written in 22.4 us and read in 24.7, 5.6 and 5.1 TB/s); a few rows are two
 // latencies of memory, 3.2 us.
 #include "seq_common.cuh"
 #include "sm100_ptx.cuh"
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(128) cache_write_kernel(const CacheMove m) {
 // A warp per 16 tokens that begin at a multiple of 16: one page and one scale,
 // a run of 16 D codes, of which a lane takes 8 at a time so that a warp's stores
 // are whole lines (a lookup per row and lane, and stores of half sectors: 26.7 us
-// where this takes 25.2, prompts of 8 sequences up to 4096; 512 tokens of 16
+// where this takes 24.7, prompts of 8 sequences up to 4096; 512 tokens of 16
 // sequences, d 64: 4.7 and 3.7).
 constexpr int kReadTokens = 16, kReadWarps = 4;
 template <int D, int kType, class T>
@@ -184,12 +184,24 @@ __global__ void __launch_bounds__(32 * kReadWarps) cache_read_kernel(const Cache
   const int b = blockIdx.z >> 1, h = blockIdx.y, lane = threadIdx.x & 31;
   const int start = __ldg(m.start + b), count = clamp_count(m, b), base = max(start, 0);
   const long long first = (base / kReadTokens + (long long)blockIdx.x * kReadWarps + (threadIdx.x >> 5)) * kReadTokens;
-  if (first - base >= m.rows) return;
+  const bool none = first - base >= count;  // rows that get no token
+  if (first - base >= m.rows || (none && !m.zero)) return;
   const int row0 = (int)(first - base) + lane / kPer, col = lane % kPer * 8;  // row0: from -15 on
   int page = -1, in_page = 0;
+  const Rows &x = is_v ? m.v : m.k;
+  char *out = x.p + 2 * ((long long)b * x.b + (long long)h * x.h + (long long)row0 * x.r + col);
+  const long long out_step = 2 * kRows * x.r;
+  if (none) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i, out += out_step)
+      if (row0 + kRows * i < m.rows) *reinterpret_cast<uint4 *>(out) = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
   if (start >= 0 && first < (long long)c.table_pages * c.page_size) {
-    page = page_of(c, b, (int)first);
-    in_page = (int)first % c.page_size;
+    const int index = (int)first / c.page_size;
+    page = __ldg(c.table + (long long)b * c.table_pages + index);
+    if ((unsigned)page >= (unsigned)c.pages) page = -1;
+    in_page = (int)first - index * c.page_size;
   }
   const long long ph = (long long)page * c.kv_heads + h;
   const uint8_t *codes = (is_v ? c.v : c.k) + (ph * c.page_size + in_page) * D + 8 * lane;
@@ -202,9 +214,6 @@ __global__ void __launch_bounds__(32 * kReadWarps) cache_read_kernel(const Cache
   }
   float s = 0.f;
   if (page >= 0) s = __ldg((is_v ? c.v_scale : c.k_scale) + ph * (c.page_size / c.block) + in_page / c.block);
-  const Rows &x = is_v ? m.v : m.k;
-  char *out = x.p + 2 * ((long long)b * x.b + (long long)h * x.h + (long long)row0 * x.r + col);
-  const long long out_step = 2 * kRows * x.r;
   const float2 s2 = make_float2(s, s);
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
