@@ -119,10 +119,12 @@ struct ItemRing {
         : "memory");
     return some ? (int)x : -1;
   }
-  // the item after the n-th, or -1: there is none left
-  __device__ __forceinline__ bool take(uint32_t n, int &item, const WaitCtl &ctl, int code) {
+  // the item after the n-th, or -1: there is none left; n counts on only once
+  // the answer is there (discard waits for the one that is not)
+  __device__ __forceinline__ bool take(uint32_t &n, int &item, const WaitCtl &ctl, int code) {
     if (!mbar_wait(answered, n & 1, ctl, code)) return false;
     item = read();
+    ++n;
     return true;
   }
   // After an abort in the n-th item (`asked`: its successor has been asked for):

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
         ring.ask();
         asked = true;
         if (it.c0 == it.c1) {
-          if (!ring.take(n++, item, ctl, kErrBwdWait)) { ok = false; break; }
+          if (!ring.take(n, item, ctl, kErrBwdWait)) { ok = false; break; }
           asked = false;
           continue;
         }
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
           ++do_bits;
           ++ld;
         }
-        if (!ok || !ring.take(n++, item, ctl, kErrBwdWait)) { ok = false; break; }
+        if (!ok || !ring.take(n, item, ctl, kErrBwdWait)) { ok = false; break; }
         asked = false;
       }
       if (!ok) {
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
         ring.ask();
         asked = true;
         if (it.nc == 0) {
-          if (!ring.take(n++, item, ctl, kErrBwdWait)) { ok = false; break; }
+          if (!ring.take(n, item, ctl, kErrBwdWait)) { ok = false; break; }
           asked = false;
           continue;
         }
@@ -835,7 +835,7 @@ __global__ void __launch_bounds__(DqCfg<D>::R::kThreads, 1)
           load_tile<D>(slots + slot * C::kTile, (s & 1) ? &tmap_v : &tmap_k, it.s.k0 + first, it.h / p.group, it.s.slice, bar);
           ++ld;
         }
-        if (!ok || !ring.take(n++, item, ctl, kErrBwdWait)) { ok = false; break; }
+        if (!ok || !ring.take(n, item, ctl, kErrBwdWait)) { ok = false; break; }
         asked = false;
       }
       if (!ok) {

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ring.ask();
         asked = true;
         if (it.nc == 0) {
-          if (!ring.take(n++, item, ctl, kErrWaitProducer)) { ok = false; break; }
+          if (!ring.take(n, item, ctl, kErrWaitProducer)) { ok = false; break; }
           asked = false;
           continue;
         }
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++ld;
           return true;
         });
-        if (!ok || !ring.take(n++, item, ctl, kErrWaitProducer)) { ok = false; break; }
+        if (!ok || !ring.take(n, item, ctl, kErrWaitProducer)) { ok = false; break; }
         asked = false;
       }
       if (!ok) {

@@ -543,3 +543,30 @@ def test_wait_timeout_is_reported_and_recoverable():
         assert torch.equal(a, b)
 
 
+def calls_under_limits(call, limit, repeats=20):
+    """`call` returns tensors: under the limit its status, or the same bits as without one."""
+    good = call()
+    try:
+        sta.sta_set_wait_limit_ns(limit)
+        for _ in range(repeats):
+            try:
+                got = call()
+            except sta.StaError as e:
+                assert e.status == 8
+            else:
+                assert all(torch.equal(a, b) for a, b in zip(got, good))
+    finally:
+        sta.sta_set_wait_limit_ns(2_000_000_000)
+    assert all(torch.equal(a, b) for a, b in zip(call(), good))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("limit", [0, 300, 1000, 3000, 10000])
+def test_waits_that_run_out_anywhere_leave_no_item_behind(limit, d):
+    """Limits that end waits early, in the middle or not at all, with more items
+    than the GPU holds, so that items have been asked for when a wait runs out."""
+    q, k, v, do = (t.cuda() for t in make(16, 8, 2000, 2000, d, BF16))
+    calls_under_limits(lambda: window_forward(q, k, v, 300, 4, check=True), limit)
+    o, lse = window_forward(q, k, v, 300, 4, check=True)
+    calls_under_limits(lambda: window_backward(q, k, v, o, lse, do, 300, 4, check=True), limit)
