@@ -406,6 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (uint32_t n = 0;; ++n) {
       const Item *at = ring.get(n, ok, ctl, kErrWaitSoftmax);
+      // The warpgroups of a split item meet at its end, at barriers without a
+      // limit: they begin it together or not at all (a wait of one warp may run
+      // out before the item is there, and another one's find it).
+      if (kSplit && !named_bar_and(1, 256, at != nullptr)) break;
       if (!at) break;
       const Item &it = *at;  // stays in shared memory: beside a row of scores registers are short
       const int u = kSplit ? 0 : x;  // its unit

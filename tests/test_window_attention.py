@@ -570,3 +570,12 @@ def test_waits_that_run_out_anywhere_leave_no_item_behind(limit, d):
     calls_under_limits(lambda: window_forward(q, k, v, 300, 4, check=True), limit)
     o, lse = window_forward(q, k, v, 300, 4, check=True)
     calls_under_limits(lambda: window_backward(q, k, v, o, lse, do, 300, 4, check=True), limit)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("limit", [0, 200, 1000, 3000, 10000])
+def test_waits_that_run_out_anywhere_end_the_call(limit, d):
+    """12 blocks take the form whose warpgroups share a block's keys and meet at its end."""
+    q, k, v, _ = (t.cuda() for t in make(2, 2, 700, 700, d, BF16))
+    calls_under_limits(lambda: window_forward(q, k, v, 300, 4, check=True), limit)
