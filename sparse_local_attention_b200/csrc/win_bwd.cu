@@ -68,9 +68,19 @@ __device__ __forceinline__ uint32_t hi_lo(float x) {
   return Elem<T>::pack(x, x - Elem<T>::unpack(h).x);
 }
 
-// The panel row of one query: elements 0, 1 carry -LSE / scale (times 1 / kLseSel),
-// 2, 3 carry -D; fp16 also 4, 5 (large D) and 6, 7 (small D), against selectors
-// that undo the factors.
+// x as three bf16 numbers, lo in bits 0..15 of r[0]: 24 bits, as many as x has
+// (two leave 2^-18 of x, 4% of P at a log-sum-exp of 10 000).
+__device__ __forceinline__ void three_parts(float x, uint32_t (&r)[2]) {
+  using E = Elem<__nv_bfloat16>;
+  x = fabsf(x) > E::kMax ? copysignf(E::kMax, x) : x;  // does not round to infinity
+  const float rest = x - E::unpack(E::pack(x, 0.f)).x;
+  r[0] = E::pack(x, rest);
+  r[1] = E::pack(rest - E::unpack(r[0]).y, 0.f);
+}
+
+// The panel row of one query.  bf16: elements 0 -- 2 carry -LSE / scale, 3 -- 5
+// -D.  fp16: elements 0, 1 carry -LSE / scale (times 1 / kLseSel), 2, 3 carry -D,
+// 4, 5 large D and 6, 7 small D, against selectors that undo the factors.
 template <class T> constexpr float kLseSel = kIsHalf<T> ? 16.f : 1.f;
 constexpr float kDSel = 16384.f;
 
@@ -175,14 +185,18 @@ __global__ void __launch_bounds__(256) window_pre_kernel(const WinParams p) {
     if (part < 4) {
       p.dd[stat_row(p, s, h, row)] = acc;
       // a row that sees nothing has LSE = -inf; all its pairs are masked
-      w[0] = hi_lo<T>(lse == -INFINITY ? 0.f : -lse / p.scale * (1.f / kLseSel<T>));
+      const float l = lse == -INFINITY ? 0.f : -lse / p.scale;
       if constexpr (kIsHalf<T>) {
+        w[0] = hi_lo<T>(l * (1.f / kLseSel<T>));
         const float big = fabsf(acc);
         if (big > 1024.f) w[2] = hi_lo<T>(-acc * (1.f / kDSel));
         else if (big < 1.f / 16) w[3] = hi_lo<T>(-acc * kDSel);
         else w[1] = hi_lo<T>(-acc);
       } else {
-        w[1] = hi_lo<T>(-acc);
+        uint32_t a[2], d[2];
+        three_parts(l, a);
+        three_parts(-acc, d);
+        w[0] = a[0], w[1] = a[1] | d[0] << 16, w[2] = d[0] >> 16 | d[1] << 16;
       }
     }
     const long long ar = aug0 + row;  // two halves of 16 bytes, the second one zero
@@ -319,16 +333,19 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  // selector panels, every row alike: (l, l, 0, ...) picks -LSE / scale, (0, 0, 1,
-  // 1[, 2^14, 2^14, 2^-14, 2^-14]) picks -D
+  // selector panels, every row alike: bf16 (1, 1, 1, 0, ...) picks -LSE / scale, (0,
+  // 0, 0, 1, 1, 1) -D; fp16 (l, l, 0, ...), (0, 0, 1, 1, 2^14, 2^14, 2^-14, 2^-14)
   for (int c = threadIdx.x; c < (int)(C::kSel / 16); c += blockDim.x) {
     const bool first_half = ((c * 16) % 256) < 128, d_panel = c * 16 >= (int)kAugBytes;
     const uint32_t one = Elem<T>::pack(1.f, 1.f), l = Elem<T>::pack(kLseSel<T>, kLseSel<T>);
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (first_half && !d_panel) w.x = l;
+    if (first_half && !d_panel) {
+      w.x = l;
+      if (!kIsHalf<T>) w.y = one & 0xffffu;
+    }
     if (first_half && d_panel) {
-      w.y = one;
-      if (kIsHalf<T>) w.z = Elem<T>::pack(kDSel, kDSel), w.w = Elem<T>::pack(1.f / kDSel, 1.f / kDSel);
+      if (kIsHalf<T>) w.y = one, w.z = Elem<T>::pack(kDSel, kDSel), w.w = Elem<T>::pack(1.f / kDSel, 1.f / kDSel);
+      else w.y = one << 16, w.z = one;
     }
     reinterpret_cast<uint4 *>(sel_s)[c] = w;
   }

@@ -579,3 +579,51 @@ def test_waits_that_run_out_anywhere_end_the_call(limit, d):
     """12 blocks take the form whose warpgroups share a block's keys and meet at its end."""
     q, k, v, _ = (t.cuda() for t in make(2, 2, 700, 700, d, BF16))
     calls_under_limits(lambda: window_forward(q, k, v, 300, 4, check=True), limit)
+
+
+def integer_scores(dtype, heads, nk, d, offset, seed=0):
+    """One query and nk keys of a head each whose products are integers below
+    2^24, which any order of fp32 sums gives exactly: small ones, and four of
+    `offset` squared (bf16 and fp16 hold it) that all keys share."""
+    g = torch.Generator().manual_seed(seed)
+    q, k = (torch.randint(-2, 3, (1, heads, n, d), generator=g).to(dtype) for n in (1, nk))
+    q[..., :4], k[..., :4] = offset, offset
+    return q, k, randn(1, heads, nk, d, seed=seed + 1, dtype=dtype), randn(1, heads, 1, d, seed=seed + 2, dtype=dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,offset,scale", [(BF16, 80, 0.125), (BF16, 253, 0.125), (BF16, 3, 2e-7), (BF16, 253, 0.02)])
+def test_gradients_of_large_log_sums(dtype, offset, scale):
+    """An offset that all keys share, or a small scale: |LSE / scale| up to 10^7.
+
+    Scores x = scale S of exact S.  The log-sum-exp is off by the roundings of
+    scale log2(e), its product with S, the product with log(2) and LSE / scale:
+    six of 2^-24 at most, below 2^-21 |x|, and each exponential and logarithm by
+    2^-20, so P is off by e = 2^-21 max |x| + 2^-20 and its own rounding u (fp16,
+    held times 2^8: at least 2^-33).  D is off by the rounding of O (twice u |O|
+    and e) and 2^-20 of its sum's magnitudes, dS by P's error, D's, its rounding
+    (fp16: at least 2^-27 max |dO|), the results by theirs."""
+    d, u = 64, seq_ref.unit(dtype)
+    q, k, v, do = integer_scores(dtype, 32, 40, d, offset)
+    qd, kd, vd, dod = (t.cuda() for t in (q, k, v, do))
+    o, lse = window_forward(qd, kd, vd, 0, 0, scale, check=True)
+    got = window_backward(qd, kd, vd, o, lse, dod, 0, 0, scale, check=True)
+    q, k, v, do = (t[0].double() for t in (q, k, v, do))
+    assert (q @ k.mT).abs().max() < 2 ** 24
+    x = scale * (q @ k.mT)
+    p = torch.softmax(x, -1)
+    e = 2.0 ** -21 * x.abs().max() + 2.0 ** -20
+    out, dp = p @ v, do @ v.mT
+    dd = (do * out).sum(-1, keepdim=True)
+    half = dtype == FP16
+    dp_err = 2.0 ** -20 * (do.abs() @ v.abs().mT)
+    dd_err = (do.abs() * ((p @ v.abs()) * (u + e) + u * out.abs() + 2.0 ** -20 * out.abs())).sum(-1, keepdim=True)
+    ds = p * (dp - dd)
+    floor = 2.0 ** -27 * float(do.norm(dim=-1).max()) if half else 0.0
+    p_err = p * (u + e) + (2.0 ** -33 if half else 0.0)
+    ds_err = ds.abs() * (u + e) + p * (dp_err + dd_err) + floor
+    want = dict(dq=(scale * ds @ k, scale * ds_err @ k.abs()), dk=(scale * ds.mT @ q, scale * ds_err.mT @ q.abs()),
+                dv=(p.mT @ do, p_err.mT @ do.abs()))
+    tiny = torch.finfo(dtype).smallest_normal * u
+    for g, (name, (w, b)) in zip(got, want.items()):
+        seq_ref.check(g[0], (w, b + u * w.abs() + tiny), name)
