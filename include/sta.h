@@ -337,7 +337,8 @@ sta_status sta_window_forward(const sta_window_problem *problem, const sta_rows 
  * outside every sequence of a packed call are not written, or become zeros with
  * STA_PACKED_ZERO in flags (where q_len is above 0).  fp16: products
  * |dO_i| |V_j| are scaled to the largest |dO_i|, and V rows up to a norm of 8192
- * do not overflow. */
+ * do not overflow.  LSE and D enter in fp32's precision and range; a positive
+ * scale below 2^-100 is refused (STA_ERR_INVALID_ARG). */
 sta_status sta_window_backward(const sta_window_problem *problem, const sta_rows *q, const sta_rows *k,
                                const sta_rows *v, const sta_rows *o, const float *lse, const sta_rows *dout,
                                const sta_rows *dq, const sta_rows *dk, const sta_rows *dv, const int32_t *cu_q,

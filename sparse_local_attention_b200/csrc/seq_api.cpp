@@ -12,6 +12,7 @@
 namespace {
 
 constexpr size_t kStatusBytes = 256;
+constexpr float kLeastScale = 7.888609052210118e-31f;  // 2^-100: |LSE / scale| is finite
 constexpr long long kMaxRows = (1ll << 31) - 1024;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -309,6 +310,7 @@ sta_status sta_window_backward(const sta_window_problem *p, const sta_rows *q, c
                                void *ws, size_t ws_bytes, void *stream_, uint32_t flags) {
   if (const sta_status st = check_problem(p)) return st;
   if (bad_window_call(flags, cu_q, cu_kv) || !lse) return STA_ERR_INVALID_ARG;
+  if (p->scale > 0.f && p->scale < kLeastScale) return STA_ERR_INVALID_ARG;
   const sta_rows *qs[] = {q, o, dout, dq}, *ks[] = {k, v, dk, dv};
   if (const sta_status st = check_tensors(p, cu_q, qs, 4, ks, 4)) return st;
   if (const sta_status st = check_workspace(ws, ws_bytes, window_bwd_bytes(p))) return st;

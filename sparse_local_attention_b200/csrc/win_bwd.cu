@@ -61,13 +61,6 @@ struct Roles {
 template <class T> constexpr bool kIsHalf = std::is_same<T, __half>::value;
 template <class T> constexpr float kPShift = kIsHalf<T> ? 8.f : 0.f;  // log2 of P's factor
 
-// x as hi + lo of type T (lo: element 1).
-template <class T>
-__device__ __forceinline__ uint32_t hi_lo(float x) {
-  const uint32_t h = Elem<T>::pack(x, 0.f);
-  return Elem<T>::pack(x, x - Elem<T>::unpack(h).x);
-}
-
 // x as three bf16 numbers, lo in bits 0..15 of r[0]: 24 bits, as many as x has
 // (two leave 2^-18 of x, 4% of P at a log-sum-exp of 10 000).
 __device__ __forceinline__ void three_parts(float x, uint32_t (&r)[2]) {
@@ -78,11 +71,8 @@ __device__ __forceinline__ void three_parts(float x, uint32_t (&r)[2]) {
   r[1] = E::pack(rest - E::unpack(r[0]).y, 0.f);
 }
 
-// The panel row of one query.  bf16: elements 0 -- 2 carry -LSE / scale, 3 -- 5
-// -D.  fp16: elements 0, 1 carry -LSE / scale (times 1 / kLseSel), 2, 3 carry -D,
-// 4, 5 large D and 6, 7 small D, against selectors that undo the factors.
-template <class T> constexpr float kLseSel = kIsHalf<T> ? 16.f : 1.f;
-constexpr float kDSel = 16384.f;
+// The panel row of one query, in bf16 whatever T is (fp16 would end at a
+// |LSE / scale| of 2^20): elements 0 -- 2 carry -LSE / scale, 3 -- 5 -D.
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -185,19 +175,10 @@ __global__ void __launch_bounds__(256) window_pre_kernel(const WinParams p) {
     if (part < 4) {
       p.dd[stat_row(p, s, h, row)] = acc;
       // a row that sees nothing has LSE = -inf; all its pairs are masked
-      const float l = lse == -INFINITY ? 0.f : -lse / p.scale;
-      if constexpr (kIsHalf<T>) {
-        w[0] = hi_lo<T>(l * (1.f / kLseSel<T>));
-        const float big = fabsf(acc);
-        if (big > 1024.f) w[2] = hi_lo<T>(-acc * (1.f / kDSel));
-        else if (big < 1.f / 16) w[3] = hi_lo<T>(-acc * kDSel);
-        else w[1] = hi_lo<T>(-acc);
-      } else {
-        uint32_t a[2], d[2];
-        three_parts(l, a);
-        three_parts(-acc, d);
-        w[0] = a[0], w[1] = a[1] | d[0] << 16, w[2] = d[0] >> 16 | d[1] << 16;
-      }
+      uint32_t a[2], d[2];
+      three_parts(lse == -INFINITY ? 0.f : -lse / p.scale, a);
+      three_parts(-acc, d);
+      w[0] = a[0], w[1] = a[1] | d[0] << 16, w[2] = d[0] >> 16 | d[1] << 16;
     }
     const long long ar = aug0 + row;  // two halves of 16 bytes, the second one zero
     *reinterpret_cast<uint4 *>(p.aug + ar / 8 * 256 + part / 4 * 128 + ar % 8 * 16) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -333,20 +314,14 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  // selector panels, every row alike: bf16 (1, 1, 1, 0, ...) picks -LSE / scale, (0,
-  // 0, 0, 1, 1, 1) -D; fp16 (l, l, 0, ...), (0, 0, 1, 1, 2^14, 2^14, 2^-14, 2^-14)
+  // selector panels, every row alike: (1, 1, 1, 0, ...) picks -LSE / scale, (0, 0, 0,
+  // 1, 1, 1, 0, ...) -D
   for (int c = threadIdx.x; c < (int)(C::kSel / 16); c += blockDim.x) {
     const bool first_half = ((c * 16) % 256) < 128, d_panel = c * 16 >= (int)kAugBytes;
-    const uint32_t one = Elem<T>::pack(1.f, 1.f), l = Elem<T>::pack(kLseSel<T>, kLseSel<T>);
+    const uint32_t one = 0x3f80u;  // bf16
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (first_half && !d_panel) {
-      w.x = l;
-      if (!kIsHalf<T>) w.y = one & 0xffffu;
-    }
-    if (first_half && d_panel) {
-      if (kIsHalf<T>) w.y = one, w.z = Elem<T>::pack(kDSel, kDSel), w.w = Elem<T>::pack(1.f / kDSel, 1.f / kDSel);
-      else w.y = one << 16, w.z = one;
-    }
+    if (first_half && !d_panel) w.x = one | one << 16, w.y = one;
+    if (first_half && d_panel) w.y = one << 16, w.z = one | one << 16;
     reinterpret_cast<uint4 *>(sel_s)[c] = w;
   }
   fence_proxy_async_cta();
@@ -450,6 +425,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
     }
   } else if (warp == R::kMmaWarp) {
     constexpr uint32_t idesc_ss = idesc_for<T>(kBM, kBM, false, false);
+    constexpr uint32_t idesc_aug = idesc_for<__nv_bfloat16>(kBM, kBM, false, false);  // the panels'
     constexpr uint32_t idesc_acc = idesc_for<T>(kBM, D, false, true);
     const uint64_t kd = smem_desc_sw128(smem_u32(k_s), 16, 1024), vd = smem_desc_sw128(smem_u32(v_s), 16, 1024);
     const uint64_t qk0 = smem_desc_sw128(smem_u32(q_st), 16, 1024), qm0 = smem_desc_sw128(smem_u32(q_st), kTilePanel, 1024);
@@ -466,7 +442,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
         const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
         mma_ss_w(tmem + C::kTmS, kd + off, qk0 + so + off, idesc_ss, kk > 0 ? 1u : 0u);
       }
-      mma_ss_w(tmem + C::kTmS, sel_l, aug0 + so, idesc_ss, 1u);
+      mma_ss_w(tmem + C::kTmS, sel_l, aug0 + so, idesc_aug, 1u);
       mma_commit_w(s_full);
     };
     auto issue_dp = [&](uint32_t st) {  // dP^T = V dO^T - D
@@ -475,7 +451,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
         const uint32_t off = ((kk / 4) * kTilePanel + (kk % 4) * 32) >> 4;
         mma_ss_w(tmem + C::kTmDP, vd + off, gk0 + ((st * C::kTile) >> 4) + off, idesc_ss, kk > 0 ? 1u : 0u);
       }
-      mma_ss_w(tmem + C::kTmDP, sel_d, aug0 + ((st * C::kQStage) >> 4), idesc_ss, 1u);
+      mma_ss_w(tmem + C::kTmDP, sel_d, aug0 + ((st * C::kQStage) >> 4), idesc_aug, 1u);
       mma_commit_w(dp_full);
     };
     auto wait_full = [&](uint64_t *full, uint32_t l) -> bool {

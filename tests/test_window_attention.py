@@ -482,6 +482,15 @@ def test_bad_calls_are_refused_before_anything_is_enqueued():
     assert bwd(lse=None) == 1 and bwd(dk=None) == 1 and bwd(dk=row(ptr=8)) == 4 and bwd(size=n.value - 1) == 5
 
 
+def test_a_scale_too_small_for_gradients_is_refused():
+    L, n, row = sta.lib(), ctypes.c_size_t(), sta._Rows(4096, 2560, 640, 64)
+    for scale, status in ((2.0 ** -101, 1), (2.0 ** -100, 5)):  # the second gets as far as the workspace
+        p = problem(scale=scale)
+        assert L.sta_window_workspace_size(ctypes.byref(p), None, ctypes.byref(n)) == 0
+        assert L.sta_window_backward(ctypes.byref(p), row, row, row, row, 4096, row, row, row, row, None, None, 4096, 0,
+                                     None, 0) == status
+
+
 def test_binding_refusals():
     q = torch.zeros(1, 2, 8, 64, dtype=BF16)
     with pytest.raises(ValueError, match="CUDA"):
@@ -592,7 +601,9 @@ def integer_scores(dtype, heads, nk, d, offset, seed=0):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("dtype,offset,scale", [(BF16, 80, 0.125), (BF16, 253, 0.125), (BF16, 3, 2e-7), (BF16, 253, 0.02)])
+@pytest.mark.parametrize("dtype,offset,scale", [(BF16, 80, 0.125), (BF16, 253, 0.125), (BF16, 3, 2e-7), (BF16, 253, 0.02),
+                                                (FP16, 3, 0.125), (FP16, 500, 0.125), (FP16, 600, 0.125), (FP16, 2000, 0.125),
+                                                (FP16, 3, 2e-6), (FP16, 3, 2e-7)])
 def test_gradients_of_large_log_sums(dtype, offset, scale):
     """An offset that all keys share, or a small scale: |LSE / scale| up to 10^7.
 
