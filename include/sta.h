@@ -282,7 +282,10 @@ void sta_set_wait_limit_ns(uint64_t ns);
  *     (positions below 0) get O = 0, LSE = -inf and gradients of 0.
  *   - K and V rows past a sequence's end, and keys that no query of a call
  *     sees, never reach a result.  A non-finite K or V row that one query of
- *     a 128-row block sees may reach the block's other rows.
+ *     a 128-row block sees may reach the block's other rows.  Gradients:
+ *     query rows (Q, dO) that see nothing never reach a result either, and a
+ *     non-finite one that sees a key may reach the gradients of the other keys
+ *     of its 128-key block.
  */
 
 /* element types */

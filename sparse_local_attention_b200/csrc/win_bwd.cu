@@ -202,9 +202,15 @@ struct KeyItem {
   Sequence s;
   int b, hk, key0, rows;  // rows: 0 for a part that is not there
   int qa, qe, per_head, c0, c1, segs;
+  int lead;  // rows of a head's first chunk before the first one that sees the block
   long long slot;  // of the part's sums, or -1: the block is one part
   __device__ __forceinline__ int first(int c) const { return qa + c % per_head * kBM; }
   __device__ __forceinline__ int valid(int c) const { return min(kBM, qe - first(c)); }
+  __device__ __forceinline__ int hidden(int c) const { return c % per_head == 0 ? lead : 0; }
+  // Rows of a chunk that the contraction meets and that do not see the block (the
+  // first `hidden`, and those past `valid` up to a multiple of 16) are cleared:
+  // NaN there would not stay behind a P of zero.
+  __device__ __forceinline__ bool clears(int c) const { return valid(c) % 16 != 0 || hidden(c) > 0; }
 };
 
 // The queries that see a key block, and its number of parts.
@@ -212,6 +218,7 @@ __device__ __forceinline__ void block_queries(const WinParams &p, KeyItem &it) {
   const int off = it.s.nk - it.s.nq;
   it.rows = min(kBM, it.s.nk - it.key0);
   it.qa = max(0, it.key0 - off) & ~7;  // panels start at multiples of 8
+  it.lead = max(0, it.key0 - off) & 7;
   const int past = it.key0 + it.rows - 1 + p.window - off;  // first row past the window of the last key
   it.qe = it.rows <= 0 ? 0 : it.key0 < p.sinks ? it.s.nq : min(it.s.nq, past);
   it.per_head = max(0, (it.qe - it.qa + kBM - 1) / kBM);
@@ -364,7 +371,7 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
         for (int c = it.c0; c < it.c1; ++c) {
           const uint32_t st = ld % C::kStages, ph = (ld / C::kStages) & 1, bit = 1u << st;
           const int h = it.hk * p.group + c / it.per_head, first = it.first(c);
-          const bool clear = it.valid(c) % 16 != 0;
+          const bool clear = it.clears(c);
           if (!mbar_wait(&q_empty[st], ph ^ 1, ctl, kErrBwdWait)) { ok = false; break; }
           raw_last = clear ? raw_last | bit : raw_last & ~bit;
           if (clear) raw_par ^= bit;
@@ -407,17 +414,19 @@ __global__ void __launch_bounds__(DkvCfg<D>::R::kThreads, 1)
       const KeyItem it = *at;
       ring.release(n, lane);
       for (int c = it.c0; c < it.c1 && ok; ++c, ++ld) {
-        const int valid = it.valid(c);
-        if (valid % 16 == 0) continue;
+        if (!it.clears(c)) continue;
+        const int valid = it.valid(c), hidden = it.hidden(c);
         const uint32_t st = ld % C::kStages, par = raw_par >> st & 1;
         const int upto = (valid + 15) & ~15;
         ok = mbar_wait_w(&q_raw[st], par, ctl, kErrBwdWait);
         if (!ok) break;
+        clear_rows<D>(q_st + st * C::kQStage, 0, hidden, lane);
         clear_rows<D>(q_st + st * C::kQStage, valid, upto, lane);
         if (lane == 0) mbar_arrive(&q_full[st]);
         ok = mbar_wait_w(&do_raw[st], par, ctl, kErrBwdWait);
         raw_par ^= 1u << st;
         if (!ok) break;
+        clear_rows<D>(do_st + st * C::kTile, 0, hidden, lane);
         clear_rows<D>(do_st + st * C::kTile, valid, upto, lane);
         if (lane == 0) mbar_arrive(&do_full[st]);
       }

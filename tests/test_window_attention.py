@@ -638,3 +638,34 @@ def test_gradients_of_large_log_sums(dtype, offset, scale):
     tiny = torch.finfo(dtype).smallest_normal * u
     for g, (name, (w, b)) in zip(got, want.items()):
         seq_ref.check(g[0], (w, b + u * w.abs() + tiny), name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("nq,nk,d", [(205, 64, 64), (300, 301, 128), (300, 307, 64), (400, 261, 128)])
+def test_hidden_queries_reach_nothing(nq, nk, d, dtype):
+    """Query rows that see nothing hold NaN and infinities, in Q and in dO; and a
+    query's reach the gradients of no key behind it."""
+    q, k, v, do = make(4, 2, nq, nk, d, dtype, seed=nq + nk)
+    mask = seq_ref.mask_of(nq, nk, 90, 3)
+    blind = ~mask.any(1)
+    top = float(do[:, :, ~blind].double().norm(dim=-1).max())
+    want = seq_ref.attention(q[0], k[0], v[0], mask, d ** -0.5, do[0], dtype, top)
+    kd, vd = k.cuda(), v.cuda()
+
+    def run(rows, bad):
+        qb, gb = q.clone(), do.clone()
+        qb[:, :, rows], gb[:, :, rows] = bad, bad
+        qd, gd = qb.cuda(), gb.cuda()
+        o, lse = window_forward(qd, kd, vd, 90, 3, check=True)
+        return window_backward(qd, kd, vd, o, lse, gd, 90, 3, check=True)
+
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        if blind.any():
+            for name, got in zip(("dq", "dk", "dv"), run(blind, bad)):
+                seq_ref.check(got[0], want[name], name)
+        # a query whose last key is the last one of a block of 128
+        row = 127 - (nk - nq)
+        if row < nq and nk > 128:
+            for name, got in zip(("dk", "dv"), run([row], bad)[1:]):
+                assert bool(got[0, :, 128:].isfinite().all()), name
