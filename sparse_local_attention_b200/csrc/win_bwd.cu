@@ -187,7 +187,10 @@ __global__ void __launch_bounds__(256) window_pre_kernel(const WinParams p) {
     __shared__ int top;
     if (threadIdx.x == 0) top = 0;
     __syncthreads();
-    const int most = __reduce_max_sync(0xffffffffu, __float_as_int(sqrtf(sum_rows<kLanes>(sqs, part))));
+    // rows that see nothing have no gradients, those of others are not finite
+    const float sq = sum_rows<kLanes>(sqs, part);
+    const bool counts = valid && lse > -INFINITY && sq < INFINITY;
+    const int most = __reduce_max_sync(0xffffffffu, counts ? __float_as_int(sqrtf(sq)) : 0);
     if (lane == 0) atomicMax(&top, most);  // nonnegative floats order like integers
     __syncthreads();
     if (threadIdx.x == 0) p.norms[((long long)b * p.heads + h) * gridDim.x + blockIdx.x] = __int_as_float(top);

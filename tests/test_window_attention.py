@@ -669,3 +669,27 @@ def test_hidden_queries_reach_nothing(nq, nk, d, dtype):
         if row < nq and nk > 128:
             for name, got in zip(("dk", "dv"), run([row], bad)[1:]):
                 assert bool(got[0, :, 128:].isfinite().all()), name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 6e4], ids=str)
+def test_hidden_or_non_finite_gradients_do_not_scale_the_others(bad):
+    """fp16 gradients are scaled by the largest row of dO: one that sees nothing,
+    or is not finite itself, does not count."""
+    nq, nk, d = 205, 64, 64
+    q, k, v, do = make(4, 2, nq, nk, d, FP16, seed=77, do_scale=2.0 ** -12)
+    mask = seq_ref.mask_of(nq, nk, 90, 3)
+    blind = ~mask.any(1)
+    want = seq_ref.attention(q[0], k[0], v[0], mask, d ** -0.5, do[0], FP16)
+    qd, kd, vd = q.cuda(), k.cuda(), v.cuda()
+    o, lse = window_forward(qd, kd, vd, 90, 3, check=True)
+    gb = do.clone()
+    gb[:, :, blind] = bad
+    for name, got in zip(("dq", "dk", "dv"), window_backward(qd, kd, vd, o, lse, gb.cuda(), 90, 3, check=True)):
+        seq_ref.check(got[0], want[name], name)
+    if bad != 6e4:
+        gb = do.clone()
+        gb[:, :, 200] = bad
+        dq = window_backward(qd, kd, vd, o, lse, gb.cuda(), 90, 3, check=True)[0]
+        others = torch.arange(nq) != 200
+        seq_ref.check(dq[0][:, others], tuple(t[:, others] for t in want["dq"]), "dq")
