@@ -13,9 +13,12 @@
 //     The blocks with the most keys come first, on whichever SM is free.
 //   * An item's keys are its sinks, then its window [lo, hi], each in chunks
 //     of 128 from its own first key on (TMA rows need no alignment), so no
-//     chunk holds keys below every row's window, and a chunk that one of the
-//     units does not see is skipped for it.  Chunks that every row of a unit
-//     sees whole take no mask; others apply a 128-bit mask per row.
+//     chunk holds keys below every row's window.  Where A and B are blocks of
+//     different rows, chunks also end where A's keys end and begin where B's
+//     window begins, so that a unit sees all of a chunk's keys or is left out
+//     of it: a V row that only the other one sees would reach it as 0 x NaN.
+//     Chunks that every row of a unit sees whole take no mask; others apply a
+//     128-bit mask per row.
 //   * Keys of a chunk past its valid ones (another sequence's, or the future)
 //     must not meet P = 0 as NaN: the product P V runs over the valid keys
 //     rounded up to 16, and the "clear" warp zeroes the V rows in between.
@@ -48,14 +51,19 @@ struct Item {
   int h[2], qb[2];   // query head and query block of A and B
   bool has[2];
   int pos0[2], lo[2], hi[2];  // position of row 0; first window key; last key (below 0: none)
-  int base, last, nsink;      // window keys [base, last], sink keys [0, nsink)
+  int nsink, base, edge, past; // sink keys [0, nsink), window keys [base, edge); only B sees [edge, past)
+  int gap, tail;              // chunks apart from the rest: keys [nsink, base + kBM) that only A sees, and [edge, past)
   int ns, nc;                 // sink chunks, chunks
   int n0;                     // split: chunks [0, n0) are warpgroup 0's, [n0, nc) warpgroup 1's
   __device__ __forceinline__ int begin(int x) const { return x ? n0 : 0; }
   __device__ __forceinline__ int end(int x) const { return x ? nc : n0; }
   __device__ __forceinline__ void chunk(int j, int &first, int &valid) const {
     first = j < ns ? j * kBM : base + (j - ns) * kBM;
-    valid = min(kBM, (j < ns ? nsink : last + 1) - first);
+    valid = min(kBM, (j < ns ? nsink : edge) - first);
+    if (j == gap || j == tail) {
+      first = j == gap ? nsink : edge;
+      valid = (j == gap ? base + kBM : past) - first;
+    }
   }
 };
 
@@ -122,11 +130,20 @@ __device__ __forceinline__ Item decode(const WinParams &p, int item) {
     it.lo[x] = max(0, it.pos0[x] - p.window + 1);
     it.hi[x] = it.has[x] ? min(it.s.nk - 1, it.pos0[x] + rows - 1) : -1;
   }
-  it.last = max(it.hi[0], it.hi[1]);
   it.base = p.sinks >= it.lo[0] ? 0 : it.lo[0];
   it.nsink = min(p.sinks, it.base);
+  it.edge = it.past = max(it.hi[0], it.hi[1]) + 1;
+  it.gap = it.tail = -1;
+  // A block of rows each: B's keys end at most 128 behind A's, and its window
+  // begins 128 behind A's, where a chunk does, or nearer if the sequence's start
+  // or the sinks cut A's.
+  const bool two = !kSplit && it.has[1] && it.qb[1] > it.qb[0] && it.hi[0] >= 0, cut = two && it.base == 0 && p.sinks < it.lo[1];
+  if (two) it.edge = it.hi[0] + 1;
+  if (cut) it.nsink = p.sinks, it.base = it.lo[1] - kBM;
   it.ns = (it.nsink + kBM - 1) / kBM;
-  it.nc = it.has[0] && it.last >= 0 ? it.ns + (it.last - it.base + kBM) / kBM : 0;
+  it.nc = it.has[0] && it.past > 0 ? it.ns + (it.edge - it.base + kBM - 1) / kBM + two : 0;
+  if (cut) it.gap = it.ns;
+  if (two) it.tail = it.nc - 1;
   it.n0 = (it.nc + 1) / 2;
   return it;
 }

@@ -693,3 +693,31 @@ def test_hidden_or_non_finite_gradients_do_not_scale_the_others(bad):
         dq = window_backward(qd, kd, vd, o, lse, gb.cuda(), 90, 3, check=True)[0]
         others = torch.arange(nq) != 200
         seq_ref.check(dq[0][:, others], tuple(t[:, others] for t in want["dq"]), "dq")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv_heads,nq,nk,window,sinks", [
+    (32, 32, 700, 700, 512, 0),   # pairs of blocks that end 128 keys apart, inside a chunk
+    (32, 32, 700, 760, 100, 0),
+    (32, 32, 600, 689, 0, 0),     # no window, off the chunks
+    (32, 32, 700, 700, 200, 40),  # the second block's window begins inside the first chunk, behind the sinks
+    (32, 32, 700, 733, 300, 64),
+    (33, 11, 640, 640, 150, 7),   # pairs of heads and pairs of blocks by turns
+], ids=str)
+@pytest.mark.parametrize("d", [64, 128])
+def test_non_finite_keys_reach_only_blocks_that_see_them(heads, kv_heads, nq, nk, window, sinks, d):
+    """More blocks than the GPU has SMs, so that two of a key head share their
+    keys: a row of NaN in K and V leaves every 128-row block that does not see it
+    as it was."""
+    q, k, v, _ = (t.cuda() for t in make(heads, kv_heads, nq, nk, d, BF16, seed=nk))
+    clean = window_forward(q, k, v, window, sinks, check=True)
+    mask = seq_ref.mask_of(nq, nk, window, sinks)
+    for key in sorted({*range(0, nk, 13), *range(nk - nq, nk, 128), nk - 1}):  # the first behind each block, too
+        kb, vb = k.clone(), v.clone()
+        kb[:, :, key], vb[:, :, key] = float("nan"), float("nan")
+        got = window_forward(q, kb, vb, window, sinks, check=True)
+        sees = [bool(mask[i:i + 128, key].any()) for i in range(0, nq, 128)]
+        rows = torch.tensor(sees).repeat_interleave(128)[:nq].cuda()
+        same = all(torch.equal(a[:, :, ~rows], b[:, :, ~rows]) for a, b in zip(got, clean))
+        assert same, f"key {key}"
+        assert bool(got[0][:, :, mask[:, key].cuda()].isnan().all()), key
