@@ -394,6 +394,9 @@ sta_status sta_cache_read(const sta_cache *cache, int32_t batch, int32_t rows, c
  * in the cache) over the cache: the forward of sta_window_forward with
  * Nk = lengths[b] (device int32, cut to [0, table_pages * page_size]) and
  * Nq = q_len.  q, o: type `type`; lse fp32 [batch][heads][q_len], nullable.
+ * P times a block's scale of values is rounded to fp16 at 2^7 or more for a
+ * row's largest such product, so that 2^-31 of it is still told from zero,
+ * whatever the scales.
  * Meant for few queries: every 16 query rows of a key head (heads / kv_heads *
  * q_len of them) read its keys once.  Needs no workspace. */
 sta_status sta_cache_attention(const sta_cache *cache, int32_t batch, int32_t heads, int32_t q_len, int32_t window,

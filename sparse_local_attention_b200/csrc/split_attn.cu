@@ -36,10 +36,13 @@ namespace cg = cooperative_groups;
 constexpr int kWarps = 8, kThreads = 32 * kWarps, kStep = 16;  // keys per step
 // P = 2^(x - m) with m set to the maximum less kHead, and moved when a score
 // exceeds m by kHead + 8: P stays below 2^15 and the smallest fp16 stands for 2^-31.
+// Where the values have scales s, what meets their codes is P s, and it has a
+// maximum of its own: P s = 2^(x + log2 s - n), n set and moved like m.  (With P s
+// over the largest s, a block's values were lost beside one of 2^31 their scale,
+// however little weight that one had.)
 constexpr float kHead = 7.f;
 // m of a row without a key so far, far below any score
 constexpr float kNoMax = -1e30f;
-constexpr float kLeastScale = 1.1754943508222875e-38f;  // 2^-126
 constexpr int kMaxSplits = 16;  // blocks of a cluster
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
@@ -337,10 +340,11 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
   auto step_of = [&](int i) { return i < sink_steps ? i : i + skipped; };
 
   float o[NT][D / 16][4], m[NT][2], l[NT][2];
-  float v_top = kLeastScale, v_inv = 1.f / kLeastScale;
+  float ms[NT][2];  // n, where the values have scales
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m[nt][0] = m[nt][1] = kNoMax, l[nt][0] = l[nt][1] = 0.f;
+    ms[nt][0] = ms[nt][1] = kNoMax;
 #pragma unroll
     for (int t = 0; t < D / 16; ++t) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
   }
@@ -475,10 +479,11 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
           for (int nt = 0; nt < NT; ++nt) mma16816(x[nt], a, qf[nt][s][0], qf[nt][s][1], Op{});
         }
       }
-      float ks = 1.f, vs = 1.f;
+      float ks = 1.f, vs = 1.f, vs_log = 0.f;
       if constexpr (Keys::kScaled) {
         const float2 f = *reinterpret_cast<const float2 *>(k_s + 2 * C::kHalf);
         ks = f.x, vs = f.y;
+        vs_log = __log2f(fabsf(vs));
       }
       // whole: every row sees the 16 keys (rows that are not there are not read)
       const int k0 = step * kStep;
@@ -488,7 +493,9 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float2 f = mul2(make_float2(fac[nt][0], fac[nt][1]), make_float2(ks, ks));
-        const float2 most = add2(make_float2(m[nt][0], m[nt][1]), make_float2(kHead + 8.f, kHead + 8.f));
+        float2 most = make_float2(m[nt][0], m[nt][1]);
+        if constexpr (Keys::kScaled) most = make_float2(fminf(most.x, ms[nt][0] - vs_log), fminf(most.y, ms[nt][1] - vs_log));
+        most = add2(most, make_float2(kHead + 8.f, kHead + 8.f));
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const float2 y = mul2(make_float2(x[nt][e], x[nt][e + 1]), f);
@@ -511,45 +518,39 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(top - kHead, m[nt][e]);
-            const float alpha = ex2_approx(m[nt][e] - top);
+            const float most = top - kHead;
+            top = fmaxf(most, m[nt][e]);
+            float alpha = ex2_approx(m[nt][e] - top);
             m[nt][e] = top;
             l[nt][e] *= alpha;
+            if constexpr (Keys::kScaled) {
+              top = fmaxf(most + vs_log, ms[nt][e]);
+              alpha = ex2_approx(ms[nt][e] - top);
+              ms[nt][e] = top;
+            }
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) o[nt][t][e] *= alpha, o[nt][t][2 + e] *= alpha;
           }
       }
-      float pv = 1.f;
-      if constexpr (Keys::kScaled) {
-        // O is held over v_top, the largest scale of values so far (a power of
-        // two), and P takes the step's own scale over it: at most 1
-        if (vs > v_top) {
-          const float top = __int_as_float(min((__float_as_int(vs) >> 23) + 1, 254) << 23);
-          const float down = v_top * (1.f / top);
-          v_top = top, v_inv = 1.f / top;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[nt][t][e] *= down;
-        }
-        pv = vs * v_inv;
-      }
+      const uint32_t sign = Keys::kScaled && vs < 0.f ? 0x80008000u : 0u;
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-          float2 y = add2(make_float2(x[nt][e], x[nt][e + 1]), make_float2(-m[nt][0], -m[nt][1]));
+          const float2 z = make_float2(x[nt][e], x[nt][e + 1]);
+          float2 y = add2(z, make_float2(-m[nt][0], -m[nt][1]));
           y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
           const float2 sum = add2(make_float2(l[nt][0], l[nt][1]), y);
           l[nt][0] = sum.x, l[nt][1] = sum.y;
-          if constexpr (Keys::kScaled) y = mul2(y, make_float2(pv, pv));
+          if constexpr (Keys::kScaled) {
+            y = add2(z, make_float2(vs_log - ms[nt][0], vs_log - ms[nt][1]));
+            y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+          }
           x[nt][e] = y.x, x[nt][e + 1] = y.y;
         }
-        pb[nt][0] = transpose8(Elem<Op>::pack(x[nt][0], x[nt][1]));
-        pb[nt][1] = transpose8(Elem<Op>::pack(x[nt][2], x[nt][3]));
+        pb[nt][0] = transpose8(Elem<Op>::pack(x[nt][0], x[nt][1]) ^ sign);
+        pb[nt][1] = transpose8(Elem<Op>::pack(x[nt][2], x[nt][3]) ^ sign);
       }
       uint32_t w[4][kRow / 32];
 #pragma unroll
@@ -601,8 +602,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
       float top = kNoMax;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w * kRows + r]);
-      float f = weight(m[nt][e], top);
-      if constexpr (Keys::kScaled) f *= v_top;
+      const float f = weight(Keys::kScaled ? ms[nt][e] : m[nt][e], top);
 #pragma unroll
       for (int t = 0; t < D / 16; ++t)
         *reinterpret_cast<float2 *>(&o_s[(warp * kRows + r) * kPitch + Keys::v_col(t, g)]) =

@@ -441,3 +441,63 @@ def test_offsets_past_32_bits(fmt):
     for a, b in zip(same, other):
         assert torch.equal(a, b)
     assert torch.equal(small_k[:2], large_k[:2]) and torch.equal(results[0][-1], results[1][-1])
+
+
+def attend_unequal(p, table, lens, q, window, sinks, **kw):
+    """attend_and_check for values of any scales: a row's P times its block's scale
+    of values is rounded to fp16 at 2^7 or more for the largest such product, so
+    half a step of the smallest numbers, 2^-25, stands for 2^-32 of it, times the
+    code.  Sums are fp32: 2^-20 of their magnitudes."""
+    o, lse = p.cache.attention(q.cuda(), table.cuda(), ints(*lens).cuda(), window, sinks, check=True, **kw)
+    c, g = p.cache, q.shape[1] // p.cache.kv_heads
+    for b, n in enumerate(lens):
+        k, there = seq_ref.cache_values(p.host[0], p.host[2], table, b, n)
+        v, _ = seq_ref.cache_values(p.host[1], p.host[3], table, b, n)
+        scale = p.host[3][table[b].long()].transpose(0, 1).flatten(1).double().repeat_interleave(c.block, 1)[:, :n]
+        mask = seq_ref.mask_of(q.shape[2], n, window, sinks) & there
+        want = seq_ref.attention(q[b], k, v, mask, q.shape[3] ** -0.5)
+        kd, vd, sd = (t.repeat_interleave(g, 0) for t in (k, v, scale))
+        x = (q[b].double() @ kd.mT * q.shape[3] ** -0.5).masked_fill(~mask, float("-inf"))
+        w = torch.softmax(x, -1).nan_to_num(0.0) * sd[:, None]
+        floor = 2.0 ** -32 * w.amax(-1, keepdim=True) * ((mask / sd[:, None].clamp_min(2.0 ** -100)) @ vd.abs())
+        o_want, o_bound = want["o"]
+        o_bound = o_bound + (seq_ref.unit(q.dtype) - seq_ref.unit(BF16)) * o_want.abs() + floor
+        seq_ref.check(o[b], (o_want, o_bound), f"o of sequence {b}")
+        seq_ref.check(lse[b], want["lse"], f"lse of sequence {b}")
+    return o, lse
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [E4M3, INT8], ids=["e4m3", "int8"])
+@pytest.mark.parametrize("heads,q_len,d", [(2, 1, 128), (8, 4, 64), (4, 1, 64)])
+@pytest.mark.parametrize("up,block_at", [(12, 3), (24, 0), (24, 9), (34, 3), (60, 5)])
+def test_values_beside_a_block_of_a_much_larger_scale(fmt, heads, q_len, d, up, block_at):
+    """One block's values are 2^up times the others', and its keys get next to no
+    weight (or its tokens are not seen): the others' contribution stays."""
+    lens = [400]
+    table, pages = tables(1, 13, seed=4)
+    p = Pair(pages, 2, 32, d, 16, fmt)
+    k, v = (randn(1, 2, 400, d, seed=60 + i, dtype=BF16) for i in (0, 1))
+    q = randn(1, heads, q_len, d, seed=62, dtype=BF16)
+    q[..., 0], k[..., 0] = 16.0, 0.0
+    rows = slice(16 * block_at, 16 * block_at + 16)
+    v[:, :, rows] *= 2.0 ** up
+    k[:, :, rows, 0] = -min(up + 8, 60) * 0.6931 * d ** 0.5 / 16  # weight 2^-(up + 8), up to 2^-60
+    p.write(k, v, table, ints(0), ints(400))
+    attend_unequal(p, table, lens, q, 0, 0)
+    attend_unequal(p, table, lens, q, 90, 16 * block_at + 3)  # some of the block's tokens are seen, or none
+
+
+@pytest.mark.gpu
+def test_an_outlier_reaches_only_rows_that_see_its_block():
+    """Rows that do not see any token of an outlier's block (behind their
+    positions, or before their window) keep their precision beside rows that do."""
+    table, pages = tables(1, 4, seed=5)
+    k, v = (randn(1, 1, 64, 64, seed=70 + i, dtype=BF16) for i in (0, 1))
+    q = randn(1, 2, 20, 64, seed=72, dtype=BF16)  # positions 44 .. 63
+    for token, window in ((50, 40), (17, 20)):
+        p = Pair(pages, 1, 16, 64, 16, E4M3)
+        vb = v.clone()
+        vb[:, :, token] = 2.0 ** 60
+        p.write(k, vb, table, ints(0))
+        attend_unequal(p, table, [64], q, window, 0)
