@@ -41,8 +41,8 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps, kStep = 16;  // keys per step
 // over the largest s, a block's values were lost beside one of 2^31 their scale,
 // however little weight that one had.)
 constexpr float kHead = 7.f;
-// m of a row without a key so far, far below any score
-constexpr float kNoMax = -1e30f;
+// m of a row without a key so far: no score is below it
+constexpr float kNoMax = -3.4028234663852886e38f;
 constexpr int kMaxSplits = 16;  // blocks of a cluster
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {

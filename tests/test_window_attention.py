@@ -721,3 +721,20 @@ def test_non_finite_keys_reach_only_blocks_that_see_them(heads, kv_heads, nq, nk
         same = all(torch.equal(a[:, :, ~rows], b[:, :, ~rows]) for a, b in zip(got, clean))
         assert same, f"key {key}"
         assert bool(got[0][:, :, mask[:, key].cuda()].isnan().all()), key
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv_heads,nq,nk", [(2, 2, 1, 5), (2, 1, 9, 9), (2, 2, 200, 200)])
+def test_scores_far_below_zero(heads, kv_heads, nq, nk):
+    """Equal scores of -2^117 for all keys: O is the mean of the visible values.
+    The sums of nk terms are off by 2^-20, P and O by their roundings."""
+    _, _, v, _ = make(heads, kv_heads, nq, nk, 64, BF16, seed=nk)
+    q, k = torch.zeros(1, heads, nq, 64, dtype=BF16), torch.zeros(1, kv_heads, nk, 64, dtype=BF16)
+    q[..., 3], k[..., 3] = 2.0 ** 60, -2.0 ** 60
+    o, lse = window_forward(q.cuda(), k.cuda(), v.cuda(), check=True)
+    seen = torch.tril(torch.ones(nq, nk, dtype=torch.float64), nk - nq)
+    p = seen / seen.sum(-1, keepdim=True)
+    vv = v[0].double().repeat_interleave(heads // kv_heads, 0)
+    want, mag = p @ vv, p @ vv.abs()
+    seq_ref.check(o[0], (want, mag * (2.0 ** -8 + 2.0 ** -20) + want.abs() * 2.0 ** -8), "o")
+    assert ((lse.double().cpu() + 2.0 ** 117).abs() <= 2.0 ** (117 - 20)).all()
