@@ -37,12 +37,13 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps, kStep = 16;  // keys per step
 // P = 2^(x - m) with m set to the maximum less kHead, and moved when a score
 // exceeds m by kHead + 8: P stays below 2^15 and the smallest fp16 stands for 2^-31.
 // Where the values have scales s, what meets their codes is P s, and it has a
-// maximum of its own: P s = 2^(x + log2 s - n), n set and moved like m.  (With P s
-// over the largest s, a block's values were lost beside one of 2^31 their scale,
-// however little weight that one had.)
+// maximum of its own: 2^(x + log2 s - n), n set and moved like m and held as m - n,
+// which stays small.  (With P s over the largest s, a block's values were lost
+// beside one of 2^31 their scale, however little weight that one had.)
 constexpr float kHead = 7.f;
 // m of a row without a key so far: no score is below it
 constexpr float kNoMax = -3.4028234663852886e38f;
+constexpr float kNoScale = 200.f;
 constexpr int kMaxSplits = 16;  // blocks of a cluster
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
@@ -340,11 +341,11 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
   auto step_of = [&](int i) { return i < sink_steps ? i : i + skipped; };
 
   float o[NT][D / 16][4], m[NT][2], l[NT][2];
-  float ms[NT][2];  // n, where the values have scales
+  float mn[NT][2];  // m - n, where the values have scales
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m[nt][0] = m[nt][1] = kNoMax, l[nt][0] = l[nt][1] = 0.f;
-    ms[nt][0] = ms[nt][1] = kNoMax;
+    mn[nt][0] = mn[nt][1] = 0.f;
 #pragma unroll
     for (int t = 0; t < D / 16; ++t) o[nt][t][0] = o[nt][t][1] = o[nt][t][2] = o[nt][t][3] = 0.f;
   }
@@ -490,12 +491,13 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
       const bool whole = k0 + kStep - 1 <= first_pos && k0 + kStep <= keys.nk &&
                          (k0 > last_pos - shape.window || k0 + kStep <= shape.sinks);
       bool grows = false;
+      float z[NT][4];  // x - m
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float2 f = mul2(make_float2(fac[nt][0], fac[nt][1]), make_float2(ks, ks));
-        float2 most = make_float2(m[nt][0], m[nt][1]);
-        if constexpr (Keys::kScaled) most = make_float2(fminf(most.x, ms[nt][0] - vs_log), fminf(most.y, ms[nt][1] - vs_log));
-        most = add2(most, make_float2(kHead + 8.f, kHead + 8.f));
+        float most[2] = {kHead + 8.f, kHead + 8.f};  // above m, or n - log2 s
+        if constexpr (Keys::kScaled)
+          for (int e = 0; e < 2; ++e) most[e] -= fmaxf(0.f, mn[nt][e] + vs_log);
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const float2 y = mul2(make_float2(x[nt][e], x[nt][e + 1]), f);
@@ -506,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
             for (int c2 = 0; c2 < 2; ++c2)
               if (key >= keys.nk || !visible(pos[nt][c2], key, shape.window, shape.sinks)) x[nt][e + c2] = -INFINITY;
           }
-          grows = grows || x[nt][e] > most.x || x[nt][e + 1] > most.y;
+          z[nt][e] = x[nt][e] - m[nt][0], z[nt][e + 1] = x[nt][e + 1] - m[nt][1];
+          grows = grows || z[nt][e] > most[0] || z[nt][e + 1] > most[1];
         }
       }
       if (__any_sync(0xffffffffu, grows)) {
@@ -520,13 +523,16 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
             const float most = top - kHead;
             top = fmaxf(most, m[nt][e]);
-            float alpha = ex2_approx(m[nt][e] - top);
+            const float down = m[nt][e] - top;
+            float alpha = ex2_approx(down);
             m[nt][e] = top;
+            z[nt][e] = x[nt][e] - top, z[nt][2 + e] = x[nt][2 + e] - top;
             l[nt][e] *= alpha;
             if constexpr (Keys::kScaled) {
-              top = fmaxf(most + vs_log, ms[nt][e]);
-              alpha = ex2_approx(ms[nt][e] - top);
-              ms[nt][e] = top;
+              // no scale but 0 so far: kNoScale, more than any other
+              const float now = fminf(fminf(top - most - vs_log, mn[nt][e] - down), kNoScale);
+              alpha = ex2_approx(now - mn[nt][e] + down);
+              mn[nt][e] = now;
             }
 #pragma unroll
             for (int t = 0; t < D / 16; ++t) o[nt][t][e] *= alpha, o[nt][t][2 + e] *= alpha;
@@ -538,13 +544,11 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-          const float2 z = make_float2(x[nt][e], x[nt][e + 1]);
-          float2 y = add2(z, make_float2(-m[nt][0], -m[nt][1]));
-          y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+          float2 y = make_float2(ex2_approx(z[nt][e]), ex2_approx(z[nt][e + 1]));
           const float2 sum = add2(make_float2(l[nt][0], l[nt][1]), y);
           l[nt][0] = sum.x, l[nt][1] = sum.y;
           if constexpr (Keys::kScaled) {
-            y = add2(z, make_float2(vs_log - ms[nt][0], vs_log - ms[nt][1]));
+            y = add2(make_float2(z[nt][e], z[nt][e + 1]), make_float2(mn[nt][0] + vs_log, mn[nt][1] + vs_log));
             y = make_float2(ex2_approx(y.x), ex2_approx(y.y));
           }
           x[nt][e] = y.x, x[nt][e + 1] = y.y;
@@ -602,7 +606,9 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
       float top = kNoMax;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w * kRows + r]);
-      const float f = weight(Keys::kScaled ? ms[nt][e] : m[nt][e], top);
+      float f = m[nt][e] - top;
+      if constexpr (Keys::kScaled) f -= mn[nt][e];
+      f = ex2_approx(f);
 #pragma unroll
       for (int t = 0; t < D / 16; ++t)
         *reinterpret_cast<float2 *>(&o_s[(warp * kRows + r) * kPitch + Keys::v_col(t, g)]) =

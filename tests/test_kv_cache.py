@@ -501,3 +501,21 @@ def test_an_outlier_reaches_only_rows_that_see_its_block():
         vb[:, :, token] = 2.0 ** 60
         p.write(k, vb, table, ints(0))
         attend_unequal(p, table, [64], q, window, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [E4M3, INT8], ids=["e4m3", "int8"])
+def test_scores_far_below_zero(fmt):
+    """Equal scores below -2^116 for all keys: O is the mean of the values."""
+    table, pages = tables(1, 2, seed=6)
+    p = Pair(pages, 1, 16, 64, 16, fmt)
+    k, v = torch.zeros(1, 1, 20, 64, dtype=BF16), randn(1, 1, 20, 64, seed=81, dtype=BF16)
+    q = torch.zeros(1, 2, 1, 64, dtype=BF16)
+    q[..., 3], k[..., 3] = 2.0 ** 60, -2.0 ** 60
+    p.write(k, v, table, ints(0))
+    o, lse = p.cache.attention(q.cuda(), table.cuda(), ints(20).cuda(), check=True)
+    values, _ = seq_ref.cache_values(p.host[1], p.host[3], table, 0, 20)
+    want, mag = values.mean(1), values.abs().mean(1)
+    for h in range(2):
+        seq_ref.check(o[0, h], (want, mag * (2.0 ** -11 + 2.0 ** -20) + want.abs() * 2.0 ** -8), "o")
+    assert ((lse.double().cpu() + 2.0 ** 117).abs() <= 2.0 ** (117 - 7)).all()  # k is rounded in the cache
