@@ -312,9 +312,12 @@ typedef struct {
 } sta_window_problem;
 
 /* Workspace bytes of sta_window_forward and sta_window_backward for a problem
- * (either pointer may be NULL).  Size limits (STA_ERR_SHAPE): batch * heads *
- * q_len, batch * kv_heads * kv_len and the packed row counts times heads below
- * 2^31 - 1024. */
+ * (either pointer may be NULL).  A problem with q_rows above 0 is a packed one.
+ * Size limits (STA_ERR_SHAPE): rows times heads, batch * heads * q_len and batch *
+ * kv_heads * kv_len of a dense problem and heads * q_rows and kv_heads * kv_rows of
+ * a packed one, below 2^31 - 1024; batch * heads * (q_len / 128 + 1) and batch *
+ * kv_heads * (kv_len / 128 + 1) below 2^30; batch at most 65534, heads at most
+ * 65535, q_len and kv_len below 2^29. */
 sta_status sta_window_workspace_size(const sta_window_problem *problem, size_t *fwd_bytes, size_t *bwd_bytes);
 
 /* O = softmax(q k^T * scale over each query's visible keys) v and lse = the

@@ -14,6 +14,7 @@ namespace {
 constexpr size_t kStatusBytes = 256;
 constexpr float kLeastScale = 7.888609052210118e-31f;  // 2^-100: |LSE / scale| is finite
 constexpr long long kMaxRows = (1ll << 31) - 1024;
+constexpr long long kMaxBlocks = 1ll << 30;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 size_t round256(size_t b) { return (b + 255) & ~size_t(255); }
@@ -37,7 +38,7 @@ sta::Rows rows_of(const sta_rows *x) {
 
 bool io_type_ok(int32_t t) { return t == STA_TYPE_BF16 || t == STA_TYPE_FP16; }
 
-sta_status check_problem(const sta_window_problem *p) {
+sta_status check_problem(const sta_window_problem *p, bool packed) {
   if (!p) return STA_ERR_INVALID_ARG;
   if (p->batch < 1 || p->heads < 1 || p->kv_heads < 1 || p->q_len < 0 || p->kv_len < 0 || p->q_rows < 0 ||
       p->kv_rows < 0 || p->heads % p->kv_heads || p->batch > 65534 || p->heads > 65535)
@@ -47,17 +48,19 @@ sta_status check_problem(const sta_window_problem *p) {
   if (p->window < 0 || p->sinks < 0 || !(p->scale == p->scale) || std::isinf(p->scale)) return STA_ERR_INVALID_ARG;
   // positions reach kv_len and -q_len: kept clear of kNoWindow
   if (p->q_len >= sta::kNoWindow / 2 || p->kv_len >= sta::kNoWindow / 2) return STA_ERR_SHAPE;
-  const long long bh = (long long)p->batch * p->heads;
-  if (bh * p->q_len >= kMaxRows || (long long)p->batch * p->kv_heads * p->kv_len >= kMaxRows ||
-      (long long)p->heads * p->q_rows >= kMaxRows || (long long)p->kv_heads * p->kv_rows >= kMaxRows)
+  // rows of the tensors, and blocks of the work lists; packed sequences share
+  // their rows, so that q_len and kv_len count for the blocks only
+  const long long bh = (long long)p->batch * p->heads, bk = (long long)p->batch * p->kv_heads;
+  if ((packed ? (long long)p->heads * p->q_rows : bh * p->q_len) >= kMaxRows ||
+      (packed ? (long long)p->kv_heads * p->kv_rows : bk * p->kv_len) >= kMaxRows ||
+      bh * (p->q_len / 128 + 1) >= kMaxBlocks || bk * (p->kv_len / 128 + 1) >= kMaxBlocks)
     return STA_ERR_SHAPE;
   return STA_OK;
 }
 
 // Rows of lse and D.
-size_t stat_rows(const sta_window_problem *p) {
-  const size_t dense = (size_t)p->batch * p->heads * p->q_len, packed = (size_t)p->heads * p->q_rows;
-  return dense > packed ? dense : packed;
+size_t stat_rows(const sta_window_problem *p, bool packed) {
+  return packed ? (size_t)p->heads * p->q_rows : (size_t)p->batch * p->heads * p->q_len;
 }
 
 // Whether a forward call splits the keys over the GPU (16 query rows of a key
@@ -93,7 +96,7 @@ struct BackwardLayout {
   size_t dd, aug, norms, parts, bytes;
 };
 
-BackwardLayout backward_layout(const sta_window_problem *p) {
+BackwardLayout backward_layout(const sta_window_problem *p, bool packed) {
   constexpr long long kTargets = 2 * 148;
   BackwardLayout l{};
   auto up = [](long long n, long long m) { return (n + m - 1) / m; };
@@ -108,23 +111,27 @@ BackwardLayout backward_layout(const sta_window_problem *p) {
   l.seg_chunks = (int)(per < 0x7fffffff ? per : 0x7fffffff);
   l.norm_segs = (int)(norm > per ? up(norm, per) : 1);
   l.sink_segs = (int)(l.sink_blocks && all * group > per ? up(all * group, per) : 1);
-  const size_t rows = (size_t)p->heads * p->batch * up(p->q_len, 8) * 8;
-  const size_t packed_row = p->q_rows ? (size_t)up(p->q_rows, 8) * 8 + 8 * (size_t)p->batch + 8 : 0;
-  const size_t aug_rows = rows > packed_row * p->heads ? rows : packed_row * p->heads;
-  l.aug_rows = (int)packed_row;  // the dense form's is set by the caller
-  l.n_norms = (int)(up(p->q_len, sta::pre_rows(p->head_dim)) * p->heads * p->batch);
+  // a packed sequence begins at a multiple of 8 panel rows, and at a place of its own among the norms
+  l.aug_rows = (int)(packed ? up(p->q_rows, 8) * 8 + 8ll * p->batch + 8 : up(p->q_len, 8) * 8);
+  const size_t aug_rows = (size_t)l.aug_rows * p->heads * (packed ? 1 : p->batch);
+  const int pre = sta::pre_rows(p->head_dim);
+  l.n_norms = (int)(packed ? (p->q_rows / pre + p->batch + 1ll) * p->heads : up(p->q_len, pre) * p->heads * p->batch);
   size_t slots = 0;
   if (l.norm_segs > 1) slots = (size_t)slices * (l.sink_blocks * l.sink_segs + (nkb - l.sink_blocks) * l.norm_segs);
   else if (l.sink_segs > 1) slots = (size_t)slices * l.sink_blocks * l.sink_segs;
   l.dd = kStatusBytes;
-  l.aug = l.dd + round256(stat_rows(p) * 4);
+  l.aug = l.dd + round256(stat_rows(p, packed) * 4);
   l.norms = l.aug + (aug_rows + 128) * 32;  // a chunk reads 128 rows from any multiple of 8 on
   l.parts = l.norms + round256((size_t)l.n_norms * 4);
   l.bytes = l.parts + slots * 2 * 128 * p->head_dim * 4;
   return l;
 }
 
-size_t window_bwd_bytes(const sta_window_problem *p) { return backward_layout(p).bytes; }
+// A problem without packed rows may still be that of a packed call over empty tensors.
+size_t window_bwd_bytes(const sta_window_problem *p) {
+  const size_t packed = backward_layout(p, true).bytes, dense = p->q_rows > 0 ? 0 : backward_layout(p, false).bytes;
+  return packed > dense ? packed : dense;
+}
 
 sta::WinParams window_params(const sta_window_problem *p, const int32_t *cu_q, const int32_t *cu_kv, void *ws) {
   sta::WinParams w{};
@@ -271,7 +278,7 @@ sta_status move_call(bool write, const sta_cache *c, int32_t batch, int32_t rows
 extern "C" {
 
 sta_status sta_window_workspace_size(const sta_window_problem *p, size_t *fwd, size_t *bwd) {
-  if (const sta_status st = check_problem(p)) return st;
+  if (const sta_status st = check_problem(p, p && p->q_rows > 0)) return st;
   if (fwd) *fwd = window_fwd_bytes(p);
   if (bwd) *bwd = window_bwd_bytes(p);
   return STA_OK;
@@ -280,7 +287,7 @@ sta_status sta_window_workspace_size(const sta_window_problem *p, size_t *fwd, s
 sta_status sta_window_forward(const sta_window_problem *p, const sta_rows *q, const sta_rows *k, const sta_rows *v,
                               const sta_rows *o, float *lse, const int32_t *cu_q, const int32_t *cu_kv, void *ws,
                               size_t ws_bytes, void *stream_, uint32_t flags) {
-  if (const sta_status st = check_problem(p)) return st;
+  if (const sta_status st = check_problem(p, cu_q != nullptr)) return st;
   if (bad_window_call(flags, cu_q, cu_kv)) return STA_ERR_INVALID_ARG;
   const sta_rows *qs[] = {q, o}, *ks[] = {k, v};
   if (const sta_status st = check_tensors(p, cu_q, qs, 2, ks, 2)) return st;
@@ -308,22 +315,22 @@ sta_status sta_window_backward(const sta_window_problem *p, const sta_rows *q, c
                                const sta_rows *o, const float *lse, const sta_rows *dout, const sta_rows *dq,
                                const sta_rows *dk, const sta_rows *dv, const int32_t *cu_q, const int32_t *cu_kv,
                                void *ws, size_t ws_bytes, void *stream_, uint32_t flags) {
-  if (const sta_status st = check_problem(p)) return st;
+  if (const sta_status st = check_problem(p, cu_q != nullptr)) return st;
   if (bad_window_call(flags, cu_q, cu_kv) || !lse) return STA_ERR_INVALID_ARG;
   if (p->scale > 0.f && p->scale < kLeastScale) return STA_ERR_INVALID_ARG;
   const sta_rows *qs[] = {q, o, dout, dq}, *ks[] = {k, v, dk, dv};
   if (const sta_status st = check_tensors(p, cu_q, qs, 4, ks, 4)) return st;
-  if (const sta_status st = check_workspace(ws, ws_bytes, window_bwd_bytes(p))) return st;
+  const BackwardLayout l = backward_layout(p, cu_q != nullptr);
+  if (const sta_status st = check_workspace(ws, ws_bytes, l.bytes)) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   sta::WinParams w = window_params(p, cu_q, cu_kv, ws);
   w.q = rows_of(q), w.k = rows_of(k), w.v = rows_of(v), w.o = rows_of(o), w.dout = rows_of(dout);
   w.dq = rows_of(dq), w.dk = rows_of(dk), w.dv = rows_of(dv);
   w.lse = const_cast<float *>(lse);
   w.zero = (flags & STA_PACKED_ZERO) != 0;
-  const BackwardLayout l = backward_layout(p);
   char *base = static_cast<char *>(ws);
   w.dd = reinterpret_cast<float *>(base + l.dd);
-  w.aug = reinterpret_cast<uint8_t *>(base + l.aug), w.aug_rows = cu_q ? l.aug_rows : (p->q_len + 7) / 8 * 8;
+  w.aug = reinterpret_cast<uint8_t *>(base + l.aug), w.aug_rows = l.aug_rows;
   w.norms = reinterpret_cast<float *>(base + l.norms), w.n_norms = l.n_norms;
   w.parts = reinterpret_cast<float *>(base + l.parts);
   w.seg_chunks = l.seg_chunks, w.sink_blocks = l.sink_blocks, w.sink_segs = l.sink_segs, w.norm_segs = l.norm_segs;

@@ -193,7 +193,12 @@ __global__ void __launch_bounds__(256) window_pre_kernel(const WinParams p) {
     const int most = __reduce_max_sync(0xffffffffu, counts ? __float_as_int(sqrtf(sq)) : 0);
     if (lane == 0) atomicMax(&top, most);  // nonnegative floats order like integers
     __syncthreads();
-    if (threadIdx.x == 0) p.norms[((long long)b * p.heads + h) * gridDim.x + blockIdx.x] = __int_as_float(top);
+    if (threadIdx.x == 0) {
+      if (!p.cu_q) p.norms[((long long)b * p.heads + h) * gridDim.x + blockIdx.x] = __int_as_float(top);
+      // packed: of the rows that are there; the others have been zeroed
+      else if ((int)blockIdx.x * pre_rows(D) < s.nq)
+        p.norms[(long long)h * (p.n_norms / p.heads) + s.q0 / pre_rows(D) + b + blockIdx.x] = __int_as_float(top);
+    }
   }
 }
 
@@ -1110,6 +1115,8 @@ cudaError_t launch(const WinParams &p, const CUtensorMap *m, cudaStream_t stream
   if (const cudaError_t e = allow_shared(window_dkdv_kernel<D, T>, (int)K::kSmem, done_kv)) return e;
   if (const cudaError_t e = allow_shared(window_dq_kernel<D, T>, (int)Q::kSmem, done_q)) return e;
   const int nqb = (p.q_len + kBM - 1) / kBM, nkb = (p.kv_len + kBM - 1) / kBM, slices = p.batch * p.kv_heads;
+  if (kIsHalf<T> && p.cu_q)
+    if (const cudaError_t e = cudaMemsetAsync(p.norms, 0, (size_t)p.n_norms * 4, stream)) return e;
   if (nqb > 0)
     window_pre_kernel<D, T>
         <<<dim3((p.q_len + pre_rows(D) - 1) / pre_rows(D), p.heads, p.batch + p.zero), 256, 0, stream>>>(p);

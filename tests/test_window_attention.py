@@ -462,6 +462,27 @@ def test_bad_problems_are_refused(kw, status):
     assert sta.lib().sta_window_workspace_size(ctypes.byref(problem(**kw)), ctypes.byref(n), None) == status
 
 
+def test_packed_sizes_follow_the_rows_that_are_there():
+    """Bounds of all rows (none given) on many sequences: neither the workspace
+    nor the limits grow with sequences times rows."""
+    def size(**kw):
+        n = ctypes.c_size_t()
+        p = problem(heads=24, kv_heads=8, head_dim=128, window=256, sinks=0, q_rows=131072, kv_rows=131072, **kw)
+        assert sta.lib().sta_window_workspace_size(ctypes.byref(p), None, ctypes.byref(n)) == 0
+        return n.value
+
+    bounded, free = size(batch=256, q_len=512, kv_len=512), size(batch=256, q_len=131072, kv_len=131072)
+    # 36 bytes a row and head for the panel and D, and no more than what the parts of 300 key blocks take
+    assert bounded <= free <= 24 * 131072 * 40 + 300 * 2 * 128 * 128 * 4
+    assert size(batch=700, q_len=131072, kv_len=131072) < 2 ** 28
+    # a dense call whose problem has packed rows needs the dense form's workspace
+    p, n = problem(head_dim=128, q_len=4096, kv_len=4096, q_rows=8, kv_rows=8), ctypes.c_size_t()
+    assert sta.lib().sta_window_workspace_size(ctypes.byref(p), None, ctypes.byref(n)) == 0
+    row = sta._Rows(4096, 4096 * 512, 4096 * 128, 128)
+    assert sta.lib().sta_window_backward(ctypes.byref(p), row, row, row, row, 4096, row, row, row, row, None, None, 4096,
+                                         4 * 4096 * 36, None, 0) == 5
+
+
 def test_bad_calls_are_refused_before_anything_is_enqueued():
     L, p = sta.lib(), problem()
     n = ctypes.c_size_t()
@@ -738,3 +759,21 @@ def test_scores_far_below_zero(heads, kv_heads, nq, nk):
     want, mag = p @ vv, p @ vv.abs()
     seq_ref.check(o[0], (want, mag * (2.0 ** -8 + 2.0 ** -20) + want.abs() * 2.0 ** -8), "o")
     assert ((lse.double().cpu() + 2.0 ** 117).abs() <= 2.0 ** (117 - 20)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+def test_many_short_documents_without_bounds(dtype):
+    """Sequences times rows times heads past 2^31."""
+    n, each, heads, d = 2000, 35, 16, 64
+    q, k, v, do, cu, _ = packed([each] * n, [each] * n, heads, 2, d, dtype, tail=0, seed=5)
+    qd, kd, vd, dod, cd = (t.cuda() for t in (q, k, v, do, cu))
+    o, lse = window_forward(qd, kd, vd, 20, 2, cu_q=cd, cu_kv=cd, check=True)
+    got = dict(zip(("dq", "dk", "dv"), window_backward(qd, kd, vd, o, lse, dod, 20, 2, cu_q=cd, cu_kv=cd, check=True)), o=o, lse=lse)
+    mask = seq_ref.mask_of(each, each, 20, 2)
+    top = float(do.double().norm(dim=-1).max())
+    for b in (0, 1, 777, 1998, 1999):
+        r = slice(b * each, (b + 1) * each)
+        want = seq_ref.attention(q[0, :, r], k[0, :, r], v[0, :, r], mask, d ** -0.5, do[0, :, r], dtype, top)
+        for name, t in got.items():
+            seq_ref.check(t[0, :, r], want[name], f"{name} of sequence {b}")
