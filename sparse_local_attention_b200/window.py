@@ -17,6 +17,7 @@ from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.utils.weak import WeakTensorKeyDictionary
 
 from .sta import STA_CALL_CHECK, _check, _Rows, lib
 
@@ -307,6 +308,11 @@ def window_backward(q, k, v, o, lse, dout, window: int = 0, sinks: int = 0, scal
                          workspace, check)
 
 
+# The graphs that each leaf is used in, as (stream, weak reference).  Beside the
+# leaves and not on them, so that they are saved and copied without it.
+_uses = WeakTensorKeyDictionary()
+
+
 def _note_use(ctx, leaf: torch.Tensor, stream: int):
     """Remember that the graph of `ctx` was built on `stream` over a leaf.
 
@@ -314,12 +320,12 @@ def _note_use(ctx, leaf: torch.Tensor, stream: int):
     leaf was first used for as long as a graph of that use lives.  A backward
     pass captured on another stream would have to join that stream, which ends
     the capture and the process, so such a capture is refused."""
-    uses = [u for u in getattr(leaf, "_sta_uses", ()) if u[1]() is not None]
+    uses = [u for u in _uses.get(leaf, ()) if u[1]() is not None]
     if torch.cuda.is_current_stream_capturing() and any(u[0] != stream for u in uses):
         raise RuntimeError("sliding_window_attention: an eager graph of the same leaf tensors is still alive; release "
                            "it (and its outputs) before capturing, or capture on detached leaves")
     uses.append((stream, weakref.ref(ctx)))
-    leaf._sta_uses = uses
+    _uses[leaf] = uses
 
 
 class _SlidingWindowAttention(torch.autograd.Function):

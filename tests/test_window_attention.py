@@ -777,3 +777,25 @@ def test_many_short_documents_without_bounds(dtype):
         want = seq_ref.attention(q[0, :, r], k[0, :, r], v[0, :, r], mask, d ** -0.5, do[0, :, r], dtype, top)
         for name, t in got.items():
             seq_ref.check(t[0, :, r], want[name], f"{name} of sequence {b}")
+
+
+@pytest.mark.gpu
+def test_leaves_keep_nothing_of_the_calls():
+    """A leaf can be saved, loaded and copied after a call, and a copy is not
+    held back by the graphs of the one it was copied from."""
+    import copy
+    import io
+    leaves = [t.cuda().requires_grad_() for t in make(2, 2, 64, 64, 64, BF16)[:3]]
+    before = [dict(t.__dict__) for t in leaves]
+    alive = sliding_window_attention(*leaves, 16, 2)
+    assert [dict(t.__dict__) for t in leaves] == before
+    file = io.BytesIO()
+    torch.save(leaves, file)
+    file.seek(0)
+    assert all(torch.equal(a, b) for a, b in zip(torch.load(file, weights_only=True), leaves))
+    copies = copy.deepcopy(leaves)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        out = sliding_window_attention(*copies, 16, 2)
+        torch.autograd.grad(out, copies, torch.ones_like(out))
+    assert alive.requires_grad
