@@ -16,6 +16,7 @@ from dataclasses import dataclass, field
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _build
 
@@ -495,6 +496,12 @@ def _per_head(windows, heads: int):
     return tuple(tuple(int(x) for x in w) for w in windows)
 
 
+def refuse_tangents(name: str, *tensors):
+    """Forward-mode derivatives would be dropped silently: raise instead."""
+    if any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"{name}: forward-mode derivatives are not implemented")
+
+
 def sliding_tile_attention(q, k, v, T, H, W, tile, windows, scale=0.0):
     """Sliding Tile Attention of bf16 [batch, heads, T*H*W, d] tensors in
     raster token order; returns O (same shape).  `windows`: one (w_t, w_h, w_w)
@@ -502,6 +509,7 @@ def sliding_tile_attention(q, k, v, T, H, W, tile, windows, scale=0.0):
     requires a gradient, the backward runs sta_backward.  The plan comes from
     a small cache keyed by the problem, so repeated calls do not rebuild it.
     Non-contiguous inputs are made contiguous first."""
+    refuse_tangents("sliding_tile_attention", q, k, v)
     B, Hh, N, d = q.shape
     if N != T * H * W:
         raise ValueError(f"token count {N} != T*H*W = {T * H * W}")

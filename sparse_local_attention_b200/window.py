@@ -19,7 +19,7 @@ import torch
 from torch.autograd.function import once_differentiable
 from torch.utils.weak import WeakTensorKeyDictionary
 
-from .sta import STA_CALL_CHECK, _check, _Rows, lib
+from .sta import STA_CALL_CHECK, _check, _Rows, lib, refuse_tangents
 
 STA_PACKED_ZERO = 0x4
 STA_TYPE_BF16, STA_TYPE_FP16, STA_TYPE_E4M3, STA_TYPE_INT8 = 0, 1, 2, 3
@@ -360,6 +360,7 @@ def sliding_window_attention(q, k, v, window: int = 0, sinks: int = 0, scale: fl
     """window_forward's o, differentiable: when q, k or v requires a gradient
     the backward is one sta_window_backward call.  Shared key heads and
     broadcast inputs get the sum of their gradients."""
+    refuse_tangents("sliding_window_attention", q, k, v)
     args = (window, sinks, scale, cu_q, cu_kv, max_q, max_kv)
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, v)):
         device = _device_of(q)

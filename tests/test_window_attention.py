@@ -512,6 +512,19 @@ def test_a_scale_too_small_for_gradients_is_refused():
                                      None, 0) == status
 
 
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_forward_mode_derivatives_are_refused(at):
+    """A tangent would be dropped silently."""
+    import torch.autograd.forward_ad as forward_ad
+    x = [torch.zeros(1, 2, 8, 64, dtype=BF16) for _ in range(3)]
+    with forward_ad.dual_level():
+        x[at] = forward_ad.make_dual(x[at], torch.ones_like(x[at]))
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            sliding_window_attention(*x, 4)
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            sta.sliding_tile_attention(*x, 2, 2, 2, (1, 1, 1), (1, 1, 1))
+
+
 def test_binding_refusals():
     q = torch.zeros(1, 2, 8, 64, dtype=BF16)
     with pytest.raises(ValueError, match="CUDA"):
