@@ -16,6 +16,20 @@ from .window import (IO_TYPES, STA_TYPE_E4M3, STA_TYPE_INT8, _at, _current_strea
 
 STA_READ_ZERO = 0x2
 CACHE_TYPES = {torch.float8_e4m3fn: STA_TYPE_E4M3, torch.int8: STA_TYPE_INT8}
+BLOCKS, HEAD_DIMS = (16, 32, 64, 128), (64, 128)
+
+
+def _check_sizes(pages: int, kv_heads: int, page_size: int, head_dim: int, block: int):
+    """The sizes that the calls take."""
+    if head_dim not in HEAD_DIMS:
+        raise ValueError(f"head_dim: expected 64 or 128, got {head_dim}")
+    if block not in BLOCKS:
+        raise ValueError(f"block: expected 16, 32, 64 or 128 tokens per scale, got {block}")
+    if page_size < 1 or page_size % block:
+        raise ValueError(f"block {block} does not divide page_size {page_size}")
+    if pages < 1 or not 1 <= kv_heads <= 65535 or pages * page_size >= 2 ** 31:
+        raise ValueError(f"expected pages and kv_heads (up to 65535) above 0 and pages * page_size below 2^31, got {pages} "
+                         f"pages of {page_size} tokens and {kv_heads} heads")
 
 
 class _Cache(ctypes.Structure):
@@ -32,14 +46,14 @@ class KVCache:
     Sequences own pages through a page table (int32 [batch, table_pages], the
     page of each page_size tokens; entries outside [0, pages) are absent pages),
     which the caller keeps, as well as the number of tokens of each sequence.
+    head_dim: 64 or 128; block: 16, 32, 64 or 128, a divisor of page_size.
     One call may not write a page for two sequences, nor twice for one."""
 
     def __init__(self, pages: int, kv_heads: int, page_size: int, head_dim: int, block: int = 64,
                  dtype: torch.dtype = torch.float8_e4m3fn, device="cuda"):
         if dtype not in CACHE_TYPES:
             raise ValueError(f"dtype: expected float8_e4m3fn or int8, got {dtype}")
-        if block < 1 or page_size % block:
-            raise ValueError(f"block {block} does not divide page_size {page_size}")
+        _check_sizes(pages, kv_heads, page_size, head_dim, block)
         codes, scales = (pages, kv_heads, page_size, head_dim), (pages, kv_heads, page_size // block)
         zeros = [torch.zeros(codes, dtype=torch.uint8, device=device).view(dtype) for _ in range(2)]
         self._take(*zeros, *(torch.zeros(scales, dtype=torch.float32, device=device) for _ in range(2)))
@@ -52,6 +66,9 @@ class KVCache:
         return self
 
     def _take(self, k, v, k_scale, v_scale):
+        for t, name in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
         if k.dim() != 4 or k_scale.dim() != 3 or k.dtype not in CACHE_TYPES or not k.is_cuda:
             raise ValueError(f"k: expected float8_e4m3fn or int8 [pages, kv_heads, page_size, head_dim] on a CUDA "
                              f"device and 3-dimensional scales, got {k.dtype} {tuple(k.shape)} on {k.device}")
@@ -59,10 +76,14 @@ class KVCache:
         blocks = k_scale.shape[2]
         if blocks < 1 or page_size % blocks:
             raise ValueError(f"k_scale: {blocks} blocks in a page of {page_size} tokens")
+        _check_sizes(pages, kv_heads, page_size, head_dim, page_size // blocks)
         _flat(k, "k", k.shape, k.dtype, k.device)
         _flat(v, "v", k.shape, k.dtype, k.device)
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             _flat(t, name, (pages, kv_heads, blocks), torch.float32, k.device)
+        for t, name in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t.data_ptr() & 15:
+                raise ValueError(f"{name}: expected a 16-byte aligned tensor")
         self._tensors = k, v, k_scale, v_scale  # whose addresses _c holds
         self.pages, self.kv_heads, self.page_size, self.head_dim = pages, kv_heads, page_size, head_dim
         self.block, self.dtype, self.device = page_size // blocks, k.dtype, k.device
@@ -139,7 +160,8 @@ class KVCache:
         """(o, lse) of the last Nq positions of each sequence over its cached
         tokens: q [batch, heads, Nq, d], lengths int32 [batch] tokens in the
         cache, the queries' own among them.  The visible keys are those of
-        window_forward with Nk = lengths[b]."""
+        window_forward with Nk = lengths[b].  Not differentiable: o carries no
+        gradient of a q that requires one."""
         if not isinstance(q, torch.Tensor) or q.dtype not in IO_TYPES or q.dim() != 4:
             raise ValueError("q: expected bfloat16 or float16 [batch, heads, rows, head_dim]")
         batch, heads, nq, _ = q.shape

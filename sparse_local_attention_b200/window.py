@@ -283,7 +283,8 @@ def window_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: in
     q [batch, heads, Nq, d], k and v [batch, kv_heads, Nk, d], bf16 or fp16, d
     64 or 128, kv_heads a divisor of heads; query row i sits at position
     i + Nk - Nq.  window 0: no limit.  Any strides with contiguous, 16-byte
-    aligned rows are read in place; other inputs are copied first.
+    aligned rows are read in place; other inputs are copied first.  Not
+    differentiable by itself: sliding_window_attention is.
 
     Packed sequences: a batch of 1 whose rows [cu[b], cu[b + 1]) hold sequence
     b (cu_q, cu_kv: int32 device tensors); max_q and max_kv are bounds on the

@@ -334,6 +334,33 @@ def test_binding_refusals():
         KVCache(2, 2, 32, 64, block=16, dtype=BF16, device="cpu")
 
 
+@pytest.mark.parametrize("kw", [dict(block=8), dict(block=48, page_size=96), dict(block=256, page_size=256), dict(head_dim=96),
+                                dict(head_dim=0), dict(pages=0), dict(kv_heads=0), dict(page_size=0),
+                                dict(pages=2 ** 20, page_size=2 ** 12)], ids=str)
+def test_caches_that_no_call_takes_are_refused(kw):
+    """Before anything is allocated."""
+    with pytest.raises(ValueError) as e:
+        KVCache(**{**dict(pages=2, kv_heads=2, page_size=32, head_dim=64, block=16, device="meta"), **kw})
+    assert "on meta" not in str(e.value)  # the sizes, not the device of tensors that were made
+
+
+@pytest.mark.gpu
+def test_tensors_that_no_call_takes_are_refused():
+    make = lambda *shape: torch.zeros(shape, dtype=INT8, device="cuda")  # noqa: E731
+    scales = lambda *shape: torch.zeros(shape, device="cuda")  # noqa: E731
+    for codes, blocks in (((2, 2, 32, 96), 2), ((2, 2, 32, 64), 4), ((0, 2, 32, 64), 2), ((2, 2, 48, 64), 1)):
+        k, s = make(*codes), scales(*codes[:2], blocks)
+        with pytest.raises(ValueError):
+            KVCache.from_tensors(k, k.clone(), s, s.clone())
+    k, s = make(2, 2, 32, 64), scales(2, 2, 2)
+    for args in ((k, None, s, s), (k, k, None, s), (k, k, s, None), (None, k, s, s)):
+        with pytest.raises((TypeError, ValueError)):
+            KVCache.from_tensors(*args)
+    odd = torch.zeros(2 * 2 * 32 * 64 + 1, dtype=INT8, device="cuda")[1:].view(2, 2, 32, 64)
+    with pytest.raises(ValueError):
+        KVCache.from_tensors(odd, k, s, s)
+
+
 @pytest.mark.gpu
 def test_binding_refusals_on_device():
     c = KVCache(4, 2, 32, 64, block=16)
