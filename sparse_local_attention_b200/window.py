@@ -190,6 +190,8 @@ class _Call:
         else:
             rows = (0, 0)
         self.empty = 0 in self.q_shape or (self.packed and batch == 0)
+        if self.empty and d not in (64, 128):  # other calls learn it from the library
+            raise ValueError(f"q: expected a head_dim of 64 or 128, got {d}")
         # no key rows: queries see nothing.  The packed form still has to tell
         # the rows of its sequences from the rest, over a key row that none owns.
         self.no_keys = 0 in self.kv_shape

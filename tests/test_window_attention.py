@@ -812,3 +812,15 @@ def test_leaves_keep_nothing_of_the_calls():
         out = sliding_window_attention(*copies, 16, 2)
         torch.autograd.grad(out, copies, torch.ones_like(out))
     assert alive.requires_grad
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [0, 32])
+def test_empty_tensors_of_other_head_dims_are_refused(d):
+    """Without rows or columns nothing is computed, so nothing else would say so."""
+    for shape in ((1, 2, 3, d), (1, 2, 0, d)):
+        if shape[2] and d:
+            continue
+        q = torch.zeros(shape, dtype=BF16, device="cuda")
+        with pytest.raises(ValueError, match="head_dim"):
+            window_forward(q, q, q, 4)
