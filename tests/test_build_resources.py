@@ -9,6 +9,7 @@ import os
 import re
 import shutil
 import subprocess
+import sys
 from concurrent.futures import ThreadPoolExecutor
 
 import pytest
@@ -69,3 +70,20 @@ def test_kernel_register_budgets(tmp_path):
         assert regs <= cap, (mangled, regs)
 
 
+def test_token_sequence_kernel_budgets(tmp_path, monkeypatch):
+    """The tile kernels and the split form fill the registers that their launches
+    allow: a limit on the bytes that each spills (stores and loads), none for the
+    other kernels of the token sequences."""
+    most = {"window_fwd_kernel": 340, "window_dkdv_kernel": 48, "window_dq_kernel": 24, "split_attn_kernel": 12,
+            "window_clear_kernel": 0, "window_pre_kernel": 0, "window_join_kernel": 0, "cache_write_kernel": 0,
+            "cache_read_kernel": 0}
+    monkeypatch.setattr(sys.modules[__name__], "KERNELS", tuple(most))
+    res = _resources(tmp_path)
+    for k, limit in most.items():
+        assert k in res, f"{k}: no ptxas report"
+        for mangled, regs, spill in res[k]:
+            if k == "window_fwd_kernel" and "Lb0E" in mangled:
+                limit_here = 0  # two blocks share their keys: the form of large calls
+            else:
+                limit_here = limit
+            assert spill <= limit_here, f"{k} ({mangled}) spills {spill} bytes"
