@@ -17,7 +17,6 @@ from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
-from torch.utils.weak import WeakTensorKeyDictionary
 
 from .sta import STA_CALL_CHECK, _check, _Rows, lib, refuse_tangents
 
@@ -311,34 +310,33 @@ def window_backward(q, k, v, o, lse, dout, window: int = 0, sinks: int = 0, scal
                          workspace, check)
 
 
-# The graphs that each leaf is used in, as (stream, weak reference).  Beside the
-# leaves and not on them, so that they are saved and copied without it.
-_uses = WeakTensorKeyDictionary()
+# The live graphs, each of which notes its stream and its leaves (by identity: it
+# keeps them alive).  Nothing is kept on the leaves, which are saved and copied.
+_graphs = weakref.WeakSet()
 
 
-def _note_use(ctx, leaf: torch.Tensor, stream: int):
-    """Remember that the graph of `ctx` was built on `stream` over a leaf.
+def _note_uses(ctx, tensors, stream: int):
+    """Remember that the graph of `ctx` was built on `stream` over these leaves.
 
     A gradient that is accumulated into a leaf runs on the stream on which the
     leaf was first used for as long as a graph of that use lives.  A backward
     pass captured on another stream would have to join that stream, which ends
     the capture and the process, so such a capture is refused."""
-    uses = [u for u in _uses.get(leaf, ()) if u[1]() is not None]
-    if torch.cuda.is_current_stream_capturing() and any(u[0] != stream for u in uses):
+    leaves = {id(t) for t, needed in zip(tensors, ctx.needs_input_grad) if needed and t.is_leaf}
+    if not leaves:
+        return
+    if torch.cuda.is_current_stream_capturing() and any(g.stream != stream and g.leaves & leaves for g in _graphs):
         raise RuntimeError("sliding_window_attention: an eager graph of the same leaf tensors is still alive; release "
                            "it (and its outputs) before capturing, or capture on detached leaves")
-    uses.append((stream, weakref.ref(ctx)))
-    _uses[leaf] = uses
+    ctx.stream, ctx.leaves = stream, leaves
+    _graphs.add(ctx)
 
 
 class _SlidingWindowAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, args):
         with _on(q.device, None):
-            stream = _current_stream(q.device)
-            for t, needed in zip((q, k, v), ctx.needs_input_grad):
-                if needed and t.is_leaf:
-                    _note_use(ctx, t, stream)
+            _note_uses(ctx, (q, k, v), _current_stream(q.device))
             c = _Call(q, k, v, *args)
             o, lse = _forward(c)
         # autograd's to keep, to let go after the backward, and to refuse where
