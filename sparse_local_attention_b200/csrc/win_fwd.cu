@@ -57,10 +57,11 @@ struct Item {
   int n0;                     // split: chunks [0, n0) are warpgroup 0's, [n0, nc) warpgroup 1's
   __device__ __forceinline__ int begin(int x) const { return x ? n0 : 0; }
   __device__ __forceinline__ int end(int x) const { return x ? nc : n0; }
+  template <bool kSplit>
   __device__ __forceinline__ void chunk(int j, int &first, int &valid) const {
     first = j < ns ? j * kBM : base + (j - ns) * kBM;
     valid = min(kBM, (j < ns ? nsink : edge) - first);
-    if (j == gap || j == tail) {
+    if (!kSplit && (j == gap || j == tail)) {
       first = j == gap ? nsink : edge;
       valid = (j == gap ? base + kBM : past) - first;
     }
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items;
         ok = for_loads<kSplit>(it, [&](int, int c, bool is_v) {
           int first, valid;
-          it.chunk(c, first, valid);
+          it.chunk<kSplit>(c, first, valid);
           const uint32_t slot = ld % C::kSlots, phase = (ld / C::kSlots) & 1, bit = 1u << slot;
           if (!mbar_wait(&empty[slot], phase ^ 1, ctl, kErrWaitProducer)) return false;
           const bool clear = is_v && valid % 16 != 0;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = for_loads<kSplit>(it, [&](int, int c, bool is_v) {
         const uint32_t slot = l++ % C::kSlots;
         int first, valid;
-        it.chunk(c, first, valid);
+        it.chunk<kSplit>(c, first, valid);
         if (!is_v || valid % 16 == 0) return true;
         if (!mbar_wait_w(&raw[slot], raw_par >> slot & 1, ctl, kErrWaitProducer)) return false;
         raw_par ^= 1u << slot;
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!kSplit) {
         if (!wait_slot(k0)) { ok = false; break; }
         int first, valid;
-        it.chunk(0, first, valid);
+        it.chunk<kSplit>(0, first, valid);
         bool act[2] = {sees(it, 0, first, valid, p.sinks), sees(it, 1, first, valid, p.sinks)};
         issued = true;
 #pragma unroll
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t vj = k0 + 2 * j + 1, kn = vj + 1;
           const bool more = j + 1 < it.nc;
           const int steps = (valid + 15) / 16;
-          it.chunk(j + 1, first, valid);
+          it.chunk<kSplit>(j + 1, first, valid);
           const bool next[2] = {more && sees(it, 0, first, valid, p.sinks), more && sees(it, 1, first, valid, p.sinks)};
           if (!wait_slot(vj) || (more && !wait_slot(kn))) { ok = false; break; }
   #pragma unroll
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c = it.begin(x) + j;
             if (c >= it.end(x)) continue;
             int first, valid;
-            it.chunk(c, first, valid);
+            it.chunk<kSplit>(c, first, valid);
             const uint32_t vl = l++;
             // the next K, too, while the softmax works
             if (!wait_slot(vl) || (c + 1 < it.end(x) && !wait_slot(l)) || !attend(x, vl % C::kSlots, (valid + 15) / 16)) {
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool seen = false;
       for (int j = kSplit ? it.begin(x) : 0; j < (kSplit ? it.end(x) : it.nc); ++j) {
         int first, valid;
-        it.chunk(j, first, valid);
+        it.chunk<kSplit>(j, first, valid);
         if (!kSplit && !sees(it, x, first, valid, p.sinks)) continue;
         // whole: every row of the unit sees all 128 keys
         const int pos0 = it.pos0[u];
