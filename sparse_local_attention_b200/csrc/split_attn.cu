@@ -1,7 +1,7 @@
 // split_attn.cu -- attention of a few query rows: the keys are split over the
 // warps of a thread block cluster and the parts joined through its shared
-// memory.  Serves attention over the 8-bit cache and the single-token form of
-// sliding-window attention.
+// memory.  Serves attention over the 8-bit cache and sliding-window attention of few
+// query rows (up to 256 of a key head, by the rule beside its call).
 //
 // For each query row i with visible keys j: O_i = sum_j P_ij V_j / sum_j P_ij,
 // P_ij = 2^(s_ij - m_i).  The query rows of one key head (group x q_len of them,
@@ -18,11 +18,12 @@
 // which the matrix instructions take.
 //
 // With one row per sequence the bound is reading the keys: 64 sequences up to
-// 8192 tokens, 8 key heads, d 128, e4m3: 117 us for 0.70 GB, 6.0 TB/s (91% of a
-// copy's rate).  With 16 rows and d 64 it is the instructions of a step, some 300
-// per warp, most of them the widening of the codes and the softmax (32 sequences x
-// 4 tokens, 16 heads over 4, window 4096, int8: 30 us for 68 MB).  Small calls are
-// latency: 8 us for one token of one sequence over 1031.
+// 8192 tokens, 8 key heads, d 128, e4m3: 121 us for 0.70 GB, 5.8 TB/s (89% of a
+// copy's rate; 118 us with one maximum for P and P s).  With 16 rows and d 64 it is
+// the latency of a step, one chain of some 300 instructions per warp, most of them
+// the widening of the codes and the softmax, on 14 -- 16 warps per SM (32 sequences x
+// 4 tokens, 16 heads over 4, window 4096, int8: 31 us for 68 MB, with the issue slots
+// 44% busy).  Small calls are latency: 8 us for one token of one sequence over 1031.
 #include <cooperative_groups.h>
 
 #include "seq_common.cuh"
@@ -677,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, SplitCfg<D, NT, Keys>::kCtas)
 // once, with a step for each warp; and twice that where the slices are no more
 // than the GPU holds and each warp is left 16 steps.  Measured with 1 / 2 / 4 / 8
 // / 16 blocks, in us (* chosen):
-//   1 x 1031 tokens, d 128, cache:              14.0  11.4   9.4   8.5   8.6*
+//   1 x 1031 tokens, d 128, cache:              14.0  11.4   9.4   8.5*  8.6
 //   1 x 8192, 16 heads over 4, d 128, bf16:     63.4  36.7  22.3  15.6  12.2*
 //   8 x 1024, 24 heads over 8, d 128, bf16:     14.5  12.3* 18.5  36.2  63.4
 //   32 x 4096, 4 key heads, d 64, cache:        41.0  32.0* 40.0  57.6   111

@@ -28,9 +28,11 @@
 //
 // P and dS are rounded to the tensors' type, the precision of the tensor
 // core's A operand.  fp16 has 5 exponent bits: P is held times 2^8 and dS times
-// a power of two near 4 / max_i |dO_i|, so that neither falls below its normal
-// range where it matters (|dS| <= 2 |dO_i| |V_j|: rows of V up to a norm of 8192
-// do not overflow).  D is taken from O as it was stored, in the tensors' type.
+// a power of two near 4 / max_i |dO_i| over the finite rows that see a key, so that
+// neither falls below its normal range where it matters (|dS| <= 2 |dO_i| |V_j|:
+// rows of V up to a norm of 8192 do not overflow).  D is taken from O as it was
+// stored, in the tensors' type; -LSE and -D enter as three bf16 numbers each, which
+// keep fp32's precision and range.
 //
 // Measured on a B200, in us: 2 x 4096 tokens, 16 heads, d 64, window 512: 149;
 // 8192 tokens, 24 heads, d 128, window 2048: 706 (0.64 PFLOP/s over the visible

@@ -33,8 +33,11 @@
 // Bound by the chain of a chunk pair, S -> softmax -> P V, of which the two units
 // hide each other's: about 3900 cycles at head dim 128 (the products alone take
 // 2100), and 1.5 pairs more for an item's start and end.  8192 tokens, 24 heads,
-// d 128: without a window 410 us (1.0 PFLOP/s, 60% of a library product's rate),
-// window 2048 222 us (0.81); window 512, d 64, 2 x 4096 tokens, 16 heads: 60 us.
+// d 128: without a window 414 us (1.0 PFLOP/s, 60% of a library product's rate),
+// window 2048 224 us (0.80); window 512, d 64, 2 x 4096 tokens, 16 heads: 61 us.
+// (A V of its own for each unit in the chunks that they see different keys of took
+// 64 us there, and 150 us instead of 145 for 8192 tokens with a window of 1024,
+// where chunks of their own cost 0 -- 2%.)
 #include "seq_tile.cuh"
 
 namespace sta {
