@@ -327,10 +327,12 @@ sta_status sta_window_workspace_size(const sta_window_problem *problem, size_t *
  *   cu_q, cu_kv: NULL for the dense form.  Packed form: both device arrays of
  * batch + 1 int32; sequence b is rows [cu[b], cu[b + 1]) of every head, at
  * most q_len / kv_len of them, inside [0, q_rows) / [0, kv_rows) (what lies
- * outside is dropped).  Rows of o and lse outside every sequence are not
- * written, or become zeros and -inf with STA_PACKED_ZERO in flags.  Calls of few query rows (a rule on the problem's sizes alone) split
- * the keys over the GPU and join the parts; the others run on the tensor
- * cores' 128-row tiles. */
+ * outside is dropped).  The starts ascend: results of rows that two sequences
+ * hold are undefined.  Rows of o and lse outside every sequence are not written,
+ * or become zeros and -inf with STA_PACKED_ZERO in flags.
+ *   Calls of few query rows (a rule on the problem's sizes alone) split the keys
+ * over the GPU and join the parts; the others run on the tensor cores' 128-row
+ * tiles. */
 #define STA_PACKED_ZERO 0x4u
 sta_status sta_window_forward(const sta_window_problem *problem, const sta_rows *q, const sta_rows *k,
                               const sta_rows *v, const sta_rows *o, float *lse, const int32_t *cu_q,

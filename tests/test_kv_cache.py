@@ -485,8 +485,8 @@ def attend_unequal(p, table, lens, q, window, sinks, **kw):
         want = seq_ref.attention(q[b], k, v, mask, q.shape[3] ** -0.5)
         kd, vd, sd = (t.repeat_interleave(g, 0) for t in (k, v, scale))
         x = (q[b].double() @ kd.mT * q.shape[3] ** -0.5).masked_fill(~mask, float("-inf"))
-        w = torch.softmax(x, -1).nan_to_num(0.0) * sd[:, None]
-        floor = 2.0 ** -32 * w.amax(-1, keepdim=True) * ((mask / sd[:, None].clamp_min(2.0 ** -100)) @ vd.abs())
+        w = torch.softmax(x, -1).nan_to_num(0.0) * sd.abs()[:, None]
+        floor = 2.0 ** -32 * w.amax(-1, keepdim=True) * ((mask / sd.abs()[:, None].clamp_min(2.0 ** -100)) @ vd.abs())
         o_want, o_bound = want["o"]
         o_bound = o_bound + (seq_ref.unit(q.dtype) - seq_ref.unit(BF16)) * o_want.abs() + floor
         seq_ref.check(o[b], (o_want, o_bound), f"o of sequence {b}")
@@ -546,3 +546,27 @@ def test_scores_far_below_zero(fmt):
     for h in range(2):
         seq_ref.check(o[0, h], (want, mag * (2.0 ** -11 + 2.0 ** -20) + want.abs() * 2.0 ** -8), "o")
     assert ((lse.double().cpu() + 2.0 ** 117).abs() <= 2.0 ** (117 - 7)).all()  # k is rounded in the cache
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [E4M3, INT8], ids=["e4m3", "int8"])
+@pytest.mark.parametrize("q_len,d,lens", [(1, 128, [300]), (6, 64, [300]), (1, 64, [3000])])
+def test_scales_of_zero_of_either_sign_and_far_apart(fmt, q_len, d, lens):
+    """Pages never written (scale 0), blocks of zeros (2^-100), scales below zero
+    and of 2^30 beside one another, in any order."""
+    per = -(-lens[0] // 32)
+    table, pages = tables(1, per, seed=9)
+    p = Pair(pages, 2, 32, d, 16, fmt)
+    q = randn(1, 4, q_len, d, seed=90, dtype=BF16)
+    o, lse = attend_unequal(p, table, lens, q, 0, 0)  # a new cache: zeros with equal weights
+    assert not o.any()
+    k, v = (randn(1, 2, lens[0], d, seed=91 + i, dtype=BF16) for i in (0, 1))
+    v[:, :, 16:48], v[:, :, 96:112] = 0.0, 2.0 ** 30
+    p.write(k, v, table, ints(0))
+    for scales in (p.host[3], p.cache.v_scale):
+        scales[int(table[0, 5])], scales[int(table[0, 2]), :, 1] = 0.0, 0.0
+        scales[int(table[0, 1])] *= -1
+    p.cache.k_scale[int(table[0, 4])] *= -1
+    p.host[2][int(table[0, 4])] *= -1
+    for window in (0, 90):
+        attend_unequal(p, table, lens, q, window, 40)
