@@ -474,7 +474,7 @@ def attend_unequal(p, table, lens, q, window, sinks, **kw):
     """attend_and_check for values of any scales: a row's P times its block's scale
     of values is rounded to fp16 at 2^7 or more for the largest such product, so
     half a step of the smallest numbers, 2^-25, stands for 2^-32 of it, times the
-    code.  Sums are fp32: 2^-20 of their magnitudes."""
+    code.  O is rounded to q's type: at least half a step of its smallest numbers."""
     o, lse = p.cache.attention(q.cuda(), table.cuda(), ints(*lens).cuda(), window, sinks, check=True, **kw)
     c, g = p.cache, q.shape[1] // p.cache.kv_heads
     for b, n in enumerate(lens):
@@ -488,7 +488,8 @@ def attend_unequal(p, table, lens, q, window, sinks, **kw):
         w = torch.softmax(x, -1).nan_to_num(0.0) * sd.abs()[:, None]
         floor = 2.0 ** -32 * w.amax(-1, keepdim=True) * ((mask / sd.abs()[:, None].clamp_min(2.0 ** -100)) @ vd.abs())
         o_want, o_bound = want["o"]
-        o_bound = o_bound + (seq_ref.unit(q.dtype) - seq_ref.unit(BF16)) * o_want.abs() + floor
+        tiny = torch.finfo(q.dtype).smallest_normal * seq_ref.unit(q.dtype)
+        o_bound = o_bound + (seq_ref.unit(q.dtype) - seq_ref.unit(BF16)) * o_want.abs() + floor + tiny
         seq_ref.check(o[b], (o_want, o_bound), f"o of sequence {b}")
         seq_ref.check(lse[b], want["lse"], f"lse of sequence {b}")
     return o, lse
