@@ -316,13 +316,15 @@ _graphs = weakref.WeakSet()
 
 
 def _note_uses(ctx, tensors, stream: int):
-    """Remember that the graph of `ctx` was built on `stream` over these leaves.
+    """Remember that the graph of `ctx` was built on `stream` over these leaves,
+    or views of leaves.
 
     A gradient that is accumulated into a leaf runs on the stream on which the
     leaf was first used for as long as a graph of that use lives.  A backward
     pass captured on another stream would have to join that stream, which ends
     the capture and the process, so such a capture is refused."""
-    leaves = {id(t) for t, needed in zip(tensors, ctx.needs_input_grad) if needed and t.is_leaf}
+    used = [t if t.is_leaf else t._base for t, needed in zip(tensors, ctx.needs_input_grad) if needed]
+    leaves = {id(t) for t in used if t is not None and t.is_leaf and t.requires_grad}
     if not leaves:
         return
     if torch.cuda.is_current_stream_capturing() and any(g.stream != stream and g.leaves & leaves for g in _graphs):

@@ -824,3 +824,41 @@ def test_empty_tensors_of_other_head_dims_are_refused(d):
         q = torch.zeros(shape, dtype=BF16, device="cuda")
         with pytest.raises(ValueError, match="head_dim"):
             window_forward(q, q, q, 4)
+
+
+@pytest.mark.gpu
+def test_capture_of_views_of_leaves_with_a_live_eager_graph_is_refused():
+    """Rows outside heads, halves of one tensor, a broadcast head: views of leaves
+    are uses of the leaves."""
+    both = torch.randn(1, 64, 4, 64, device="cuda").bfloat16().requires_grad_()
+    one = torch.randn(1, 1, 64, 64, device="cuda").bfloat16().requires_grad_()
+
+    def call():
+        k, v = both.transpose(1, 2)[:, :2], both.transpose(1, 2)[:, 2:]
+        return sliding_window_attention(one.expand(-1, 4, -1, -1), k, v, 16, 2)
+
+    side = torch.cuda.Stream()
+    for leaf in (both, one):
+        other = one if leaf is both else both
+        other.requires_grad_(False)
+        alive = call()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph = torch.cuda.CUDAGraph()
+            graph.capture_begin()
+            with pytest.raises(RuntimeError, match="still alive"):
+                call()
+            graph.capture_end()
+        del alive
+        other.requires_grad_()
+    want = torch.autograd.grad(call(), (both, one), torch.ones(1, 4, 64, 64, device="cuda").bfloat16())
+    ones, grads = torch.ones(1, 4, 64, 64, device="cuda").bfloat16(), [torch.zeros_like(t) for t in want]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for g, x in zip(grads, torch.autograd.grad(call(), (both, one), ones)):
+            g.copy_(x)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(grads, want):
+        assert torch.equal(a, b)
