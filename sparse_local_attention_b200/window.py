@@ -12,6 +12,7 @@ import contextlib
 import copy
 import ctypes
 import functools
+import threading
 import weakref
 from typing import Optional
 
@@ -313,6 +314,7 @@ def window_backward(q, k, v, o, lse, dout, window: int = 0, sinks: int = 0, scal
 # The live graphs, each of which notes its stream and its leaves (by identity: it
 # keeps them alive).  Nothing is kept on the leaves, which are saved and copied.
 _graphs = weakref.WeakSet()
+_graphs_lock = threading.Lock()
 
 
 def _note_uses(ctx, tensors, stream: int):
@@ -327,11 +329,12 @@ def _note_uses(ctx, tensors, stream: int):
     leaves = {id(t) for t in used if t is not None and t.is_leaf and t.requires_grad}
     if not leaves:
         return
-    if torch.cuda.is_current_stream_capturing() and any(g.stream != stream and g.leaves & leaves for g in _graphs):
-        raise RuntimeError("sliding_window_attention: an eager graph of the same leaf tensors is still alive; release "
-                           "it (and its outputs) before capturing, or capture on detached leaves")
     ctx.stream, ctx.leaves = stream, leaves
-    _graphs.add(ctx)
+    with _graphs_lock:
+        if torch.cuda.is_current_stream_capturing() and any(g.stream != stream and g.leaves & leaves for g in _graphs):
+            raise RuntimeError("sliding_window_attention: an eager graph of the same leaf tensors is still alive; "
+                               "release it (and its outputs) before capturing, or capture on detached leaves")
+        _graphs.add(ctx)
 
 
 class _SlidingWindowAttention(torch.autograd.Function):

@@ -862,3 +862,34 @@ def test_capture_of_views_of_leaves_with_a_live_eager_graph_is_refused():
     torch.cuda.synchronize()
     for a, b in zip(grads, want):
         assert torch.equal(a, b)
+
+
+def test_uses_are_noted_from_several_threads(monkeypatch):
+    """A capture looks through the live graphs while other threads add theirs."""
+    import threading
+
+    class Graph:
+        needs_input_grad = (True,)
+
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    leaves = [torch.zeros(2, requires_grad=True) for _ in range(4)]
+    kept, failed = [[] for _ in leaves], []
+
+    def run(i):
+        try:
+            for _ in range(1500):
+                kept[i].append(Graph())
+                window._note_uses(kept[i][-1], (leaves[i],), i)
+                if len(kept[i]) > 40:
+                    del kept[i][:30]
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(leaves))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    with pytest.raises(RuntimeError, match="still alive"):
+        window._note_uses(Graph(), (leaves[0],), 9)
